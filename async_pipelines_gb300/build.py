@@ -1,6 +1,6 @@
 """Builds the CUDA library in-tree with nvcc for sm_103a (GB300).
 
-One translation unit, one -gencode; the shared library links the CUDA
+A few translation units, compiled in parallel, one -gencode; the shared library links the CUDA
 runtime statically and reaches the driver's tensor-map encoder through the
 runtime's driver-entry-point query, so it needs no libcuda at link time.
 """
@@ -18,9 +18,10 @@ LIB = os.path.join(PKG, "libgemm_ws.so")
 # Debug build: the same sources with the test hooks of include/gemm_ws_debug.h
 # (fault injection for the watchdog, per-tile timestamps). Tests only.
 DEBUG_LIB = os.path.join(PKG, "libgemm_ws_debug.so")
-SOURCES = [os.path.join(CSRC, "gemm_ws.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("ptx.cuh", "gemm_ws_kernel.cuh")] + [
-    os.path.join(INCLUDE, "gemm_ws.h"), os.path.join(INCLUDE, "gemm_ws_debug.h")]
+SOURCES = [os.path.join(CSRC, f) for f in ("gemm_ws.cu", "lm_norm.cu")]
+DEPS = SOURCES + [os.path.join(CSRC, f) for f in (
+    "ptx.cuh", "watchdog.cuh", "handle.cuh", "gemm_ws_kernel.cuh", "lm_norm_kernel.cuh")] + [
+    os.path.join(INCLUDE, f) for f in ("gemm_ws.h", "gemm_ws_debug.h", "gemm_ws_lm.h")]
 
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
@@ -41,7 +42,7 @@ def stale(out: str = LIB) -> bool:
 
 def _cmd(out: str, extra=(), verbose: bool = False):
     cmd = [nvcc(), ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
-           f"-I{INCLUDE}", "-o", out, *extra, *SOURCES]
+           "--threads", str(len(SOURCES)), f"-I{INCLUDE}", "-o", out, *extra, *SOURCES]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
     return cmd

@@ -20,66 +20,16 @@
 #include "gemm_ws_debug.h"
 #endif
 #include "gemm_ws_kernel.cuh"
-
-// A tensor map the handle encoded before, and what it describes.
-struct MapCacheEntry {
-  const void* ptr;
-  uint64_t d0, d1, d2;
-  uint32_t b0, b1;
-  int swizzle, promotion;
-  bool valid;
-  CUtensorMap map;
-};
-constexpr int kMapCache = 16;
-
-struct gemm_ws {
-  int device;
-  int num_sms;
-  int cta_group;                  // 0: chosen per problem (default); 1: single-CTA tiles; 2: CTA pairs
-  int pdl;                        // launch with programmatic stream serialisation
-  int group_m;                    // raster group: m-tiles walked per n step
-  int max_pair_clusters;          // co-resident 2-CTA clusters of the pair kernel
-  int stream_k;                   // 0 off, 1 where the cost model gains (default), 2 always
-  int sk_inline;                  // two-piece tiles: fix-up inside the GEMM (default 1)
-  int k_snake;                    // every other unit of a cluster walks K backwards
-  uint32_t* work;                 // [0] stream-out counter, [1] status, [2] done count, then
-                                  // the in-kernel fix-up words (work_words)
-  float* partial;                 // stream-K partials: num_sms parts of 128 x 256 fp32
-  int last_cuda_error;
-  unsigned long long timeout_ns;
-  PFN_cuTensorMapEncodeTiled_v12000 encode;
-  MapCacheEntry map_cache[kMapCache];   // recently encoded tensor maps (host memory)
-  int map_cache_next;
-#ifdef GEMM_WS_DEBUG
-  int debug_fault;
-  unsigned long long* trace;
-  unsigned long long* phases;
-#endif
-};
+#include "handle.cuh"
 
 namespace {
 
-constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
-constexpr int64_t kMaxElems = int64_t{1} << 40;
 constexpr int kWorkWords = 4;   // counter [0], status [1], consumers done [2]
 
 // Words of a handle's work area: kWorkWords, then the in-kernel fix-up's
 // arrival counts and written flags (one per epilogue warp of each CTA).
 size_t work_words(int num_sms) {
   return kWorkWords + 2 * static_cast<size_t>(num_sms) * gws::NUM_EPI_WARPS;
-}
-
-int cuda_fail(gemm_ws* h, cudaError_t e) {
-  if (h) h->last_cuda_error = static_cast<int>(e);
-  return GEMM_WS_ERR_CUDA;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool overlaps(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
-  if (!a || !b || abytes <= 0 || bbytes <= 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + static_cast<uintptr_t>(bbytes) && b0 < a0 + static_cast<uintptr_t>(abytes);
 }
 
 // A 3-D bf16 tensor {d0 (contiguous), d1, d2}, packed, tiled box {b0, b1, 1}.
@@ -567,21 +517,6 @@ int group_m_from_env() {
   }
   return 8;
 }
-
-class DeviceGuard {
- public:
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev_) != cudaSuccess) prev_ = -1;
-    if (prev_ != dev) cudaSetDevice(dev);
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev_ >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev_) cudaSetDevice(prev_);
-  }
-
- private:
-  int prev_ = -1;
-};
 
 }  // namespace
 

@@ -1,0 +1,337 @@
+// Host side of dropout and the norm (include/gemm_ws_lm.h): argument checks,
+// the choice of a row's team of threads, and the launches.
+#include <cmath>
+#include <cstring>
+
+#include "gemm_ws_lm.h"
+#include "handle.cuh"
+#include "lm_norm_kernel.cuh"
+
+namespace {
+
+constexpr int64_t kMaxCols = 1024 * gws::MAX_VPT * gws::GROUP;   // 32768: a block holds a row
+// fp32 partials of the handle: one row of kMaxCols for each SM.
+constexpr int64_t kPartialPerSm = int64_t{128} * 256;
+static_assert(kPartialPerSm >= kMaxCols, "a block's dweight partial fits its SM's share");
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+int element_size(int dtype) { return dtype == GEMM_WS_F32 ? 4 : 2; }
+
+// A matrix argument as the checks see it.
+struct Mat {
+  const void* ptr;
+  int64_t ld;
+  int64_t size;   // bytes of an element
+  bool given() const { return ptr != nullptr; }
+  int64_t bytes(int64_t rows, int64_t cols) const { return ((rows - 1) * ld + cols) * size; }
+  // Each row starts on a boundary of 8 elements (16 bytes at most).
+  bool wide() const {
+    const int64_t step = size * 8 < 16 ? size * 8 : 16;
+    return reinterpret_cast<uintptr_t>(ptr) % step == 0 && (ld * size) % step == 0;
+  }
+};
+
+// The output `out` may be exactly the input `in`, and else not overlap it.
+bool clash(const Mat& out, const Mat& in, int64_t rows, int64_t cols, bool may_equal) {
+  if (!out.given() || !in.given()) return false;
+  if (may_equal && out.ptr == in.ptr && out.ld == in.ld && out.size == in.size) return false;
+  return overlaps(out.ptr, out.bytes(rows, cols), in.ptr, in.bytes(rows, cols));
+}
+
+bool bad_matrix(const Mat& m, int64_t cols) {
+  return m.given() && (m.ld < cols || m.ld > kMaxElems ||
+                       reinterpret_cast<uintptr_t>(m.ptr) % m.size != 0);
+}
+
+// p and rng as a launch takes them. Returns false where p is not in [0, 1] or
+// a mask is wanted and rng is missing.
+bool make_dropout(double p, const uint64_t* rng, gws::Dropout* d) {
+  if (!(p >= 0.0 && p <= 1.0)) return false;
+  d->below = static_cast<uint32_t>(std::nearbyint(p * 65536.0));
+  d->rng = rng;
+  d->scale = d->below < 65536 ? static_cast<float>(65536.0 / (65536 - d->below)) : 0.0f;
+  return d->below == 0 || (rng && reinterpret_cast<uintptr_t>(rng) % 8 == 0);
+}
+
+// A launch that may start while the stream's previous kernel ends; each of
+// these kernels waits for that one before it touches global memory.
+template <typename P>
+int launch(gemm_ws* h, void (*kernel)(P), int64_t blocks, int threads, size_t smem, cudaStream_t s,
+           const P& params) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  if (h->pdl) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, params);
+  return e == cudaSuccess ? GEMM_WS_OK : cuda_fail(h, e);
+}
+
+// The threads of a row and the groups that each holds.
+struct Team {
+  int threads, vpt, rows;   // rows: of a block
+};
+
+// Up to 1024 columns a warp holds a row and a block has several (no barrier).
+// Longer rows take a block. With few rows (less than two for each SM) every
+// thread takes one group, for the shortest row; with many, up to `most`, so
+// that more bytes are in flight for each thread.
+Team pick_team(const gemm_ws* h, int64_t rows, int64_t cols, int most) {
+  const int64_t groups = ceil_div(cols, gws::GROUP);
+  Team t;
+  if (groups <= 32 * gws::MAX_VPT) {
+    t.vpt = groups <= 32 ? 1 : groups <= 64 ? 2 : 4;
+    t.threads = 32;
+    t.rows = rows >= 8 * h->num_sms ? 8 : rows >= 2 * h->num_sms ? 4 : 1;
+    return t;
+  }
+  t.vpt = rows < 2 * h->num_sms ? 1 : most;
+  while (ceil_div(groups, t.vpt) > 1024) t.vpt *= 2;
+  t.threads = static_cast<int>(ceil_div(ceil_div(groups, t.vpt), 32) * 32);
+  t.rows = 1;
+  return t;
+}
+
+template <typename T, int Q>
+int launch_norm(gemm_ws* h, const Team& t, const gws::NormParams& p, cudaStream_t s) {
+  const int64_t blocks = ceil_div(p.rows, t.rows);
+  const int threads = t.threads * t.rows;
+  switch (t.vpt) {
+    case 1: return launch(h, gws::add_rms_norm_kernel<T, 1, Q>, blocks, threads, 0, s, p);
+    case 2: return launch(h, gws::add_rms_norm_kernel<T, 2, Q>, blocks, threads, 0, s, p);
+    default: return launch(h, gws::add_rms_norm_kernel<T, 4, Q>, blocks, threads, 0, s, p);
+  }
+}
+
+template <typename T>
+int launch_norm(gemm_ws* h, int output, const Team& t, const gws::NormParams& p, cudaStream_t s) {
+  switch (output) {
+    case GEMM_WS_NORM_SAME: return launch_norm<T, 0>(h, t, p, s);
+    case GEMM_WS_NORM_E4M3_ROW: return launch_norm<T, 1>(h, t, p, s);
+    default: return launch_norm<T, 2>(h, t, p, s);
+  }
+}
+
+template <typename T>
+int launch_grad(gemm_ws* h, const Team& t, const gws::NormGradParams& p, void* dweight,
+                cudaStream_t s) {
+  const int threads = t.threads * t.rows;
+  const size_t smem = t.rows > 1 ? static_cast<size_t>(p.cols) * sizeof(float) : 0;
+  // As many blocks as run at once (1024 threads of an SM hold their rows in
+  // registers), no more than the partials have room for.
+  int64_t blocks = ceil_div(p.rows, t.rows);
+  const int64_t resident = static_cast<int64_t>(h->num_sms) * (threads >= 1024 ? 1 : 1024 / threads);
+  if (blocks > resident) blocks = resident;
+  const int64_t room = h->num_sms * kPartialPerSm / p.cols;
+  if (p.partial && blocks > room) blocks = room;
+  int rc;
+  switch (t.vpt) {
+    case 1: rc = launch(h, gws::add_rms_norm_grad_kernel<T, 1>, blocks, threads, smem, s, p); break;
+    case 2: rc = launch(h, gws::add_rms_norm_grad_kernel<T, 2>, blocks, threads, smem, s, p); break;
+    default: rc = launch(h, gws::add_rms_norm_grad_kernel<T, 4>, blocks, threads, smem, s, p); break;
+  }
+  if (rc != GEMM_WS_OK || !dweight) return rc;
+  gws::DweightParams q;
+  q.partial = p.partial;
+  q.blocks = static_cast<int>(blocks);
+  q.cols = p.cols;
+  q.dweight = dweight;
+  return launch(h, gws::dweight_kernel<T>, ceil_div(p.cols, gws::DW_COLS),
+                gws::DW_COLS * gws::DW_LANES, 0, s, q);
+}
+
+}  // namespace
+
+extern "C" {
+
+int gemm_ws_dropout(gemm_ws_t* h, int dtype, const void* x, int64_t ldx, void* y, int64_t ldy,
+                    int64_t rows, int64_t cols, double p, const uint64_t* rng, void* stream) {
+  if (!h || dtype < GEMM_WS_BF16 || dtype > GEMM_WS_F32 || rows < 0 || cols < 0 ||
+      rows > kMaxDim || cols > kMaxDim)
+    return GEMM_WS_ERR_INVALID_ARG;
+  gws::DropoutParams q;
+  std::memset(&q, 0, sizeof q);
+  if (!make_dropout(p, rng, &q.drop)) return GEMM_WS_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return GEMM_WS_OK;
+  const int64_t size = element_size(dtype);
+  const Mat mx{x, ldx, size}, my{y, ldy, size};
+  const Mat mr{q.drop.below ? rng : nullptr, 2, 8};
+  if (!x || !y || bad_matrix(mx, cols) || bad_matrix(my, cols)) return GEMM_WS_ERR_INVALID_ARG;
+  if (clash(my, mx, rows, cols, true) ||
+      (mr.given() && overlaps(y, my.bytes(rows, cols), rng, 16)))
+    return GEMM_WS_ERR_INVALID_ARG;
+  q.x = x;
+  q.y = y;
+  q.ldx = ldx;
+  q.ldy = ldy;
+  q.cols = static_cast<int>(cols);
+  q.row_groups = static_cast<int>(ceil_div(cols, gws::GROUP));
+  q.groups = rows * q.row_groups;
+  q.wide = mx.wide() && my.wide();
+  const int64_t blocks = ceil_div(q.groups, gws::DROP_THREADS * gws::DROP_VPT);
+  if (blocks > kMaxDim) return GEMM_WS_ERR_INVALID_ARG;
+  DeviceGuard guard(h->device);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  switch (dtype) {
+    case GEMM_WS_BF16:
+      return launch(h, gws::dropout_kernel<__nv_bfloat16>, blocks, gws::DROP_THREADS, 0, s, q);
+    case GEMM_WS_F16:
+      return launch(h, gws::dropout_kernel<__half>, blocks, gws::DROP_THREADS, 0, s, q);
+    default:
+      return launch(h, gws::dropout_kernel<float>, blocks, gws::DROP_THREADS, 0, s, q);
+  }
+}
+
+int gemm_ws_add_rms_norm(gemm_ws_t* h, int dtype, const void* x, int64_t ldx,
+                         const void* residual, int64_t ldr, const void* weight, void* hidden,
+                         int64_t ldh, void* y, int64_t ldy, int output, float* scales,
+                         float* rstd, int64_t rows, int64_t cols, float eps, double p,
+                         const uint64_t* rng, void* stream) {
+  if (!h || dtype < GEMM_WS_BF16 || dtype > GEMM_WS_F32 || output < GEMM_WS_NORM_SAME ||
+      output > GEMM_WS_NORM_E4M3_GROUP || rows < 0 || rows > kMaxDim || cols < 1 ||
+      cols > kMaxCols || !(eps >= 0.0f))
+    return GEMM_WS_ERR_INVALID_ARG;
+  gws::NormParams q;
+  std::memset(&q, 0, sizeof q);
+  if (!make_dropout(p, rng, &q.drop)) return GEMM_WS_ERR_INVALID_ARG;
+  if (rows == 0) return GEMM_WS_OK;
+  const bool same = output == GEMM_WS_NORM_SAME;
+  const int64_t size = element_size(dtype);
+  const int64_t per_row = output == GEMM_WS_NORM_E4M3_GROUP ? ceil_div(cols, gws::QUANT_GROUP) : 1;
+  const Mat in[3] = {{x, ldx, size}, {residual, ldr, size}, {weight, cols, size}};
+  const Mat mh{hidden, ldh, size}, my{y, ldy, same ? size : 1};
+  if (!x || !weight || !y || (!same && !scales)) return GEMM_WS_ERR_INVALID_ARG;
+  for (const Mat& m : in)
+    if (bad_matrix(m, cols)) return GEMM_WS_ERR_INVALID_ARG;
+  if (bad_matrix(mh, cols) || bad_matrix(my, cols) ||
+      reinterpret_cast<uintptr_t>(scales) % 4 != 0 || reinterpret_cast<uintptr_t>(rstd) % 4 != 0)
+    return GEMM_WS_ERR_INVALID_ARG;
+  // Outputs against the inputs and against each other.
+  const Mat vec[4] = {{same ? nullptr : scales, per_row, 4}, {rstd, 1, 4}, {weight, 0, size},
+                      {q.drop.below ? rng : nullptr, 0, 8}};
+  const int64_t vec_bytes[4] = {rows * per_row * 4, rows * 4, cols * size, 16};
+  const Mat mats[4] = {in[0], in[1], mh, my};
+  if (clash(mh, in[0], rows, cols, true) || clash(mh, in[1], rows, cols, true) ||
+      clash(my, in[0], rows, cols, true) || clash(my, in[1], rows, cols, false) ||
+      clash(my, mh, rows, cols, false))
+    return GEMM_WS_ERR_INVALID_ARG;
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < 4; ++j) {
+      // scales and rstd against every matrix, weight and rng against the outputs
+      if (mats[j].given() && (i < 2 || j >= 2) &&
+          overlaps(vec[i].ptr, vec_bytes[i], mats[j].ptr, mats[j].bytes(rows, cols)))
+        return GEMM_WS_ERR_INVALID_ARG;
+      if (i < 2 && j > i && overlaps(vec[i].ptr, vec_bytes[i], vec[j].ptr, vec_bytes[j]))
+        return GEMM_WS_ERR_INVALID_ARG;
+    }
+  q.x = x;
+  q.residual = residual;
+  q.weight = weight;
+  q.h = hidden;
+  q.y = y;
+  q.rstd = rstd;
+  q.scales = scales;
+  q.ldx = ldx;
+  q.ldr = ldr;
+  q.ldh = ldh;
+  q.ldy = ldy;
+  q.rows = rows;
+  q.cols = static_cast<int>(cols);
+  q.eps = eps;
+  q.wide = in[0].wide() && (!residual || in[1].wide()) &&
+           reinterpret_cast<uintptr_t>(weight) % 16 == 0 && (!hidden || mh.wide()) && my.wide();
+  const Team t = pick_team(h, rows, cols, 4);
+  q.team = t.threads;
+  DeviceGuard guard(h->device);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  switch (dtype) {
+    case GEMM_WS_BF16: return launch_norm<__nv_bfloat16>(h, output, t, q, s);
+    case GEMM_WS_F16: return launch_norm<__half>(h, output, t, q, s);
+    default: return launch_norm<float>(h, output, t, q, s);
+  }
+}
+
+int gemm_ws_add_rms_norm_backward(gemm_ws_t* h, int dtype, const void* dy, int64_t lddy,
+                                  const void* dhidden, int64_t lddh, const void* hidden,
+                                  int64_t ldh, const void* weight, const float* rstd, void* dx,
+                                  int64_t lddx, void* dresidual, int64_t lddr, void* dweight,
+                                  int64_t rows, int64_t cols, double p, const uint64_t* rng,
+                                  void* stream) {
+  if (!h || dtype < GEMM_WS_BF16 || dtype > GEMM_WS_F32 || rows < 0 || rows > kMaxDim ||
+      cols < 1 || cols > kMaxCols)
+    return GEMM_WS_ERR_INVALID_ARG;
+  gws::NormGradParams q;
+  std::memset(&q, 0, sizeof q);
+  if (!make_dropout(p, rng, &q.drop)) return GEMM_WS_ERR_INVALID_ARG;
+  const int64_t size = element_size(dtype);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (reinterpret_cast<uintptr_t>(dweight) % size != 0) return GEMM_WS_ERR_INVALID_ARG;
+  if (rows == 0) {
+    if (!dweight) return GEMM_WS_OK;
+    DeviceGuard guard(h->device);
+    const cudaError_t e = cudaMemsetAsync(dweight, 0, static_cast<size_t>(cols * size), s);
+    return e == cudaSuccess ? GEMM_WS_OK : cuda_fail(h, e);
+  }
+  const Mat in[3] = {{dy, lddy, size}, {dhidden, lddh, size}, {hidden, ldh, size}};
+  const Mat out[2] = {{dx, lddx, size}, {dresidual, lddr, size}};
+  if (!dy || !hidden || !weight || !rstd || !dx) return GEMM_WS_ERR_INVALID_ARG;
+  for (const Mat& m : in)
+    if (bad_matrix(m, cols)) return GEMM_WS_ERR_INVALID_ARG;
+  for (const Mat& m : out)
+    if (bad_matrix(m, cols)) return GEMM_WS_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(weight) % size != 0 || reinterpret_cast<uintptr_t>(rstd) % 4 != 0)
+    return GEMM_WS_ERR_INVALID_ARG;
+  const Mat vec[3] = {{weight, 0, size}, {rstd, 0, 4}, {q.drop.below ? rng : nullptr, 0, 8}};
+  const int64_t vec_bytes[3] = {cols * size, rows * 4, 16};
+  for (const Mat& o : out) {
+    if (clash(o, in[0], rows, cols, true) || clash(o, in[1], rows, cols, true) ||
+        clash(o, in[2], rows, cols, false))
+      return GEMM_WS_ERR_INVALID_ARG;
+    for (int i = 0; i < 3; ++i)
+      if (o.given() && overlaps(vec[i].ptr, vec_bytes[i], o.ptr, o.bytes(rows, cols)))
+        return GEMM_WS_ERR_INVALID_ARG;
+    if (o.given() && overlaps(dweight, cols * size, o.ptr, o.bytes(rows, cols)))
+      return GEMM_WS_ERR_INVALID_ARG;
+  }
+  if (clash(out[1], out[0], rows, cols, false)) return GEMM_WS_ERR_INVALID_ARG;
+  for (const Mat& m : in)
+    if (m.given() && overlaps(dweight, cols * size, m.ptr, m.bytes(rows, cols)))
+      return GEMM_WS_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i)
+    if (overlaps(dweight, cols * size, vec[i].ptr, vec_bytes[i])) return GEMM_WS_ERR_INVALID_ARG;
+  q.dy = dy;
+  q.dh = dhidden;
+  q.h = hidden;
+  q.weight = weight;
+  q.rstd = rstd;
+  q.dx = dx;
+  q.dres = dresidual;
+  q.partial = dweight ? h->partial : nullptr;
+  q.lddy = lddy;
+  q.lddh = lddh;
+  q.ldh = ldh;
+  q.lddx = lddx;
+  q.lddres = lddr;
+  q.rows = rows;
+  q.cols = static_cast<int>(cols);
+  q.wide = in[0].wide() && (!dhidden || in[1].wide()) && in[2].wide() && out[0].wide() &&
+           (!dresidual || out[1].wide()) && reinterpret_cast<uintptr_t>(weight) % 16 == 0;
+  const Team t = pick_team(h, rows, cols, 2);
+  q.team = t.threads;
+  DeviceGuard guard(h->device);
+  switch (dtype) {
+    case GEMM_WS_BF16: return launch_grad<__nv_bfloat16>(h, t, q, dweight, s);
+    case GEMM_WS_F16: return launch_grad<__half>(h, t, q, dweight, s);
+    default: return launch_grad<float>(h, t, q, dweight, s);
+  }
+}
+
+}  // extern "C"

@@ -14,6 +14,7 @@ from typing import Optional
 import torch
 
 from . import build as _build
+from . import lm_ops as _lm
 
 OK = 0
 ERR_INVALID_ARG = 1
@@ -78,6 +79,7 @@ def load_library(path: Optional[str] = None):
                  "gemm_ws_query_status", "gemm_ws_last_cuda_error",
                  "gemm_ws_run_streamout_noalloc"):
         getattr(lib, name).restype = ctypes.c_int
+    _lm.declare(lib)
     if path is None:
         _lib = lib
     return lib
@@ -210,8 +212,9 @@ def _check_operands(A, B, C, D):
     return M, N, K, L
 
 
-class GemmWS:
-    """Owns one library handle on one CUDA device.
+class GemmWS(_lm.LmOps):
+    """Owns one library handle on one CUDA device; runs the GEMM and, by the
+    methods of `lm_ops.LmOps`, the operators around it.
 
     `lib` selects the loaded library (default: the production build; tests
     pass the debug build from `load_debug_library()`)."""
@@ -235,6 +238,8 @@ class GemmWS:
             self.close()
         except Exception:
             pass
+
+    _stream_of = staticmethod(_stream_handle)
 
     def _raise(self, rc, what):
         if rc != OK:

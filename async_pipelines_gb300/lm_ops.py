@@ -1,0 +1,154 @@
+"""Tensor API of the language-model operators in include/gemm_ws_lm.h.
+
+`LmOps` holds their methods; `gemm_ws.GemmWS` inherits them, so one handle
+runs the matrix products and what surrounds them. As there, outputs are the
+caller's tensors, calls run asynchronously on the current (or the given)
+stream, and there is no fallback.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+BF16, F16, F32 = 0, 1, 2                                  # gemm_ws_dtype
+NORM_SAME, NORM_E4M3_ROW, NORM_E4M3_GROUP = 0, 1, 2       # gemm_ws_norm_output
+QUANT_GROUP = 128                                         # columns of one scale
+
+EXPORTS = ("gemm_ws_dropout", "gemm_ws_add_rms_norm", "gemm_ws_add_rms_norm_backward")
+
+_DTYPES = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
+
+
+def declare(lib) -> None:
+    """Argument and result types of the entry points, on a loaded library."""
+    vp, i64, f32, f64, i32 = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_double,
+                              ctypes.c_int)
+    lib.gemm_ws_dropout.argtypes = [vp, i32, vp, i64, vp, i64, i64, i64, f64, vp, vp]
+    lib.gemm_ws_add_rms_norm.argtypes = [vp, i32, vp, i64, vp, i64, vp, vp, i64, vp, i64, i32, vp,
+                                         vp, i64, i64, f32, f64, vp, vp]
+    lib.gemm_ws_add_rms_norm_backward.argtypes = [vp, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp,
+                                                  i64, vp, i64, vp, i64, i64, f64, vp, vp]
+    for name in EXPORTS:
+        getattr(lib, name).restype = i32
+
+
+def _rows(name, t, shape, dtype):
+    """(pointer, elements between rows) of a matrix argument; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.dtype is not dtype or not t.is_cuda or t.shape != shape:
+        raise ValueError(f"{name} must be a {tuple(shape)} {dtype} CUDA tensor, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    step, inner = t.stride()
+    rows, cols = shape
+    if (inner != 1 and cols > 1) or (step < cols and rows > 1):
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return t.data_ptr(), step if step > cols else cols
+
+
+def _flat(name, t, n, dtype):
+    """The pointer of a contiguous argument of n elements; None for None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or not t.is_cuda or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of {n} elements")
+    return t.data_ptr()
+
+
+def _mask(p, rng):
+    """The pointer of the generator's words; None where nothing is dropped."""
+    if not 0.0 <= p <= 1.0:
+        raise ValueError("p must be in [0, 1]")
+    if p == 0.0:
+        return None
+    if rng is None:
+        raise ValueError("dropout needs rng: an int64 CUDA tensor (seed, first counter)")
+    return _flat("rng", rng, 2, torch.int64)
+
+
+def _type_of(x):
+    code = _DTYPES.get(x.dtype)
+    if code is None or x.dim() != 2:
+        raise ValueError("x must be a 2-D bf16, f16 or f32 tensor (rows, cols)")
+    return code
+
+
+class LmOps:
+    """The operators' methods, on an object with `lib` and `handle`."""
+
+    def dropout(self, x, y, p, rng, stream=None):
+        """y = keep * x / (1 - p); x, y: (rows, cols) of one type; y may be x.
+
+        rng: int64 (seed, first counter) on the GPU. The call uses
+        rows * ceil(cols / 8) counters; the same words give the same mask, which
+        is how the gradient is taken.
+        """
+        code = _type_of(x)
+        px, ldx = _rows("x", x, x.shape, x.dtype)
+        py, ldy = _rows("y", y, x.shape, x.dtype)
+        rows, cols = x.shape
+        rc = self.lib.gemm_ws_dropout(self.handle, code, px, ldx, py, ldy, rows, cols, p,
+                                      _mask(p, rng), self._stream_of(stream))
+        if rc:
+            self._raise(rc, "gemm_ws_dropout")
+        return y
+
+    def add_rms_norm(self, x, weight, y, residual=None, h=None, rstd=None, scales=None, eps=1e-6,
+                     p=0.0, rng=None, stream=None):
+        """h = residual + dropout(x); y = weight * h / sqrt(mean(h^2) + eps).
+
+        x, residual, h, y: (rows, cols); weight: (cols,). With y of type
+        torch.float8_e4m3fn, scales is f32 and says how y is scaled: rows
+        elements, one a row, or (rows, ceil(cols / 128)), one for each 128
+        columns; y * scale is the norm. rstd: (rows,) f32, for the backward
+        pass. h may be x or residual, y may be x.
+        """
+        code = _type_of(x)
+        shape, dtype = x.shape, x.dtype
+        rows, cols = shape
+        px, ldx = _rows("x", x, shape, dtype)
+        pr, ldr = _rows("residual", residual, shape, dtype)
+        ph, ldh = _rows("h", h, shape, dtype)
+        output = NORM_SAME
+        ps = None
+        if scales is not None:
+            groups = (cols + QUANT_GROUP - 1) // QUANT_GROUP
+            by_group = groups > 1 and scales.dim() == 2 and scales.shape[1] == groups
+            output = NORM_E4M3_GROUP if by_group else NORM_E4M3_ROW
+            ps = _flat("scales", scales, rows * groups if by_group else rows, torch.float32)
+            py, ldy = _rows("y", y, shape, torch.float8_e4m3fn)
+        else:
+            py, ldy = _rows("y", y, shape, dtype)
+        rc = self.lib.gemm_ws_add_rms_norm(
+            self.handle, code, px, ldx, pr, ldr, _flat("weight", weight, cols, dtype), ph, ldh,
+            py, ldy, output, ps, _flat("rstd", rstd, rows, torch.float32), rows, cols, eps, p,
+            _mask(p, rng), self._stream_of(stream))
+        if rc:
+            self._raise(rc, "gemm_ws_add_rms_norm")
+        return y
+
+    def add_rms_norm_backward(self, dy, h, weight, rstd, dx, dweight=None, dh=None,
+                              dresidual=None, p=0.0, rng=None, stream=None):
+        """Gradients of add_rms_norm: dx of x, dresidual of residual, dweight.
+
+        dy: of y; dh: what reaches h from its other uses (None: zero); h, rstd:
+        what the forward call wrote; p, rng: as given to it. Without dropout
+        dx is the residual's gradient too.
+        """
+        code = _type_of(dy)
+        shape, dtype = dy.shape, dy.dtype
+        rows, cols = shape
+        pdy, lddy = _rows("dy", dy, shape, dtype)
+        pdh, lddh = _rows("dh", dh, shape, dtype)
+        ph, ldh = _rows("h", h, shape, dtype)
+        pdx, lddx = _rows("dx", dx, shape, dtype)
+        pdr, lddr = _rows("dresidual", dresidual, shape, dtype)
+        rc = self.lib.gemm_ws_add_rms_norm_backward(
+            self.handle, code, pdy, lddy, pdh, lddh, ph, ldh,
+            _flat("weight", weight, cols, dtype), _flat("rstd", rstd, rows, torch.float32), pdx,
+            lddx, pdr, lddr, _flat("dweight", dweight, cols, dtype), rows, cols, p,
+            _mask(p, rng), self._stream_of(stream))
+        if rc:
+            self._raise(rc, "gemm_ws_add_rms_norm_backward")
+        return dx
