@@ -18,9 +18,10 @@ LIB = os.path.join(PKG, "libgemm_ws.so")
 # Debug build: the same sources with the test hooks of include/gemm_ws_debug.h
 # (fault injection for the watchdog, per-tile timestamps). Tests only.
 DEBUG_LIB = os.path.join(PKG, "libgemm_ws_debug.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("gemm_ws.cu", "lm_norm.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("gemm_ws.cu", "lm_norm.cu", "lm_loss.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in (
-    "ptx.cuh", "watchdog.cuh", "handle.cuh", "gemm_ws_kernel.cuh", "lm_norm_kernel.cuh")] + [
+    "ptx.cuh", "watchdog.cuh", "handle.cuh", "gemm_ws_kernel.cuh", "lm_norm_kernel.cuh",
+    "lm_loss_kernel.cuh")] + [
     os.path.join(INCLUDE, f) for f in ("gemm_ws.h", "gemm_ws_debug.h", "gemm_ws_lm.h")]
 
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"

@@ -24,7 +24,7 @@
 
 namespace {
 
-constexpr int kWorkWords = 4;   // counter [0], status [1], consumers done [2]
+constexpr int kWorkWords = 4;   // counter [0], status [1], consumers done [2], blocks done [3]
 
 // Words of a handle's work area: kWorkWords, then the in-kernel fix-up's
 // arrival counts and written flags (one per epilogue warp of each CTA).
@@ -563,6 +563,7 @@ int gemm_ws_create(gemm_ws_t** out, int device) {
   h->k_snake = k_snake_from_env();
   e = configure_kernels(h->num_sms, &h->max_pair_clusters);
   if (e == cudaSuccess && h->max_pair_clusters < 1) h->cta_group = 1;
+  if (e == cudaSuccess) e = ce_configure(h->num_sms, &h->ce_pair_clusters);
   const size_t wbytes = work_words(h->num_sms) * sizeof(uint32_t);
   if (e == cudaSuccess) e = cudaMalloc(&h->work, wbytes);
   if (e == cudaSuccess) e = cudaMemset(h->work, 0, wbytes);

@@ -31,8 +31,10 @@ struct gemm_ws {
   int stream_k;                   // 0 off, 1 where the cost model gains (default), 2 always
   int sk_inline;                  // two-piece tiles: fix-up inside the GEMM (default 1)
   int k_snake;                    // every other unit of a cluster walks K backwards
-  uint32_t* work;                 // [0] stream-out counter, [1] status, [2] done count, then
-                                  // the in-kernel fix-up words (work_words)
+  int ce_pair_clusters;           // co-resident 2-CTA clusters of the cross entropy's product
+  uint32_t* work;                 // [0] stream-out counter, [1] status, [2] done count, [3] the
+                                  // cross entropy's done count, then the in-kernel fix-up words
+                                  // (work_words)
   float* partial;                 // stream-K partials: num_sms parts of 128 x 256 fp32
   int last_cuda_error;
   unsigned long long timeout_ns;
@@ -45,6 +47,10 @@ struct gemm_ws {
   unsigned long long* phases;
 #endif
 };
+
+// Sets the shared-memory attributes of the cross entropy's product kernels on
+// the current device; *pair_clusters: how many of its 2-CTA clusters fit at once.
+cudaError_t ce_configure(int num_sms, int* pair_clusters);
 
 namespace {
 

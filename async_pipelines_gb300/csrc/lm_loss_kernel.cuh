@@ -1,0 +1,770 @@
+// Softmax cross entropy of x * weight^T over a vocabulary, and its gradients,
+// without the logits in memory.
+//
+//   z = x * weight^T (T x V);  lse_i = log sum_j exp(z_ij);
+//   loss_i = lse_i - z_i,target(i)
+//   G_ij = g_i * (exp(z_ij - lse_i) - [j == target(i)])
+//   dx = G * weight;  dweight = G^T * x
+//
+// Tokens that are not counted (target == ignore) are left out before the
+// first product: a gather packs the counted rows of x, so such a row costs
+// nothing, is never read, and cannot put a NaN into dweight. How many rows
+// are counted is known on the device only; every kernel reads it there.
+//
+// One persistent warp-specialised product kernel serves all of it, with the
+// roles of the GEMM (two TMA producer warps, one MMA thread, eight epilogue
+// warps, two TMEM accumulators) and one of three epilogues:
+//   LSE    the logits' tile stays in TMEM; each row's running maximum and sum
+//          of exponentials leave, and the target's logit.
+//   GRAD   the tile is computed again for a piece of the vocabulary and G
+//          leaves in bf16. That is the one rounding of G (2^-9 of each
+//          value, independent from element to element, so the sums that dx and
+//          dweight are lose no more than by their own rounding).
+//   SUMS   the two products of that piece in one launch, dx's units (fp32,
+//          added to by later pieces) before dweight's (bf16, final). G^T, x
+//          and weight are read as they lie, as MN-major operands, so nothing
+//          is transposed in memory.
+// The work is 8 T V H operations for both gradients (6 without computing the
+// logits twice), for a workspace of one piece of G instead of T x V.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "ptx.cuh"
+#include "watchdog.cuh"
+
+namespace gws {
+namespace ce {
+
+constexpr int BM = 128;                   // rows of a CTA's tile = TMEM lanes
+constexpr int BN_MAX = 256;               // columns of a tile, at most
+constexpr int BK = 64;                    // k-block: one 128-byte swizzle row of bf16
+constexpr int UMMA_K = 16;
+constexpr int ACC_BUFS = 2;
+constexpr int EPI_N = 32;                 // columns of one TMEM load
+constexpr int EPI_WARPS = 8;              // two for each 32-lane quarter
+constexpr int WARP_A = 0, WARP_MMA = 1, WARP_EPI0 = 2, WARP_B = WARP_EPI0 + EPI_WARPS;
+constexpr int THREADS = (WARP_B + 1) * 32;
+constexpr int MAX_STAGES = 8;
+constexpr uint32_t A_BLOCK = BM * BK * 2;              // 16 KiB: 128 x 64 of A
+constexpr uint32_t MN_BOX = 64 * BK * 2;               // 8 KiB: a 64 x 64 box of an MN-major operand
+constexpr uint32_t RING_BYTES = 192 * 1024;
+constexpr uint32_t OUT_BYTES = 32 * 128;               // an epilogue warp's 32 rows x 128 bytes
+constexpr uint32_t OFF_OUT = RING_BYTES;
+constexpr uint32_t OFF_BAR = OFF_OUT + EPI_WARPS * OUT_BYTES;
+constexpr int BAR_FULL = 0, BAR_EMPTY = BAR_FULL + MAX_STAGES, BAR_ACC_FULL = BAR_EMPTY + MAX_STAGES,
+              BAR_ACC_EMPTY = BAR_ACC_FULL + ACC_BUFS, BAR_DRAIN = BAR_ACC_EMPTY + ACC_BUFS,
+              NUM_BARS = BAR_DRAIN + 1;
+constexpr uint32_t OFF_TMEM = OFF_BAR + NUM_BARS * 8;
+constexpr uint32_t OFF_ABORT = OFF_TMEM + 4;
+constexpr uint32_t SMEM_BYTES = OFF_ABORT + 4 + 1024;   // + slack to align the base
+static_assert(SMEM_BYTES <= 232448, "exceeds the 227 KiB per-CTA shared memory");
+constexpr float LOG2E = 1.4426950408889634f;
+
+enum Mode { LSE = 0, GRAD = 1, SUMS = 2 };
+enum Output { OUT_LSE = 0, OUT_GRAD = 1, OUT_ADD = 2, OUT_BF16 = 3 };
+
+// 64-deep k-blocks of a ring stage: two for a CTA pair (half the barrier
+// round trips for each MMA), one for a single CTA (finer stages).
+template <int CG>
+__host__ __device__ constexpr int ksub() { return CG; }
+template <int CG>
+__host__ __device__ constexpr uint32_t stage_bytes(int bn) {
+  return ksub<CG>() * (A_BLOCK + static_cast<uint32_t>(bn / CG) * BK * 2);
+}
+
+// One product: D (M x N) from A and B over K. The M and K that are the
+// counted rows are read from the device.
+struct Job {
+  CUtensorMap tmA, tmB, tmD;
+  int m, n, k;          // extents; -1: the counted rows
+  int a_mn, b_mn;       // the operand lies MN-major
+  int b_row0;           // added to B's row coordinate (a piece's first vocabulary row)
+  int d_row0;           // added to D's row coordinate
+  int splits;           // cuts of K, each with a D of its own (third coordinate)
+  int add;              // OUT_ADD: add to D (later pieces) instead of storing
+  int out;              // Output
+};
+
+struct Params {
+  Job job[2];
+  int jobs;
+  int bn, stages;            // tile columns; ring stages
+  const int* count;          // counted rows
+  // LSE and GRAD: the logits' rows and columns
+  int cols;                  // valid columns of the launch (its piece of the vocabulary)
+  int col0;                  // the first of them in the vocabulary
+  const int* target;         // [row] of the packed rows, -1: outside the vocabulary
+  float* target_logit;       // [row]
+  float2* part;              // [slot][row]: maximum and sum of exponentials
+  int64_t part_stride;
+  int carry;                 // one row of tiles: a CTA keeps its sums over its tiles
+  const float *lse, *grad;   // [row]: lse, and g
+  uint32_t* status;
+  unsigned long long timeout_ns;
+};
+
+// A unit of work: a tile of a job, or of one cut of its K.
+struct Unit {
+  const Job* job;
+  int m0, n0;      // first row of the cluster's tile, first column
+  int nb;          // tile column
+  int cut;
+  int s0, s1;      // ring stages of K
+};
+
+constexpr int GROUP_M = 8;   // tiles walk 8 rows of tiles down, then step a column (L2 reuse)
+
+// The i-th unit of cluster c of `clusters`: units c, c + clusters, ... of the
+// jobs' units one after the other.
+template <int CG>
+__device__ __forceinline__ bool next_unit(const Params& p, int count, int c, int clusters, int i,
+                                          Unit& w) {
+  int u = c + i * clusters;
+  for (int j = 0; j < p.jobs; ++j) {
+    const Job& job = p.job[j];
+    const int m = job.m < 0 ? count : job.m;
+    const int tm = (m + BM * CG - 1) / (BM * CG), tn = (job.n + p.bn - 1) / p.bn;
+    const int tiles = tm * tn;
+    if (u >= tiles * job.splits) {
+      u -= tiles * job.splits;
+      continue;
+    }
+    w.job = &job;
+    w.cut = u / tiles;
+    const int t = u - w.cut * tiles;
+    const int g = t / (GROUP_M * tn), first = g * GROUP_M;
+    const int gm = tm - first < GROUP_M ? tm - first : GROUP_M;
+    const int r = t - g * GROUP_M * tn;
+    w.m0 = (first + r % gm) * BM * CG;
+    w.nb = r / gm;
+    w.n0 = w.nb * p.bn;
+    const int k = job.k < 0 ? count : job.k;
+    const int ns = (k + BK * ksub<CG>() - 1) / (BK * ksub<CG>());
+    w.s0 = static_cast<int>(static_cast<int64_t>(w.cut) * ns / job.splits);
+    w.s1 = static_cast<int>(static_cast<int64_t>(w.cut + 1) * ns / job.splits);
+    return true;
+  }
+  return false;
+}
+
+// ------------------------------------------------------------ producers
+
+template <int CG>
+__device__ __forceinline__ void producer(const Params& p, uint32_t sbase, uint32_t rank, bool a_part,
+                                         int count, const Watchdog& wd) {
+  auto full = [&](uint32_t s) { return sbase + OFF_BAR + 8 * (BAR_FULL + s); };
+  auto empty = [&](uint32_t s) { return sbase + OFF_BAR + 8 * (BAR_EMPTY + s); };
+  const int cluster = blockIdx.x / CG, clusters = gridDim.x / CG;
+  const bool leader = a_part && rank == 0;   // arms full[s] for the pair
+  const uint32_t stages = p.stages, sbytes = stage_bytes<CG>(p.bn), tx = CG * sbytes;
+  const uint32_t b_block = static_cast<uint32_t>(p.bn / CG) * BK * 2;
+  uint32_t s = 0, ph = 0, g = 0;
+  bool ok = true;
+  Unit w;
+  for (int i = 0; ok && next_unit<CG>(p, count, cluster, clusters, i, w); ++i) {
+    const Job& job = *w.job;
+    const CUtensorMap* map = a_part ? &job.tmA : &job.tmB;
+    const bool mn = a_part ? job.a_mn : job.b_mn;
+    // this CTA's first row (or column) of the operand, and how much it holds
+    const int at = a_part ? w.m0 + static_cast<int>(rank) * BM
+                          : w.n0 + static_cast<int>(rank) * (p.bn / CG);
+    const int boxes = (a_part ? BM : p.bn / CG) / 64;
+    const int row0 = a_part ? 0 : job.b_row0;
+    for (int st = w.s0; st < w.s1; ++st) {
+      if (!wait_spin<false>(empty(s), ph ^ 1, wd)) {
+        ok = false;
+        break;
+      }
+      if (leader) mbar_arrive_expect_tx(full(s), tx);
+      const uint32_t bar = CG == 1 ? full(s) : mapa_shared(full(s), 0u);
+      uint32_t dst = sbase + s * sbytes + (a_part ? 0u : ksub<CG>() * A_BLOCK);
+#pragma unroll
+      for (int ks = 0; ks < ksub<CG>(); ++ks) {
+        const int k0 = (st * ksub<CG>() + ks) * BK;
+        auto load = [&](uint32_t to, int x, int y) {
+          if constexpr (CG == 1)
+            tma_load_3d(to, map, bar, x, y, 0);
+          else
+            tma_load_3d_pair(to, map, bar, x, y, 0);
+        };
+        if (mn) {
+          for (int b = 0; b < boxes; ++b) load(dst + b * MN_BOX, at + 64 * b, k0 + row0);
+        } else {
+          load(dst, k0, at + row0);
+        }
+        dst += a_part ? A_BLOCK : b_block;
+      }
+      ++g;
+      if (++s == stages) {
+        s = 0;
+        ph ^= 1;
+      }
+    }
+  }
+  if (!ok && leader) {
+    // Abort: the copies of the stages armed last land before the CTA goes on.
+    for (uint32_t j = g > stages ? g - stages : 0; j < g; ++j)
+      wait_drain(full(j % stages), (j / stages) & 1);
+  } else if (!ok) {
+    // Copies into a stage that the leader never armed have no barrier: give
+    // them 100 us (they take a few).
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 100000ull) __nanosleep(1000);
+  }
+}
+
+// ------------------------------------------------------------ MMA issuer
+
+template <int CG>
+__device__ __forceinline__ void mma_issuer(const Params& p, uint32_t sbase, uint32_t tmem,
+                                           uint32_t rank, int count, const Watchdog& wd) {
+  auto bar = [&](int i) { return sbase + OFF_BAR + 8 * i; };
+  auto commit = [&](uint32_t b) {
+    if constexpr (CG == 1)
+      umma_commit(b);
+    else
+      umma_commit_pair(b, static_cast<uint16_t>(0x3u));
+  };
+  const int cluster = blockIdx.x / CG, clusters = gridDim.x / CG;
+  const uint32_t stages = p.stages, sbytes = stage_bytes<CG>(p.bn);
+  const uint32_t b_block = static_cast<uint32_t>(p.bn / CG) * BK * 2;
+  uint32_t s = 0, ph = 0;
+  bool issued = false;
+  Unit w;
+  for (int i = 0; next_unit<CG>(p, count, cluster, clusters, i, w); ++i) {
+    const Job& job = *w.job;
+    const bool a_mn = job.a_mn, b_mn = job.b_mn;
+    const uint32_t idesc = idesc_bf16_f32(BM * CG, p.bn, a_mn, b_mn);
+    // 16 of K: 32 bytes along a K-major row, or 16 rows of 128 bytes
+    const uint32_t a_step = a_mn ? UMMA_K * 128 : UMMA_K * 2;
+    const uint32_t b_step = b_mn ? UMMA_K * 128 : UMMA_K * 2;
+    const uint32_t b = i & 1, aph = (i >> 1) & 1;
+    if (!wait_spin<true>(bar(BAR_ACC_EMPTY + b), aph ^ 1, wd)) break;
+    tc_fence_after_sync();
+    const uint32_t d = tmem + b * BN_MAX;
+    bool ok = true;
+    for (int st = w.s0; st < w.s1; ++st) {
+      if (!wait_spin<true>(bar(BAR_FULL + s), ph, wd)) {
+        ok = false;
+        break;
+      }
+      const uint32_t a_addr = sbase + s * sbytes, b_addr = a_addr + ksub<CG>() * A_BLOCK;
+#pragma unroll
+      for (int kk = 0; kk < ksub<CG>() * (BK / UMMA_K); ++kk) {
+        const int blk = kk / (BK / UMMA_K), kin = kk % (BK / UMMA_K);
+        const uint32_t aa = a_addr + blk * A_BLOCK + kin * a_step;
+        const uint32_t bb = b_addr + blk * b_block + kin * b_step;
+        const uint64_t ad = a_mn ? sdesc_mnmajor_sw128(aa) : sdesc_kmajor_sw128(aa);
+        const uint64_t bd = b_mn ? sdesc_mnmajor_sw128(bb) : sdesc_kmajor_sw128(bb);
+        const uint32_t acc = (st != w.s0 || kk != 0) ? 1u : 0u;
+        if constexpr (CG == 1)
+          umma_bf16(d, ad, bd, idesc, acc);
+        else
+          umma_bf16_pair(d, ad, bd, idesc, acc);
+      }
+      issued = true;
+      commit(bar(BAR_EMPTY + s));
+      if (++s == stages) {
+        s = 0;
+        ph ^= 1;
+      }
+    }
+    if (!ok) break;
+    if (w.s1 > w.s0) {
+      commit(bar(BAR_ACC_FULL + b));
+    } else {   // nothing to sum: signal the accumulator barriers directly
+      for (int r = 0; r < CG; ++r) {
+        if constexpr (CG == 1)
+          mbar_arrive(bar(BAR_ACC_FULL + b));
+        else
+          mbar_arrive_cluster(mapa_shared(bar(BAR_ACC_FULL + b), r));
+      }
+    }
+  }
+  if (issued) {
+    // Every MMA issued has finished once this arrives (also after an abort).
+    if constexpr (CG == 1)
+      umma_commit(bar(BAR_DRAIN));
+    else
+      umma_commit_pair(bar(BAR_DRAIN), static_cast<uint16_t>(1u << rank));
+    wait_drain(bar(BAR_DRAIN), 0);
+  }
+}
+
+// ------------------------------------------------------------ epilogue
+
+// exp(x - y). The difference is taken before the change of base: a logit that
+// is the maximum, or all of the sum, gives exactly 1, so the gradient of a token
+// that the model is sure of does not drown in the rounding of a large logit.
+__device__ __forceinline__ float exp_diff(float x, float y) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"((x - y) * LOG2E));
+  return r;
+}
+
+template <int CG, int MODE>
+__device__ __forceinline__ void epilogue(const Params& p, uint32_t sbase, uint8_t* smem,
+                                         uint32_t tmem, uint32_t rank, int warp, int count,
+                                         const Watchdog& wd) {
+  const int lane = threadIdx.x & 31;
+  const int e = warp - WARP_EPI0;
+  const int q = warp & 3;         // the TMEM lane quarter that this warp may read
+  const int hf = e / 4;           // it takes the unit's column blocks b with b % 2 == hf
+  auto bar = [&](int i) { return sbase + OFF_BAR + 8 * i; };
+  const int cluster = blockIdx.x / CG, clusters = gridDim.x / CG;
+  uint8_t* out = smem + OFF_OUT + e * OUT_BYTES;
+  const uint32_t out_row = lane * 128, swz = lane & 7;   // 128-byte swizzle, as the TMA reads it
+  float top = -INFINITY, sum = 0.0f;                     // LSE
+  int row = 0;
+  auto flush = [&](int slot) {
+    if (row < count) p.part[static_cast<int64_t>(slot) * p.part_stride + row] = make_float2(top, sum);
+    top = -INFINITY;
+    sum = 0.0f;
+  };
+  bool any = false;
+  Unit w;
+  for (int i = 0; next_unit<CG>(p, count, cluster, clusters, i, w); ++i) {
+    const Job& job = *w.job;
+    any = true;
+    const int part0 = w.m0 + static_cast<int>(rank) * BM;   // this CTA's first row
+    row = part0 + 32 * q + lane;
+    const int m = job.m < 0 ? count : job.m;
+    const int width = min(p.bn, (MODE == SUMS ? job.n : p.cols) - w.n0);   // valid columns
+    const int step = MODE == LSE || job.out == OUT_ADD ? EPI_N : 2 * EPI_N;   // columns of a block
+    const int blocks = part0 < m ? (width + step - 1) / step : 0;
+    int target = -1;
+    float lse = 0.0f, grad = 0.0f;
+    if (MODE != SUMS && row < count) {
+      target = p.target[row] - p.col0 - w.n0;   // the target's column in this tile, if in it
+      if (MODE == GRAD) {
+        lse = p.lse[row];
+        grad = p.grad[row];
+      }
+    }
+    const uint32_t b = i & 1, aph = (i >> 1) & 1;
+    auto release = [&]() {
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 1 || rank == 0)
+          mbar_arrive(bar(BAR_ACC_EMPTY + b));
+        else
+          mbar_arrive_cluster(mapa_shared(bar(BAR_ACC_EMPTY + b), 0));
+      }
+    };
+    if (!warp_wait_spin(bar(BAR_ACC_FULL + b), aph, wd)) break;
+    tc_fence_after_sync();
+    const uint32_t tacc = tmem + (static_cast<uint32_t>(32 * q) << 16) + b * BN_MAX;
+    if (hf >= blocks) release();
+    for (int j = hf; j < blocks; j += 2) {
+      uint32_t a0[32];
+      if constexpr (MODE == LSE) {
+        tmem_ld_32x32b_x32(tacc + j * EPI_N, a0);
+        tmem_wait_ld();
+        if (j + 2 >= blocks) release();
+        const int valid = width - j * EPI_N;
+        float most = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < 32; ++x) {
+          const float z = x < valid ? __uint_as_float(a0[x]) : -INFINITY;
+          if (target == j * EPI_N + x) p.target_logit[row] = __uint_as_float(a0[x]);
+          a0[x] = __float_as_uint(z);
+          most = fmaxf(most, z);
+        }
+        const float next = fmaxf(top, most);
+        const float base = next == -INFINITY ? 0.0f : next;   // nothing finite yet: all terms 0
+        float add = 0.0f;
+#pragma unroll
+        for (int x = 0; x < 32; ++x) add += exp_diff(__uint_as_float(a0[x]), base);
+        sum = fmaf(sum, exp_diff(top, base), add);
+        top = next;
+        continue;
+      }
+      const bool has_acc = w.s1 > w.s0;
+      if (MODE == SUMS && job.out == OUT_ADD) {
+        if (has_acc) {
+          tmem_ld_32x32b_x32(tacc + j * EPI_N, a0);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) a0[x] = 0u;
+        }
+        if (j + 2 >= blocks) release();
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(out + out_row + ((c ^ swz) << 4)) =
+              make_uint4(a0[4 * c], a0[4 * c + 1], a0[4 * c + 2], a0[4 * c + 3]);
+      } else {
+        uint32_t a1[32];
+        if (has_acc) {
+          tmem_ld_32x32b_x32(tacc + 2 * j * EPI_N, a0);
+          tmem_ld_32x32b_x32(tacc + (2 * j + 1) * EPI_N, a1);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) a0[x] = a1[x] = 0u;
+        }
+        if (j + 2 >= blocks) release();
+        if constexpr (MODE == GRAD) {
+          // Rows that are not there (or have no gradient) and columns past
+          // the vocabulary are 0: the products after this one run over them.
+          const int valid = grad != 0.0f ? width - 2 * j * EPI_N : 0;
+          const int hit = target - 2 * j * EPI_N;
+          auto gradient = [&](uint32_t acc, int x) {
+            float pr = exp_diff(__uint_as_float(acc), lse);
+            if (x == hit) pr -= 1.0f;
+            return x < valid ? pr * grad : 0.0f;
+          };
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            a0[x] = __float_as_uint(gradient(a0[x], x));
+            a1[x] = __float_as_uint(gradient(a1[x], 32 + x));
+          }
+        }
+        if (lane == 0) bulk_wait_read<0>();   // this warp's previous block has been read
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint32_t* a = c < 4 ? a0 : a1;
+          const int o = 8 * (c & 3);
+          uint4 v;
+          v.x = pack_bf16x2(__uint_as_float(a[o]), __uint_as_float(a[o + 1]));
+          v.y = pack_bf16x2(__uint_as_float(a[o + 2]), __uint_as_float(a[o + 3]));
+          v.z = pack_bf16x2(__uint_as_float(a[o + 4]), __uint_as_float(a[o + 5]));
+          v.w = pack_bf16x2(__uint_as_float(a[o + 6]), __uint_as_float(a[o + 7]));
+          *reinterpret_cast<uint4*>(out + out_row + ((c ^ swz) << 4)) = v;
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        const int x = w.n0 + j * step, y = job.d_row0 + part0 + 32 * q;
+        if (MODE == SUMS && job.add)
+          tma_add_3d(&job.tmD, smem_addr(out), x, y, w.cut);
+        else
+          tma_store_3d(&job.tmD, smem_addr(out), x, y, w.cut);
+        bulk_commit();
+      }
+    }
+    if (MODE == LSE && !p.carry) flush(2 * w.nb + hf);
+  }
+  if (MODE == LSE && p.carry && any) flush(2 * cluster + hf);
+  if (MODE != LSE) {
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+  }
+}
+
+// ------------------------------------------------------------ product kernel
+
+template <int CG, int MODE>
+__global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
+  uint8_t* smem = smem_raw + pad;
+  const uint32_t sbase = raw + pad;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0);
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 1 ? 0u : cluster_ctarank();
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + OFF_ABORT);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
+  if (warp == WARP_A && lane == 0) {
+    auto bar = [&](int i) { return sbase + OFF_BAR + 8 * i; };
+    for (int s = 0; s < MAX_STAGES; ++s) {
+      mbar_init(bar(BAR_FULL + s), 1);
+      mbar_init(bar(BAR_EMPTY + s), 1);
+    }
+    for (int b = 0; b < ACC_BUFS; ++b) {
+      mbar_init(bar(BAR_ACC_FULL + b), 1);
+      mbar_init(bar(BAR_ACC_EMPTY + b), EPI_WARPS * CG);
+    }
+    mbar_init(bar(BAR_DRAIN), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    for (int j = 0; j < p.jobs; ++j) {
+      prefetch_tensormap(&p.job[j].tmA);
+      prefetch_tensormap(&p.job[j].tmB);
+      if (MODE != LSE) prefetch_tensormap(&p.job[j].tmD);
+    }
+  }
+  if (warp == WARP_MMA) {
+    if constexpr (CG == 1) {
+      tmem_alloc(smem_addr(tmem_slot), ACC_BUFS * BN_MAX);
+      tmem_relinquish();
+    } else {
+      tmem_alloc_pair(smem_addr(tmem_slot), ACC_BUFS * BN_MAX);
+      tmem_relinquish_pair();
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if constexpr (CG > 1) cluster_sync();
+  tc_fence_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  const Watchdog wd{abort_flag, p.status, p.timeout_ns};
+  // The set-up above overlaps the previous kernel's end; nothing below does.
+  grid_dependency_wait();
+  if (threadIdx.x == 0) grid_launch_dependents();
+  const int count = *p.count;
+
+  if (warp == WARP_A || warp == WARP_B) {
+    if (lane == 0) producer<CG>(p, sbase, rank, warp == WARP_A, count, wd);
+  } else if (warp == WARP_MMA) {
+    if (lane == 0 && rank == 0) mma_issuer<CG>(p, sbase, tmem, rank, count, wd);
+  } else {
+    epilogue<CG, MODE>(p, sbase, smem, tmem, rank, warp, count, wd);
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  if constexpr (CG > 1) cluster_sync();
+  if (warp == WARP_MMA) {
+    tc_fence_after_sync();
+    if constexpr (CG == 1)
+      tmem_dealloc(tmem, ACC_BUFS * BN_MAX);
+    else
+      tmem_dealloc_pair(tmem, ACC_BUFS * BN_MAX);
+  }
+}
+
+// ------------------------------------------------------------ packing the counted rows
+
+struct PackParams {
+  const uint16_t* x;          // T x H bf16
+  int64_t ldx;
+  const void* target;         // T int64 or int32
+  int wide_target;            // int64
+  int64_t ignore;
+  int rows, cols, vocab;
+  int wide;                   // x's rows allow 16-byte accesses
+  int chunk;                  // rows of a block, at most PACK_THREADS
+  uint16_t* packed;           // T x H
+  int* place;                 // [row]: its packed row, -1 if not counted
+  int* target_out;            // [packed row]
+  int* count;
+  float* target_logit;        // LSE: [packed row], NaN where the target is outside the vocabulary
+  const float *lse, *grad;    // GRAD: [row] (grad: grad_step 0 has one for all)
+  int grad_step;
+  float *lse_out, *grad_out;  // GRAD: [packed row]
+};
+
+constexpr int PACK_THREADS = 256;
+constexpr int NO_ROW = -0x7FFFFFFF - 1;
+
+__device__ __forceinline__ int64_t target_of(const PackParams& p, int row) {
+  return p.wide_target ? static_cast<const int64_t*>(p.target)[row]
+                       : static_cast<int64_t>(static_cast<const int*>(p.target)[row]);
+}
+
+// The sum over the block of a value a thread, in every thread.
+__device__ __forceinline__ int block_sum(int v, int* box) {
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) box[threadIdx.x >> 5] = v;
+  __syncthreads();
+  int s = 0;
+  for (int w = 0; w < PACK_THREADS / 32; ++w) s += box[w];
+  __syncthreads();
+  return s;
+}
+
+// Block b packs the counted rows of [b * chunk, (b + 1) * chunk). Each block
+// counts all targets itself (8 bytes a row, from L2 after the first block), which
+// saves a scan of its own before it. The rows that follow the last counted
+// one up to a multiple of 128 are zeroed, since dweight's product sums over
+// them; the uncounted rows' blocks do that.
+__global__ void __launch_bounds__(PACK_THREADS) pack_kernel(const __grid_constant__ PackParams p) {
+  __shared__ int box[PACK_THREADS / 32];
+  __shared__ int dst_row[PACK_THREADS];   // [row of the chunk]: packed row; -1 - packed row: zeros; NO_ROW
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int r0 = blockIdx.x * p.chunk, r1 = min(p.rows, r0 + p.chunk);
+  int before = 0, all = 0;
+#pragma unroll 4
+  for (int r = threadIdx.x; r < p.rows; r += PACK_THREADS) {
+    const int c = target_of(p, r) != p.ignore;
+    all += c;
+    before += r < r0 ? c : 0;
+  }
+  before = block_sum(before, box);
+  all = block_sum(all, box);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.count = all;
+  const int row = r0 + threadIdx.x;
+  const bool mine = threadIdx.x < p.chunk && row < r1;
+  const int64_t t = mine ? target_of(p, row) : p.ignore;
+  const bool counted = mine && t != p.ignore;
+  const unsigned vote = __ballot_sync(0xffffffffu, counted);
+  if ((threadIdx.x & 31) == 0) box[threadIdx.x >> 5] = __popc(vote);
+  __syncthreads();
+  int rank = before + __popc(vote & ((1u << (threadIdx.x & 31)) - 1u));
+  for (int w = 0; w < static_cast<int>(threadIdx.x >> 5); ++w) rank += box[w];
+  if (mine) {
+    p.place[row] = counted ? rank : -1;
+    if (counted) {
+      const bool inside = t >= 0 && t < p.vocab;
+      p.target_out[rank] = inside ? static_cast<int>(t) : -1;
+      if (p.target_logit) p.target_logit[rank] = inside ? 0.0f : __int_as_float(0x7FC00000);
+      if (p.lse_out) {
+        p.lse_out[rank] = p.lse[row];
+        p.grad_out[rank] = inside ? p.grad[static_cast<int64_t>(row) * p.grad_step] : 0.0f;
+      }
+    }
+    // the k-th uncounted row zeroes the k-th packed row after the counted ones
+    const int behind = all + (row - rank);
+    dst_row[threadIdx.x] = counted ? rank : behind < (all + 127) / 128 * 128 ? -1 - behind : NO_ROW;
+  }
+  __syncthreads();
+  const int groups = p.cols / 8;   // cols is a multiple of 8
+  for (int v = threadIdx.x; v < (r1 - r0) * groups; v += PACK_THREADS) {
+    const int r = v / groups, c = (v - r * groups) * 8;
+    const int to = dst_row[r];
+    if (to == NO_ROW) continue;
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (to >= 0) {
+      const uint16_t* src = p.x + static_cast<int64_t>(r0 + r) * p.ldx + c;
+      if (p.wide) {
+        w = *reinterpret_cast<const uint4*>(src);
+      } else {
+        w.x = src[0] | static_cast<uint32_t>(src[1]) << 16;
+        w.y = src[2] | static_cast<uint32_t>(src[3]) << 16;
+        w.z = src[4] | static_cast<uint32_t>(src[5]) << 16;
+        w.w = src[6] | static_cast<uint32_t>(src[7]) << 16;
+      }
+    }
+    *reinterpret_cast<uint4*>(p.packed + static_cast<int64_t>(to >= 0 ? to : -1 - to) * p.cols + c) = w;
+  }
+}
+
+// ------------------------------------------------------------ joining the sums
+
+struct JoinParams {
+  const float2* part;
+  int64_t part_stride;
+  int slots;
+  const int* place;
+  const int* count;
+  const float* target_logit;
+  int rows;
+  float *loss, *lse, *mean;   // mean may be NULL
+  float* block_sum;           // [block]
+  uint32_t* done;             // blocks finished; zero at launch, left zero
+};
+
+constexpr int JOIN_ROWS = 32, JOIN_LANES = 32;
+
+// lse and loss of 32 rows a block, from the partial maxima and sums in slot
+// order; the block that finishes last adds the blocks' loss sums in block
+// order, so the mean's bits do not depend on which one that is.
+__global__ void __launch_bounds__(JOIN_ROWS* JOIN_LANES)
+    join_kernel(const __grid_constant__ JoinParams p) {
+  __shared__ float2 box[JOIN_LANES][JOIN_ROWS];
+  __shared__ float sums[JOIN_LANES];
+  __shared__ bool last;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int x = threadIdx.x % JOIN_ROWS, lane = threadIdx.x / JOIN_ROWS;
+  const int row = blockIdx.x * JOIN_ROWS + x;
+  const int at = row < p.rows ? p.place[row] : -1;
+  float top = -INFINITY, sum = 0.0f;
+  if (at >= 0) {
+#pragma unroll 4
+    for (int s = lane; s < p.slots; s += JOIN_LANES) {
+      const float2 v = p.part[s * p.part_stride + at];
+      const float next = fmaxf(top, v.x), base = next == -INFINITY ? 0.0f : next;
+      sum = sum * exp_diff(top, base) + v.y * exp_diff(v.x, base);
+      top = next;
+    }
+  }
+  box[lane][x] = make_float2(top, sum);
+  __syncthreads();
+  float loss = 0.0f;
+  if (lane == 0) {
+    for (int l = 1; l < JOIN_LANES; ++l) {
+      const float2 v = box[l][x];
+      const float next = fmaxf(top, v.x), base = next == -INFINITY ? 0.0f : next;
+      sum = sum * exp_diff(top, base) + v.y * exp_diff(v.x, base);
+      top = next;
+    }
+    if (row < p.rows) {
+      const float rest = at >= 0 ? logf(sum) : 0.0f;
+      loss = at >= 0 ? (top - p.target_logit[at]) + rest : 0.0f;
+      p.lse[row] = at >= 0 ? top + rest : 0.0f;
+      p.loss[row] = loss;
+    }
+    for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
+  }
+  if (!p.mean) return;
+  if (threadIdx.x == 0) {
+    p.block_sum[blockIdx.x] = loss;
+    __threadfence();
+    last = atomicAdd(p.done, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  float s = 0.0f;
+  for (int b = threadIdx.x; b < static_cast<int>(gridDim.x); b += blockDim.x)
+    s += __ldcg(p.block_sum + b);
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (x == 0) sums[lane] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s = 0.0f;
+    for (int l = 0; l < JOIN_LANES; ++l) s += sums[l];
+    const int n = *p.count;
+    const float share = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
+    p.mean[0] = s * share;
+    p.mean[1] = share;
+    *p.done = 0u;
+  }
+}
+
+// ------------------------------------------------------------ dx
+
+struct SpreadParams {
+  const float* sums;    // [cut][packed row][col] fp32
+  int cuts;
+  int64_t cut_stride;
+  const int* place;
+  int rows, cols;
+  uint16_t* dx;
+  int64_t lddx;
+};
+
+constexpr int SPREAD_THREADS = 256;
+
+// dx of every row: the cuts' sums of its packed row added in order and rounded
+// once, or zeros. Four columns a thread.
+__global__ void __launch_bounds__(SPREAD_THREADS) spread_kernel(const __grid_constant__ SpreadParams p) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int quads = p.cols / 4;
+  const int64_t v = static_cast<int64_t>(blockIdx.x) * SPREAD_THREADS + threadIdx.x;
+  const int64_t row = v / quads;
+  if (row >= p.rows) return;
+  const int c = static_cast<int>(v - row * quads) * 4;
+  const int at = p.place[row];
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (at >= 0) {
+    const float* src = p.sums + static_cast<int64_t>(at) * p.cols + c;
+#pragma unroll 4
+    for (int k = 0; k < p.cuts; ++k) {
+      const float4 f = *reinterpret_cast<const float4*>(src + k * p.cut_stride);
+      s.x += f.x;
+      s.y += f.y;
+      s.z += f.z;
+      s.w += f.w;
+    }
+  }
+  uint2 out;
+  out.x = pack_bf16x2(s.x, s.y);
+  out.y = pack_bf16x2(s.z, s.w);
+  *reinterpret_cast<uint2*>(p.dx + row * p.lddx + c) = out;
+}
+
+}  // namespace ce
+}  // namespace gws

@@ -157,6 +157,16 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src,
       : "memory");
 }
 
+// As tma_store_3d, but adds the f32 elements to what the tensor holds.
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* m, uint32_t src, int x, int y,
+                                           int z) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group"
+      " [%0, {%1, %2, %3}], [%4];" ::"l"(reinterpret_cast<uint64_t>(m)),
+      "r"(x), "r"(y), "r"(z), "r"(src)
+      : "memory");
+}
+
 // 1-D bulk copy of `bytes` from shared to global memory (both 16-byte
 // aligned, bytes a multiple of 16); joins this thread's bulk group.
 __device__ __forceinline__ void bulk_store_1d(void* dst, uint32_t src, uint32_t bytes) {
@@ -346,6 +356,23 @@ __device__ __forceinline__ uint64_t sdesc_kmajor_sw128(uint32_t saddr) {
   return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
          (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
          (static_cast<uint64_t>(2) << 61);
+}
+
+// The same instruction descriptor with either operand MN-major (bit 15: A,
+// bit 16: B).
+__host__ __device__ constexpr uint32_t idesc_bf16_f32(int m, int n, bool a_mn, bool b_mn) {
+  return idesc_bf16_f32(m, n) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+}
+
+// Shared-memory matrix descriptor of an MN-major operand stored with the
+// 128-byte swizzle, as TMA writes boxes of 64 (M or N, contiguous) x 64 (K):
+// each k is a 128-byte row, so 8 of them lie 1024 bytes apart (stride byte
+// offset), and the next 64 of M or N is the next box, 8192 bytes on (leading
+// byte offset). Stepping K by 16 adds 2048 bytes to the start address.
+__device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) |
+         (static_cast<uint64_t>(8192 >> 4) << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
+         (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
 }
 
 }  // namespace gws

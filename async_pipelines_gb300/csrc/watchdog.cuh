@@ -135,7 +135,7 @@ __device__ __forceinline__ bool warp_wait_spin(uint32_t bar, uint32_t parity,
 // lane 0 polls with acquire loads; on success every lane loads the flag once
 // more with acquire, so each thread itself is ordered after the writer's
 // partial stores.
-__device__ __noinline__ bool flag_wait_slow(const uint32_t* f, const Watchdog& wd) {
+inline __device__ __noinline__ bool flag_wait_slow(const uint32_t* f, const Watchdog& wd) {
   const uint64_t t0 = global_timer_ns();
   for (uint32_t it = 1;; ++it) {
     if (ld_acquire_gpu(f) != 0u) return true;

@@ -15,7 +15,10 @@ BF16, F16, F32 = 0, 1, 2                                  # gemm_ws_dtype
 NORM_SAME, NORM_E4M3_ROW, NORM_E4M3_GROUP = 0, 1, 2       # gemm_ws_norm_output
 QUANT_GROUP = 128                                         # columns of one scale
 
-EXPORTS = ("gemm_ws_dropout", "gemm_ws_add_rms_norm", "gemm_ws_add_rms_norm_backward")
+EXPORTS = ("gemm_ws_dropout", "gemm_ws_add_rms_norm", "gemm_ws_add_rms_norm_backward",
+           "gemm_ws_linear_ce", "gemm_ws_linear_ce_backward", "gemm_ws_linear_ce_workspace")
+
+TARGET_BYTES = {torch.int64: 8, torch.int32: 4}
 
 _DTYPES = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
 
@@ -29,8 +32,14 @@ def declare(lib) -> None:
                                          vp, i64, i64, f32, f64, vp, vp]
     lib.gemm_ws_add_rms_norm_backward.argtypes = [vp, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp,
                                                   i64, vp, i64, vp, i64, i64, f64, vp, vp]
+    lib.gemm_ws_linear_ce.argtypes = [vp, vp, i64, vp, i64, vp, i32, i64, vp, vp, vp, i64, i64,
+                                      i64, vp, i64, vp]
+    lib.gemm_ws_linear_ce_backward.argtypes = [vp, vp, i64, vp, i64, vp, i32, i64, vp, vp, i32, vp,
+                                               i64, vp, i64, i64, i64, i64, vp, i64, vp]
+    lib.gemm_ws_linear_ce_workspace.argtypes = [vp, i64, i64, i64, i32]
     for name in EXPORTS:
         getattr(lib, name).restype = i32
+    lib.gemm_ws_linear_ce_workspace.restype = i64
 
 
 def _rows(name, t, shape, dtype):
@@ -152,3 +161,90 @@ class LmOps:
         if rc:
             self._raise(rc, "gemm_ws_add_rms_norm_backward")
         return dx
+
+    # -------------------------------------------------------------- cross entropy
+
+    def linear_cross_entropy_workspace(self, tokens, hidden, vocab, backward=False) -> int:
+        """Bytes of workspace that one call needs."""
+        n = self.lib.gemm_ws_linear_ce_workspace(self.handle, tokens, hidden, vocab,
+                                                 int(bool(backward)))
+        if n < 0:
+            self._raise(-n, "gemm_ws_linear_ce_workspace")
+        return n
+
+    def _workspace(self, workspace, need, x, stream):
+        """(tensor, pointer, bytes): the caller's, or one from torch's allocator for this call."""
+        if workspace is None:
+            if stream is None:
+                workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            else:   # allocated for the stream that the call runs on
+                if not isinstance(stream, torch.cuda.Stream):
+                    stream = torch.cuda.ExternalStream(int(stream), device=x.device)
+                with torch.cuda.stream(stream):
+                    workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        elif workspace.dtype is not torch.uint8 or not workspace.is_cuda or \
+                not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous uint8 CUDA tensor")
+        return workspace, workspace.data_ptr(), workspace.numel()
+
+    def _ce_operands(self, x, weight, targets):
+        bf16 = torch.bfloat16
+        if x.dim() != 2 or weight.dim() != 2 or weight.shape[1] != x.shape[1]:
+            raise ValueError("x must be (tokens, hidden) and weight (vocab, hidden)")
+        px, ldx = _rows("x", x, x.shape, bf16)
+        pw, ldw = _rows("weight", weight, weight.shape, bf16)
+        size = TARGET_BYTES.get(targets.dtype)
+        if size is None:
+            raise ValueError("targets must be int64 or int32")
+        return px, ldx, pw, ldw, _flat("targets", targets, x.shape[0], targets.dtype), size
+
+    def linear_cross_entropy(self, x, weight, targets, loss, lse, mean=None, ignore_index=-100,
+                             workspace=None, stream=None):
+        """Softmax cross entropy of x @ weight^T, the logits never held.
+
+        x: (tokens, hidden), weight: (vocab, hidden), bf16; targets: (tokens,)
+        int64 or int32. loss, lse: (tokens,) f32; mean: 2 f32, the mean loss
+        over the counted tokens and 1 / their number. A token whose target is
+        ignore_index is not counted: loss and lse 0, its row not read; one
+        whose target is outside the vocabulary has loss NaN. Without a
+        workspace (uint8, linear_cross_entropy_workspace bytes) the call takes
+        one from torch's allocator.
+        """
+        px, ldx, pw, ldw, pt, size = self._ce_operands(x, weight, targets)
+        tokens, hidden = x.shape
+        vocab = weight.shape[0]
+        f32 = torch.float32
+        ploss, plse = _flat("loss", loss, tokens, f32), _flat("lse", lse, tokens, f32)
+        pmean = _flat("mean", mean, 2, f32)
+        need = self.linear_cross_entropy_workspace(tokens, hidden, vocab)
+        workspace, pws, bytes_ = self._workspace(workspace, need, x, stream)
+        rc = self.lib.gemm_ws_linear_ce(
+            self.handle, px, ldx, pw, ldw, pt, size, ignore_index, ploss, plse, pmean, tokens,
+            hidden, vocab, pws, bytes_, self._stream_of(stream))
+        if rc:
+            self._raise(rc, "gemm_ws_linear_ce")
+        return loss
+
+    def linear_cross_entropy_backward(self, x, weight, targets, lse, grad, dx=None, dweight=None,
+                                      ignore_index=-100, workspace=None, stream=None):
+        """Gradients of sum(grad * loss): dx (tokens, hidden), dweight (vocab, hidden), bf16.
+
+        lse: what linear_cross_entropy wrote. grad: f32, one for each token, or
+        one element for all: mean[1:] gives the gradient of the mean.
+        """
+        px, ldx, pw, ldw, pt, size = self._ce_operands(x, weight, targets)
+        tokens, hidden = x.shape
+        vocab = weight.shape[0]
+        bf16, f32 = torch.bfloat16, torch.float32
+        step = 0 if grad.numel() == 1 else 1
+        plse, pgrad = _flat("lse", lse, tokens, f32), _flat("grad", grad, tokens if step else 1, f32)
+        pdx, lddx = _rows("dx", dx, x.shape, bf16)
+        pdw, lddw = _rows("dweight", dweight, weight.shape, bf16)
+        need = self.linear_cross_entropy_workspace(tokens, hidden, vocab, backward=True)
+        workspace, pws, bytes_ = self._workspace(workspace, need, x, stream)
+        rc = self.lib.gemm_ws_linear_ce_backward(
+            self.handle, px, ldx, pw, ldw, pt, size, ignore_index, plse, pgrad, step, pdx, lddx,
+            pdw, lddw, tokens, hidden, vocab, pws, bytes_, self._stream_of(stream))
+        if rc:
+            self._raise(rc, "gemm_ws_linear_ce_backward")
+        return dx, dweight

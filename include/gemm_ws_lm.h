@@ -8,6 +8,9 @@
  *   gemm_ws_add_rms_norm            h = residual + dropout(x); y = weight * h / rms(h),
  *                                   also in 8 bits with scales
  *   gemm_ws_add_rms_norm_backward   its gradients
+ *   gemm_ws_linear_ce               softmax cross entropy of x * weight^T over a
+ *                                   vocabulary, the logits never held
+ *   gemm_ws_linear_ce_backward      its gradients
  *
  * Everything that gemm_ws.h says of handles, threads, streams, ownership and
  * errors holds here: calls are asynchronous on `stream`, allocate nothing,
@@ -92,6 +95,51 @@ int gemm_ws_add_rms_norm_backward(gemm_ws_t* h, int dtype, const void* dy, int64
                                   int64_t lddx, void* dresidual, int64_t lddr, void* dweight,
                                   int64_t rows, int64_t cols, double p, const uint64_t* rng,
                                   void* stream);
+
+/* Softmax cross entropy of z = x * weight^T over a vocabulary, in pieces of the
+ * vocabulary, the logits z never held:
+ *   lse[t] = log sum_j exp(z[t][j]);  loss[t] = lse[t] - z[t][target[t]].
+ *  - x: tokens x hidden bf16; weight: vocab x hidden bf16; target: tokens
+ *    int64 (target_bytes 8) or int32 (4).
+ *  - A token whose target is `ignore` is not counted: its loss and lse are 0
+ *    and its row of x is not read (it may hold anything). A counted token
+ *    whose target is outside [0, vocab) has loss NaN, and no gradient.
+ *  - loss, lse: tokens fp32; mean: two fp32, the mean loss over the counted
+ *    tokens and 1 / their number (both 0 with none), or NULL.
+ *  - workspace: gemm_ws_linear_ce_workspace bytes on the device, 256-byte
+ *    aligned, for this call alone (its contents mean nothing before or after).
+ *  - hidden: a multiple of 8; weight 16-byte aligned, ldw a multiple of 8 (x
+ *    may lie anywhere). 0 <= tokens, 1 <= vocab, 8 <= hidden, each < 2^31,
+ *    tokens * hidden, vocab * hidden and tokens * vocab < 2^40.
+ * Products in bf16 with fp32 sums in tensor memory; everything after them in
+ * fp32. Launches three kernels. */
+int gemm_ws_linear_ce(gemm_ws_t* h, const uint16_t* x, int64_t ldx, const uint16_t* weight,
+                      int64_t ldw, const void* target, int target_bytes, int64_t ignore,
+                      float* loss, float* lse, float* mean, int64_t tokens, int64_t hidden,
+                      int64_t vocab, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The gradients of sum_t grad[t] * loss[t].
+ *  - x, weight, target, ignore: as given to gemm_ws_linear_ce; lse: what it wrote.
+ *  - grad: fp32, one for each token (grad_step 1) or one for all (grad_step
+ *    0; with &mean[1] the gradient of the mean loss).
+ *  - dx: tokens x hidden bf16, zero for uncounted tokens; dweight: vocab x
+ *    hidden bf16; either may be NULL. 16-byte aligned, lddx and lddw multiples
+ *    of 8.
+ * A piece's gradient of the logits is rounded to bf16; the sums over the
+ * vocabulary (dx) and the tokens (dweight) are fp32 and rounded once. */
+int gemm_ws_linear_ce_backward(gemm_ws_t* h, const uint16_t* x, int64_t ldx,
+                               const uint16_t* weight, int64_t ldw, const void* target,
+                               int target_bytes, int64_t ignore, const float* lse,
+                               const float* grad, int grad_step, uint16_t* dx, int64_t lddx,
+                               uint16_t* dweight, int64_t lddw, int64_t tokens, int64_t hidden,
+                               int64_t vocab, void* workspace, int64_t workspace_bytes,
+                               void* stream);
+
+/* Workspace bytes of gemm_ws_linear_ce (backward 0) or its backward (nonzero)
+ * for these sizes on this handle; negative (a gemm_ws_status, negated) for
+ * sizes that they refuse. Host arithmetic only. */
+int64_t gemm_ws_linear_ce_workspace(gemm_ws_t* h, int64_t tokens, int64_t hidden, int64_t vocab,
+                                    int backward);
 
 #ifdef __cplusplus
 }

@@ -67,3 +67,25 @@ def add_rms_norm_backward(dy, h, weight, rstd, dh=None, keep=None):
         size = size + dh.double().abs()
     dx = dres if keep is None else apply_keep(dres, keep)
     return dx, dres, (dy * n).sum(0), size, (dy * n).abs().sum(0)
+
+
+def linear_cross_entropy(x, weight, target, ignore):
+    """loss, lse and the mean over the counted tokens, in 64 bits."""
+    z = x.double() @ weight.double().T
+    counted = target != ignore
+    lse = torch.where(counted, torch.logsumexp(z, 1), 0.0)
+    at = torch.where(counted, target, 0)
+    loss = torch.where(counted, lse - z.gather(1, at[:, None])[:, 0], 0.0)
+    n = int(counted.sum())
+    return loss, lse, float(loss.sum()) / max(n, 1)
+
+
+def linear_cross_entropy_backward(x, weight, target, grad, ignore):
+    """dx and dweight, and the sums of magnitudes that their errors go by."""
+    x, w = x.double(), weight.double()
+    counted = target != ignore
+    x = torch.where(counted[:, None], x, 0.0)
+    g = torch.softmax(x @ w.T, 1)
+    g[torch.arange(len(target)), torch.where(counted, target, 0)] -= 1.0
+    g = torch.where(counted[:, None], g * grad.double()[:, None], 0.0)
+    return g @ w, g.T @ x, g.abs() @ w.abs(), g.abs().T @ x.abs()
