@@ -46,12 +46,14 @@ bool bad_matrix(const Mat& m, int64_t cols) {
 
 // p and rng as a launch takes them. Returns false where p is not in [0, 1] or
 // a mask is wanted and rng is missing.
-bool make_dropout(double p, const uint64_t* rng, gws::Dropout* d) {
+bool make_dropout(const gemm_ws* h, double p, const uint64_t* rng, gws::Dropout* d) {
   if (!(p >= 0.0 && p <= 1.0)) return false;
-  d->below = static_cast<uint32_t>(std::nearbyint(p * 65536.0));
-  d->rng = rng;
-  d->scale = d->below < 65536 ? static_cast<float>(65536.0 / (65536 - d->below)) : 0.0f;
-  return d->below == 0 || (rng && reinterpret_cast<uintptr_t>(rng) % 8 == 0);
+  const int64_t below = static_cast<int64_t>(std::nearbyint(p * 65536.0));
+  d->on = below > 0;
+  d->rng = d->on ? rng : reinterpret_cast<const uint64_t*>(h->work);
+  d->limit = static_cast<uint32_t>((below << 16) - 1);
+  d->scale = below < 65536 ? static_cast<float>(65536.0 / (65536 - below)) : 0.0f;
+  return !d->on || (rng && reinterpret_cast<uintptr_t>(rng) % 8 == 0);
 }
 
 // A launch that may start while the stream's previous kernel ends; each of
@@ -75,6 +77,11 @@ int launch(gemm_ws* h, void (*kernel)(P), int64_t blocks, int threads, size_t sm
   return e == cudaSuccess ? GEMM_WS_OK : cuda_fail(h, e);
 }
 
+gws::Path pick_path(bool wide, int64_t cols, const gws::Dropout& drop) {
+  if (!wide || cols % gws::GROUP != 0) return gws::ANY;
+  return drop.on ? gws::DROP : gws::FAST;
+}
+
 // The threads of a row and the groups that each holds.
 struct Team {
   int threads, vpt, rows;   // rows: of a block
@@ -82,47 +89,57 @@ struct Team {
 
 // Up to 1024 columns a warp holds a row and a block has several (no barrier).
 // Longer rows take a block. With few rows (less than two for each SM) every
-// thread takes one group, for the shortest row; with many, up to `most`, so
-// that more bytes are in flight for each thread.
-Team pick_team(const gemm_ws* h, int64_t rows, int64_t cols, int most) {
+// thread takes one group, for the shortest row; with many, two (up to 512
+// threads), so that more than one row is in flight on an SM; beyond 8192
+// columns four.
+Team pick_team(const gemm_ws* h, int64_t rows, int64_t cols) {
   const int64_t groups = ceil_div(cols, gws::GROUP);
   Team t;
-  if (groups <= 32 * gws::MAX_VPT) {
+  if (groups <= 128) {
     t.vpt = groups <= 32 ? 1 : groups <= 64 ? 2 : 4;
     t.threads = 32;
     t.rows = rows >= 8 * h->num_sms ? 8 : rows >= 2 * h->num_sms ? 4 : 1;
     return t;
   }
-  t.vpt = rows < 2 * h->num_sms ? 1 : most;
-  while (ceil_div(groups, t.vpt) > 1024) t.vpt *= 2;
+  t.vpt = rows < 2 * h->num_sms && groups <= 1024 ? 1 : groups <= 1024 ? 2 : 4;
   t.threads = static_cast<int>(ceil_div(ceil_div(groups, t.vpt), 32) * 32);
   t.rows = 1;
   return t;
 }
 
+// The kernel instance for a team and a path. Fewer threads a block leave each
+// more registers: 64 with 1024, 128 with 512.
+#define LM_NORM_INSTANCE(KERNEL, T, PATH, ...)                                     \
+  (t.vpt == 1                      ? gws::KERNEL<T, PATH, 1, 1024, ##__VA_ARGS__>  \
+   : t.vpt == 2                    ? gws::KERNEL<T, PATH, 2, 512, ##__VA_ARGS__>   \
+   : t.threads * t.rows <= 512     ? gws::KERNEL<T, PATH, 4, 512, ##__VA_ARGS__>   \
+                                   : gws::KERNEL<T, PATH, 4, 1024, ##__VA_ARGS__>)
+
 template <typename T, int Q>
-int launch_norm(gemm_ws* h, const Team& t, const gws::NormParams& p, cudaStream_t s) {
-  const int64_t blocks = ceil_div(p.rows, t.rows);
-  const int threads = t.threads * t.rows;
-  switch (t.vpt) {
-    case 1: return launch(h, gws::add_rms_norm_kernel<T, 1, Q>, blocks, threads, 0, s, p);
-    case 2: return launch(h, gws::add_rms_norm_kernel<T, 2, Q>, blocks, threads, 0, s, p);
-    default: return launch(h, gws::add_rms_norm_kernel<T, 4, Q>, blocks, threads, 0, s, p);
-  }
+int launch_norm(gemm_ws* h, const Team& t, gws::Path path, const gws::NormParams& p, cudaStream_t s) {
+  auto kernel = LM_NORM_INSTANCE(add_rms_norm_kernel, T, gws::ANY, Q);
+  if (path == gws::FAST) kernel = LM_NORM_INSTANCE(add_rms_norm_kernel, T, gws::FAST, Q);
+  if constexpr (Q == 0)   // 8 bits are for serving: with dropout they take the general path
+    if (path == gws::DROP) kernel = LM_NORM_INSTANCE(add_rms_norm_kernel, T, gws::DROP, Q);
+  return launch(h, kernel, ceil_div(p.rows, t.rows), t.threads * t.rows, 0, s, p);
 }
 
 template <typename T>
-int launch_norm(gemm_ws* h, int output, const Team& t, const gws::NormParams& p, cudaStream_t s) {
-  switch (output) {
-    case GEMM_WS_NORM_SAME: return launch_norm<T, 0>(h, t, p, s);
-    case GEMM_WS_NORM_E4M3_ROW: return launch_norm<T, 1>(h, t, p, s);
-    default: return launch_norm<T, 2>(h, t, p, s);
-  }
-}
-
-template <typename T>
-int launch_grad(gemm_ws* h, const Team& t, const gws::NormGradParams& p, void* dweight,
+int launch_norm(gemm_ws* h, int output, const Team& t, gws::Path path, const gws::NormParams& p,
                 cudaStream_t s) {
+  switch (output) {
+    case GEMM_WS_NORM_SAME: return launch_norm<T, 0>(h, t, path, p, s);
+    case GEMM_WS_NORM_E4M3_ROW: return launch_norm<T, 1>(h, t, path, p, s);
+    default: return launch_norm<T, 2>(h, t, path, p, s);
+  }
+}
+
+template <typename T>
+int launch_grad(gemm_ws* h, const Team& t, gws::Path path, const gws::NormGradParams& p, void* dweight,
+                cudaStream_t s) {
+  const auto kernel = path == gws::ANY    ? LM_NORM_INSTANCE(add_rms_norm_grad_kernel, T, gws::ANY)
+                      : path == gws::FAST ? LM_NORM_INSTANCE(add_rms_norm_grad_kernel, T, gws::FAST)
+                                          : LM_NORM_INSTANCE(add_rms_norm_grad_kernel, T, gws::DROP);
   const int threads = t.threads * t.rows;
   const size_t smem = t.rows > 1 ? static_cast<size_t>(p.cols) * sizeof(float) : 0;
   // As many blocks as run at once (1024 threads of an SM hold their rows in
@@ -132,12 +149,7 @@ int launch_grad(gemm_ws* h, const Team& t, const gws::NormGradParams& p, void* d
   if (blocks > resident) blocks = resident;
   const int64_t room = h->num_sms * kPartialPerSm / p.cols;
   if (p.partial && blocks > room) blocks = room;
-  int rc;
-  switch (t.vpt) {
-    case 1: rc = launch(h, gws::add_rms_norm_grad_kernel<T, 1>, blocks, threads, smem, s, p); break;
-    case 2: rc = launch(h, gws::add_rms_norm_grad_kernel<T, 2>, blocks, threads, smem, s, p); break;
-    default: rc = launch(h, gws::add_rms_norm_grad_kernel<T, 4>, blocks, threads, smem, s, p); break;
-  }
+  const int rc = launch(h, kernel, blocks, threads, smem, s, p);
   if (rc != GEMM_WS_OK || !dweight) return rc;
   gws::DweightParams q;
   q.partial = p.partial;
@@ -146,6 +158,16 @@ int launch_grad(gemm_ws* h, const Team& t, const gws::NormGradParams& p, void* d
   q.dweight = dweight;
   return launch(h, gws::dweight_kernel<T>, ceil_div(p.cols, gws::DW_COLS),
                 gws::DW_COLS * gws::DW_LANES, 0, s, q);
+}
+
+template <typename T>
+int launch_dropout(gemm_ws* h, bool flat, int64_t blocks, const gws::DropoutParams& p,
+                   cudaStream_t s) {
+  return launch(h,
+                !flat       ? gws::dropout_rows_kernel<T>
+                : p.drop.on ? gws::dropout_flat_kernel<T, true>
+                            : gws::dropout_flat_kernel<T, false>,
+                blocks, gws::DROP_THREADS, 0, s, p);
 }
 
 }  // namespace
@@ -159,11 +181,11 @@ int gemm_ws_dropout(gemm_ws_t* h, int dtype, const void* x, int64_t ldx, void* y
     return GEMM_WS_ERR_INVALID_ARG;
   gws::DropoutParams q;
   std::memset(&q, 0, sizeof q);
-  if (!make_dropout(p, rng, &q.drop)) return GEMM_WS_ERR_INVALID_ARG;
+  if (!make_dropout(h, p, rng, &q.drop)) return GEMM_WS_ERR_INVALID_ARG;
   if (rows == 0 || cols == 0) return GEMM_WS_OK;
   const int64_t size = element_size(dtype);
   const Mat mx{x, ldx, size}, my{y, ldy, size};
-  const Mat mr{q.drop.below ? rng : nullptr, 2, 8};
+  const Mat mr{q.drop.on ? rng : nullptr, 2, 8};
   if (!x || !y || bad_matrix(mx, cols) || bad_matrix(my, cols)) return GEMM_WS_ERR_INVALID_ARG;
   if (clash(my, mx, rows, cols, true) ||
       (mr.given() && overlaps(y, my.bytes(rows, cols), rng, 16)))
@@ -172,21 +194,25 @@ int gemm_ws_dropout(gemm_ws_t* h, int dtype, const void* x, int64_t ldx, void* y
   q.y = y;
   q.ldx = ldx;
   q.ldy = ldy;
+  q.rows = rows;
   q.cols = static_cast<int>(cols);
-  q.row_groups = static_cast<int>(ceil_div(cols, gws::GROUP));
-  q.groups = rows * q.row_groups;
+  q.groups = ceil_div(cols, gws::GROUP);
   q.wide = mx.wide() && my.wide();
-  const int64_t blocks = ceil_div(q.groups, gws::DROP_THREADS * gws::DROP_VPT);
+  q.row_threads = 1;
+  while (q.row_threads < gws::DROP_THREADS && q.row_threads < q.groups) q.row_threads *= 2;
+  const bool flat = q.wide && cols % gws::GROUP == 0 && (rows == 1 || (ldx == cols && ldy == cols));
+  int64_t blocks = ceil_div(rows, gws::DROP_THREADS / q.row_threads);
+  if (flat) {
+    q.groups *= rows;
+    blocks = ceil_div(q.groups, gws::DROP_THREADS * gws::DROP_VPT);
+  }
   if (blocks > kMaxDim) return GEMM_WS_ERR_INVALID_ARG;
   DeviceGuard guard(h->device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (dtype) {
-    case GEMM_WS_BF16:
-      return launch(h, gws::dropout_kernel<__nv_bfloat16>, blocks, gws::DROP_THREADS, 0, s, q);
-    case GEMM_WS_F16:
-      return launch(h, gws::dropout_kernel<__half>, blocks, gws::DROP_THREADS, 0, s, q);
-    default:
-      return launch(h, gws::dropout_kernel<float>, blocks, gws::DROP_THREADS, 0, s, q);
+    case GEMM_WS_BF16: return launch_dropout<__nv_bfloat16>(h, flat, blocks, q, s);
+    case GEMM_WS_F16: return launch_dropout<__half>(h, flat, blocks, q, s);
+    default: return launch_dropout<float>(h, flat, blocks, q, s);
   }
 }
 
@@ -201,7 +227,7 @@ int gemm_ws_add_rms_norm(gemm_ws_t* h, int dtype, const void* x, int64_t ldx,
     return GEMM_WS_ERR_INVALID_ARG;
   gws::NormParams q;
   std::memset(&q, 0, sizeof q);
-  if (!make_dropout(p, rng, &q.drop)) return GEMM_WS_ERR_INVALID_ARG;
+  if (!make_dropout(h, p, rng, &q.drop)) return GEMM_WS_ERR_INVALID_ARG;
   if (rows == 0) return GEMM_WS_OK;
   const bool same = output == GEMM_WS_NORM_SAME;
   const int64_t size = element_size(dtype);
@@ -216,7 +242,7 @@ int gemm_ws_add_rms_norm(gemm_ws_t* h, int dtype, const void* x, int64_t ldx,
     return GEMM_WS_ERR_INVALID_ARG;
   // Outputs against the inputs and against each other.
   const Mat vec[4] = {{same ? nullptr : scales, per_row, 4}, {rstd, 1, 4}, {weight, 0, size},
-                      {q.drop.below ? rng : nullptr, 0, 8}};
+                      {q.drop.on ? rng : nullptr, 0, 8}};
   const int64_t vec_bytes[4] = {rows * per_row * 4, rows * 4, cols * size, 16};
   const Mat mats[4] = {in[0], in[1], mh, my};
   if (clash(mh, in[0], rows, cols, true) || clash(mh, in[1], rows, cols, true) ||
@@ -248,14 +274,15 @@ int gemm_ws_add_rms_norm(gemm_ws_t* h, int dtype, const void* x, int64_t ldx,
   q.eps = eps;
   q.wide = in[0].wide() && (!residual || in[1].wide()) &&
            reinterpret_cast<uintptr_t>(weight) % 16 == 0 && (!hidden || mh.wide()) && my.wide();
-  const Team t = pick_team(h, rows, cols, 4);
+  const gws::Path path = pick_path(q.wide, cols, q.drop);
+  const Team t = pick_team(h, rows, cols);
   q.team = t.threads;
   DeviceGuard guard(h->device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (dtype) {
-    case GEMM_WS_BF16: return launch_norm<__nv_bfloat16>(h, output, t, q, s);
-    case GEMM_WS_F16: return launch_norm<__half>(h, output, t, q, s);
-    default: return launch_norm<float>(h, output, t, q, s);
+    case GEMM_WS_BF16: return launch_norm<__nv_bfloat16>(h, output, t, path, q, s);
+    case GEMM_WS_F16: return launch_norm<__half>(h, output, t, path, q, s);
+    default: return launch_norm<float>(h, output, t, path, q, s);
   }
 }
 
@@ -270,7 +297,7 @@ int gemm_ws_add_rms_norm_backward(gemm_ws_t* h, int dtype, const void* dy, int64
     return GEMM_WS_ERR_INVALID_ARG;
   gws::NormGradParams q;
   std::memset(&q, 0, sizeof q);
-  if (!make_dropout(p, rng, &q.drop)) return GEMM_WS_ERR_INVALID_ARG;
+  if (!make_dropout(h, p, rng, &q.drop)) return GEMM_WS_ERR_INVALID_ARG;
   const int64_t size = element_size(dtype);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (reinterpret_cast<uintptr_t>(dweight) % size != 0) return GEMM_WS_ERR_INVALID_ARG;
@@ -289,7 +316,7 @@ int gemm_ws_add_rms_norm_backward(gemm_ws_t* h, int dtype, const void* dy, int64
     if (bad_matrix(m, cols)) return GEMM_WS_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(weight) % size != 0 || reinterpret_cast<uintptr_t>(rstd) % 4 != 0)
     return GEMM_WS_ERR_INVALID_ARG;
-  const Mat vec[3] = {{weight, 0, size}, {rstd, 0, 4}, {q.drop.below ? rng : nullptr, 0, 8}};
+  const Mat vec[3] = {{weight, 0, size}, {rstd, 0, 4}, {q.drop.on ? rng : nullptr, 0, 8}};
   const int64_t vec_bytes[3] = {cols * size, rows * 4, 16};
   for (const Mat& o : out) {
     if (clash(o, in[0], rows, cols, true) || clash(o, in[1], rows, cols, true) ||
@@ -324,13 +351,14 @@ int gemm_ws_add_rms_norm_backward(gemm_ws_t* h, int dtype, const void* dy, int64
   q.cols = static_cast<int>(cols);
   q.wide = in[0].wide() && (!dhidden || in[1].wide()) && in[2].wide() && out[0].wide() &&
            (!dresidual || out[1].wide()) && reinterpret_cast<uintptr_t>(weight) % 16 == 0;
-  const Team t = pick_team(h, rows, cols, 2);
+  const gws::Path path = pick_path(q.wide, cols, q.drop);
+  const Team t = pick_team(h, rows, cols);
   q.team = t.threads;
   DeviceGuard guard(h->device);
   switch (dtype) {
-    case GEMM_WS_BF16: return launch_grad<__nv_bfloat16>(h, t, q, dweight, s);
-    case GEMM_WS_F16: return launch_grad<__half>(h, t, q, dweight, s);
-    default: return launch_grad<float>(h, t, q, dweight, s);
+    case GEMM_WS_BF16: return launch_grad<__nv_bfloat16>(h, t, path, q, dweight, s);
+    case GEMM_WS_F16: return launch_grad<__half>(h, t, path, q, dweight, s);
+    default: return launch_grad<float>(h, t, path, q, dweight, s);
   }
 }
 

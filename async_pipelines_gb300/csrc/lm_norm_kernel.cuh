@@ -38,108 +38,197 @@ constexpr float E4M3_MAX = 448.0f;       // largest finite e4m3
 // bits each, lowest first: half the rounds' cost of 32 bits a column (which
 // would take more issue slots than dropout's 4 bytes of traffic a column
 // leave), for a p that is a multiple of 2^-16.
-__device__ __forceinline__ uint4 philox(uint64_t counter, uint64_t seed) {
-  uint32_t c0 = static_cast<uint32_t>(counter), c1 = static_cast<uint32_t>(counter >> 32);
-  uint32_t c2 = 0, c3 = 0;
+//
+// N counters at a time: they share the rounds' keys, and the rounds of one fill
+// the latency of the others'.
+template <int N>
+__device__ __forceinline__ void philox(const uint64_t (&counter)[N], uint64_t seed,
+                                       uint32_t (&words)[N][4]) {
   uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
 #pragma unroll
+  for (int n = 0; n < N; ++n) {
+    words[n][0] = static_cast<uint32_t>(counter[n]);
+    words[n][1] = static_cast<uint32_t>(counter[n] >> 32);
+    words[n][2] = words[n][3] = 0;
+  }
+#pragma unroll
   for (int i = 0; i < 10; ++i) {
-    const uint64_t m0 = static_cast<uint64_t>(c0) * 0xD2511F53u;
-    const uint64_t m1 = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
-    c0 = static_cast<uint32_t>(m1 >> 32) ^ c1 ^ k0;
-    c1 = static_cast<uint32_t>(m1);
-    c2 = static_cast<uint32_t>(m0 >> 32) ^ c3 ^ k1;
-    c3 = static_cast<uint32_t>(m0);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      uint32_t(&c)[4] = words[n];
+      const uint64_t m0 = static_cast<uint64_t>(c[0]) * 0xD2511F53u;
+      const uint64_t m1 = static_cast<uint64_t>(c[2]) * 0xCD9E8D57u;
+      c[0] = static_cast<uint32_t>(m1 >> 32) ^ c[1] ^ k0;
+      c[1] = static_cast<uint32_t>(m1);
+      c[2] = static_cast<uint32_t>(m0 >> 32) ^ c[3] ^ k1;
+      c[3] = static_cast<uint32_t>(m0);
+    }
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
   }
-  return make_uint4(c0, c1, c2, c3);
 }
 
-// What a launch's dropout is: a column is dropped where its word is below
-// `below` (0: no dropout; 65536: everything is dropped), else scaled.
+// What a launch's dropout is: a column is kept, and scaled, where its word,
+// shifted to the top of 32 bits, is above `limit`.
 struct Dropout {
-  const uint64_t* rng;   // device: seed, first counter
-  uint32_t below;
-  float scale;           // 65536 / (65536 - below)
+  const uint64_t* rng;   // device: seed, first counter (readable, if unused, without dropout)
+  int on;
+  uint32_t limit;        // (round(65536 p) << 16) - 1
+  float scale;           // 65536 / (65536 - round(65536 p)); 0 where all is dropped
 };
 
-// v = d(v) for the group at `counter`. A dropped value is 0 whatever it was.
-__device__ __forceinline__ void drop_group(const Dropout& d, uint64_t seed, uint64_t counter,
-                                           float (&v)[GROUP]) {
-  const uint4 w = philox(counter, seed);
-  const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+// v = d(v) for N groups at their counters. A dropped value is 0 whatever it was.
+// Words are compared in the upper half of a register: the high one as it
+// stands (what is below it cannot change the verdict), the low one shifted up.
+template <int N>
+__device__ __forceinline__ void drop_groups(const Dropout& d, uint64_t seed,
+                                            const uint64_t (&counter)[N], float (&v)[N][GROUP]) {
+  uint32_t words[N][4];
+  philox(counter, seed, words);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = (words[i] & 0xFFFFu) >= d.below ? v[2 * i] * d.scale : 0.0f;
-    v[2 * i + 1] = (words[i] >> 16) >= d.below ? v[2 * i + 1] * d.scale : 0.0f;
-  }
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[n][2 * i] = (words[n][i] << 16) > d.limit ? v[n][2 * i] * d.scale : 0.0f;
+      v[n][2 * i + 1] = words[n][i] > d.limit ? v[n][2 * i + 1] * d.scale : 0.0f;
+    }
 }
 
 // ------------------------------------------------------------ groups
 
-__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_float(float v) { return v; }
-template <typename T>
-__device__ __forceinline__ T from_float(float v);
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float(float v) { return __float2bfloat16_rn(v); }
-template <>
-__device__ __forceinline__ __half from_float(float v) { return __float2half_rn(v); }
-template <>
-__device__ __forceinline__ float from_float(float v) { return v; }
-
-// A group as it lies in memory.
+// A group as it lies in memory, and its values in 32 bits.
 template <typename T>
 struct alignas(16) Raw {
   uint4 w[sizeof(T) * GROUP / 16];
 };
 
-template <typename T>
-__device__ __forceinline__ void unpack(const Raw<T>& raw, float (&v)[GROUP]) {
-  const T* e = reinterpret_cast<const T*>(&raw);
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16>& raw, float (&v)[GROUP]) {
+  const uint32_t w[4] = {raw.w[0].x, raw.w[0].y, raw.w[0].z, raw.w[0].w};
 #pragma unroll
-  for (int i = 0; i < GROUP; ++i) v[i] = to_float(e[i]);
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void unpack(const Raw<__half>& raw, float (&v)[GROUP]) {
+  const uint32_t w[4] = {raw.w[0].x, raw.w[0].y, raw.w[0].z, raw.w[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void unpack(const Raw<float>& raw, float (&v)[GROUP]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v[4 * i] = __uint_as_float(raw.w[i].x);
+    v[4 * i + 1] = __uint_as_float(raw.w[i].y);
+    v[4 * i + 2] = __uint_as_float(raw.w[i].z);
+    v[4 * i + 3] = __uint_as_float(raw.w[i].w);
+  }
 }
 
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, __nv_bfloat16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, __half) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// The group's values rounded to T.
 template <typename T>
 __device__ __forceinline__ Raw<T> pack(const float (&v)[GROUP]) {
   Raw<T> raw;
-  T* e = reinterpret_cast<T*>(&raw);
-#pragma unroll
-  for (int i = 0; i < GROUP; ++i) e[i] = from_float<T>(v[i]);
-  return raw;
-}
-
-// Columns [c, c + 8) of a row whose end is `cols`; past it zeros. `wide`: the
-// row starts on a 16-byte boundary, so whole groups move in 16-byte pieces.
-template <typename T>
-__device__ __forceinline__ Raw<T> load_group(const T* row, int c, int cols, bool wide) {
-  Raw<T> raw;
-  if (wide && c + GROUP <= cols) {
-    const uint4* src = reinterpret_cast<const uint4*>(row + c);
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) * GROUP / 16); ++i) raw.w[i] = src[i];
+  if constexpr (sizeof(T) == 2) {
+    raw.w[0] = make_uint4(pack2(v[0], v[1], T()), pack2(v[2], v[3], T()), pack2(v[4], v[5], T()),
+                          pack2(v[6], v[7], T()));
   } else {
-    T* e = reinterpret_cast<T*>(&raw);
 #pragma unroll
-    for (int i = 0; i < GROUP; ++i) e[i] = c + i < cols ? row[c + i] : from_float<T>(0.0f);
+    for (int i = 0; i < 2; ++i)
+      raw.w[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                            __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
   }
   return raw;
 }
 
+__device__ __forceinline__ float round_to(float v, float) { return v; }
+__device__ __forceinline__ __nv_bfloat16 round_to(float v, __nv_bfloat16) { return __float2bfloat16_rn(v); }
+__device__ __forceinline__ __half round_to(float v, __half) { return __float2half_rn(v); }
+
+// Element i of a group in registers: its bits, and a group made of them. (By
+// shifts, so that the group stays in registers.)
 template <typename T>
-__device__ __forceinline__ void store_group(T* row, int c, int cols, bool wide, const Raw<T>& raw) {
-  if (wide && c + GROUP <= cols) {
-    uint4* dst = reinterpret_cast<uint4*>(row + c);
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) * GROUP / 16); ++i) dst[i] = raw.w[i];
+__device__ __forceinline__ uint32_t bits_of(const Raw<T>& raw, int i) {
+  const uint32_t w[8] = {raw.w[0].x, raw.w[0].y, raw.w[0].z, raw.w[0].w,
+                         raw.w[sizeof(T) / 4].x, raw.w[sizeof(T) / 4].y,
+                         raw.w[sizeof(T) / 4].z, raw.w[sizeof(T) / 4].w};
+  return sizeof(T) == 4 ? w[i] : (w[i / 2] >> (16 * (i % 2))) & 0xFFFFu;
+}
+template <typename T>
+__device__ __forceinline__ Raw<T> from_bits(const uint32_t (&e)[GROUP]) {
+  Raw<T> raw;
+  if constexpr (sizeof(T) == 2) {
+    raw.w[0] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
   } else {
-    const T* e = reinterpret_cast<const T*>(&raw);
+    raw.w[0] = make_uint4(e[0], e[1], e[2], e[3]);
+    raw.w[1] = make_uint4(e[4], e[5], e[6], e[7]);
+  }
+  return raw;
+}
+
+template <int SIZE>
+struct Bits;
+template <>
+struct Bits<2> { using type = uint16_t; };
+template <>
+struct Bits<4> { using type = uint32_t; };
+
+// How a kernel's rows lie, and whether values are dropped. FAST: every row of
+// every matrix starts on a 16-byte boundary and ends with a whole group. DROP
+// is FAST with dropout: the generator's rounds only overlap the loads around
+// them where no branch stands before them (8192 x 8192 bf16, dropout alone: 55
+// us behind a branch, 42 without; the copy alone takes 40). ANY is the rest, with
+// dropout behind a branch.
+enum Path { ANY = 0, FAST = 1, DROP = 2 };
+
+// Columns [c, c + 8) of a row whose end is `cols`; past it zeros. WHOLE: not
+// ANY, so a group moves in 16-byte pieces and nothing is tested. Else `wide` says
+// whether rows start on such a boundary.
+template <bool WHOLE, typename T>
+__device__ __forceinline__ Raw<T> load_group(const T* row, int c, int cols, bool wide) {
+  const auto* src = reinterpret_cast<const typename Bits<sizeof(T)>::type*>(row) + c;
+  if (WHOLE || (wide && c + GROUP <= cols)) {
+    Raw<T> raw;
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) * GROUP / 16); ++i)
+      raw.w[i] = reinterpret_cast<const uint4*>(src)[i];
+    return raw;
+  }
+  if (c + GROUP <= cols) {
+    const uint32_t e[GROUP] = {src[0], src[1], src[2], src[3], src[4], src[5], src[6], src[7]};
+    return from_bits<T>(e);
+  }
+  uint32_t e[GROUP];
+#pragma unroll
+  for (int i = 0; i < GROUP; ++i) e[i] = c + i < cols ? src[i] : 0u;
+  return from_bits<T>(e);
+}
+
+template <bool WHOLE, typename T>
+__device__ __forceinline__ void store_group(T* row, int c, int cols, bool wide, const Raw<T>& raw) {
+  auto* dst = reinterpret_cast<typename Bits<sizeof(T)>::type*>(row) + c;
+  if (WHOLE || (wide && c + GROUP <= cols)) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) * GROUP / 16); ++i)
+      reinterpret_cast<uint4*>(dst)[i] = raw.w[i];
+    return;
+  }
+  if constexpr (!WHOLE) {
 #pragma unroll
     for (int i = 0; i < GROUP; ++i)
-      if (c + i < cols) row[c + i] = e[i];
+      if (c + i < cols) dst[i] = static_cast<typename Bits<sizeof(T)>::type>(bits_of(raw, i));
   }
 }
 
@@ -189,49 +278,53 @@ struct NormParams {
   int cols;
   int team;                            // threads a row: 32 (blockDim / 32 rows a block), or all
   float eps;
-  int wide;                            // rows of x, residual, h, y and weight allow wide accesses
+  int wide;                            // ANY: rows of x, residual, h, y and weight start on
+                                       // 16-byte boundaries
   Dropout drop;
 };
 
 // One row a team. Q: 0 y has the type of x; 1 e4m3 with one scale a row; 2
 // e4m3 with a scale for each 128 columns.
-template <typename T, int VPT, int Q>
-__global__ void __launch_bounds__(1024) add_rms_norm_kernel(const __grid_constant__ NormParams p) {
+template <typename T, Path PATH, int VPT, int MOST, int Q>
+__global__ void __launch_bounds__(MOST) add_rms_norm_kernel(const __grid_constant__ NormParams p) {
   __shared__ SumMax box[32];
   grid_dependency_wait();
   grid_launch_dependents();
   const int team = p.team, t = threadIdx.x % team;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / team) + threadIdx.x / team;
   if (row >= p.rows) return;   // only whole warps, and only where a team is a warp
-  const bool wide = p.wide;
   const T* x = static_cast<const T*>(p.x) + row * p.ldx;
   const T* res = p.residual ? static_cast<const T*>(p.residual) + row * p.ldr : nullptr;
   const T* weight = static_cast<const T*>(p.weight);
   const int cols = p.cols, groups = (cols + GROUP - 1) / GROUP;
+  const bool wide = p.wide;
 
-  Raw<T> xr[VPT], rr[VPT], wr[VPT];
+  Raw<T> xr[VPT] = {}, rr[VPT], wr[VPT];
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
     const int g = k * team + t;
     if (g < groups) {
-      xr[k] = load_group(x, g * GROUP, cols, wide);
-      if (res) rr[k] = load_group(res, g * GROUP, cols, wide);
-      wr[k] = load_group(weight, g * GROUP, cols, wide);
+      xr[k] = load_group<PATH != ANY>(x, g * GROUP, cols, wide);
+      if (res) rr[k] = load_group<PATH != ANY>(res, g * GROUP, cols, wide);
+      wr[k] = load_group<PATH != ANY>(weight, g * GROUP, cols, wide);
     }
   }
-  uint64_t seed = 0, first = 0;
-  if (p.drop.below) {
-    seed = p.drop.rng[0];
-    first = p.drop.rng[1] + static_cast<uint64_t>(row) * groups;
-  }
+  const uint64_t seed = p.drop.rng[0];
+  const uint64_t first = p.drop.rng[1] + static_cast<uint64_t>(row) * groups;
   float v[VPT][GROUP];
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) unpack(xr[k], v[k]);
+  if (PATH == DROP || (PATH == ANY && p.drop.on)) {
+    uint64_t counter[VPT];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) counter[k] = first + k * team + t;
+    drop_groups(p.drop, seed, counter, v);
+  }
   SumMax s = {0.0f, 0.0f};
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
     const int g = k * team + t;
     if (g < groups) {
-      unpack(xr[k], v[k]);
-      if (p.drop.below) drop_group(p.drop, seed, first + g, v[k]);
       float w[GROUP];
       unpack(wr[k], w);
       if (res) {
@@ -245,7 +338,7 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const __grid_constan
         s.sum = fmaf(v[k][i], v[k][i], s.sum);
         if (Q == 1) s.max = max_nan(s.max, fabsf(v[k][i] * w[i]));
       }
-      if (p.h) store_group(static_cast<T*>(p.h) + row * p.ldh, g * GROUP, cols, wide, pack<T>(v[k]));
+      if (p.h) store_group<PATH != ANY>(static_cast<T*>(p.h) + row * p.ldh, g * GROUP, cols, wide, pack<T>(v[k]));
     }
   }
   s = reduce_team<Q == 1>(s, team / 32, box);
@@ -269,7 +362,7 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const __grid_constan
     }
     if (Q == 0) {
       if (g < groups)
-        store_group(static_cast<T*>(p.y) + row * p.ldy, g * GROUP, cols, wide, pack<T>(v[k]));
+        store_group<PATH != ANY>(static_cast<T*>(p.y) + row * p.ldy, g * GROUP, cols, wide, pack<T>(v[k]));
     } else {
       if (Q == 2) {
         // the 16 groups of 128 columns sit on 16 neighbouring lanes
@@ -296,7 +389,7 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const __grid_constan
           out[i] = lo | (hi << 16);
         }
         uint8_t* y = static_cast<uint8_t*>(p.y) + row * p.ldy + g * GROUP;
-        if (wide && (g + 1) * GROUP <= cols) {
+        if (PATH != ANY || (wide && (g + 1) * GROUP <= cols)) {
           *reinterpret_cast<uint2*>(y) = make_uint2(out[0], out[1]);
         } else {
 #pragma unroll
@@ -319,7 +412,7 @@ struct NormGradParams {
   int64_t rows;
   int cols;
   int team;
-  int wide;
+  int wide;                            // as above
   Dropout drop;
 };
 
@@ -327,21 +420,17 @@ struct NormGradParams {
 // grid, and keeps its columns' share of dweight in registers; a block leaves
 // one partial row, and dweight_kernel adds those in block order. So dweight
 // has the same bits on every run, whatever the timing.
-template <typename T, int VPT>
-__global__ void __launch_bounds__(1024) add_rms_norm_grad_kernel(const __grid_constant__ NormGradParams p) {
+template <typename T, Path PATH, int VPT, int MOST>
+__global__ void __launch_bounds__(MOST, 1024 / MOST) add_rms_norm_grad_kernel(const __grid_constant__ NormGradParams p) {
   __shared__ SumMax box[2][32];
   extern __shared__ float share[];   // where a team is a warp: the block's sum of dweight
   grid_dependency_wait();
   grid_launch_dependents();
   const int team = p.team, t = threadIdx.x % team, teams = blockDim.x / team;
-  const bool wide = p.wide;
   const int cols = p.cols, groups = (cols + GROUP - 1) / GROUP;
+  const bool wide = p.wide;
   const T* weight = static_cast<const T*>(p.weight);
-  uint64_t seed = 0, first = 0;
-  if (p.drop.below) {
-    seed = p.drop.rng[0];
-    first = p.drop.rng[1];
-  }
+  const uint64_t seed = p.drop.rng[0], first = p.drop.rng[1];
   float acc[VPT][GROUP];
 #pragma unroll
   for (int k = 0; k < VPT; ++k)
@@ -354,14 +443,14 @@ __global__ void __launch_bounds__(1024) add_rms_norm_grad_kernel(const __grid_co
     const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
     const T* h = static_cast<const T*>(p.h) + row * p.ldh;
     const T* dh = p.dh ? static_cast<const T*>(p.dh) + row * p.lddh : nullptr;
-    Raw<T> yr[VPT], hr[VPT], dr[VPT];
+    Raw<T> yr[VPT], hr[VPT], dr[VPT] = {};
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int g = k * team + t;
       if (g < groups) {
-        yr[k] = load_group(dy, g * GROUP, cols, wide);
-        hr[k] = load_group(h, g * GROUP, cols, wide);
-        if (dh) dr[k] = load_group(dh, g * GROUP, cols, wide);
+        yr[k] = load_group<PATH != ANY>(dy, g * GROUP, cols, wide);
+        hr[k] = load_group<PATH != ANY>(h, g * GROUP, cols, wide);
+        if (dh) dr[k] = load_group<PATH != ANY>(dh, g * GROUP, cols, wide);
       }
     }
     const float r = p.rstd[row];
@@ -373,7 +462,7 @@ __global__ void __launch_bounds__(1024) add_rms_norm_grad_kernel(const __grid_co
         float a[GROUP], n[GROUP], w[GROUP];
         unpack(yr[k], a);
         unpack(hr[k], n);
-        unpack(load_group(weight, g * GROUP, cols, wide), w);
+        unpack(load_group<PATH != ANY>(weight, g * GROUP, cols, wide), w);
 #pragma unroll
         for (int i = 0; i < GROUP; ++i) {
           const float ni = n[i] * r;
@@ -383,28 +472,35 @@ __global__ void __launch_bounds__(1024) add_rms_norm_grad_kernel(const __grid_co
       }
     }
     const float c = reduce_team<false>(s, team / 32, box[turn]).sum / static_cast<float>(cols);
+    const float rc = r * c;
+    float d[VPT][GROUP];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int g = k * team + t;
       if (g < groups) {
-        float a[GROUP], n[GROUP], w[GROUP], d[GROUP];
+        float a[GROUP], n[GROUP], w[GROUP];
         unpack(yr[k], a);
         unpack(hr[k], n);
-        unpack(load_group(weight, g * GROUP, cols, wide), w);
-        if (dh) {
-          unpack(dr[k], d);
-        } else {
+        unpack(load_group<PATH != ANY>(weight, g * GROUP, cols, wide), w);
+        unpack(dr[k], d[k]);
 #pragma unroll
-          for (int i = 0; i < GROUP; ++i) d[i] = 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < GROUP; ++i) d[i] = fmaf(r, a[i] * w[i] - n[i] * r * c, d[i]);
+        for (int i = 0; i < GROUP; ++i) d[k][i] = fmaf(r, a[i] * w[i] - n[i] * rc, d[k][i]);
         if (p.dres)
-          store_group(static_cast<T*>(p.dres) + row * p.lddres, g * GROUP, cols, wide, pack<T>(d));
-        if (p.drop.below)
-          drop_group(p.drop, seed, first + static_cast<uint64_t>(row) * groups + g, d);
-        store_group(static_cast<T*>(p.dx) + row * p.lddx, g * GROUP, cols, wide, pack<T>(d));
+          store_group<PATH != ANY>(static_cast<T*>(p.dres) + row * p.lddres, g * GROUP, cols, wide, pack<T>(d[k]));
       }
+    }
+    if (PATH == DROP || (PATH == ANY && p.drop.on)) {
+      uint64_t counter[VPT];
+#pragma unroll
+      for (int k = 0; k < VPT; ++k)
+        counter[k] = first + static_cast<uint64_t>(row) * groups + k * team + t;
+      drop_groups(p.drop, seed, counter, d);
+    }
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int g = k * team + t;
+      if (g < groups)
+        store_group<PATH != ANY>(static_cast<T*>(p.dx) + row * p.lddx, g * GROUP, cols, wide, pack<T>(d[k]));
     }
   }
   if (!p.partial) return;
@@ -463,7 +559,7 @@ __global__ void __launch_bounds__(DW_COLS* DW_LANES)
   __syncthreads();
   if (lane == 0 && c < p.cols) {
     for (int l = 1; l < DW_LANES; ++l) s += box[l][x];
-    static_cast<T*>(p.dweight)[c] = from_float<T>(s);
+    static_cast<T*>(p.dweight)[c] = round_to(s, T());
   }
 }
 
@@ -473,42 +569,61 @@ struct DropoutParams {
   const void* x;
   void* y;
   int64_t ldx, ldy;
-  int64_t groups;      // of all rows
-  int row_groups;      // of one row
+  int64_t rows;
   int cols;
-  int wide;
+  int64_t groups;      // FLAT: of the whole matrix; else of a row
+  int row_threads;     // not FLAT: threads of a row, a power of two
+  int wide;            // not FLAT: rows start on 16-byte boundaries
   Dropout drop;
 };
 
-constexpr int DROP_THREADS = 256, DROP_VPT = 4;
+constexpr int DROP_THREADS = 256, DROP_VPT = 2;
 
-template <typename T>
-__global__ void __launch_bounds__(DROP_THREADS) dropout_kernel(const __grid_constant__ DropoutParams p) {
+// FLAT: rows follow one another without gaps in whole groups, so the matrix is
+// one run of groups and no row has to be found. ON: p > 0.
+template <typename T, bool ON>
+__global__ void __launch_bounds__(DROP_THREADS) dropout_flat_kernel(const __grid_constant__ DropoutParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
-  const uint64_t seed = p.drop.below ? p.drop.rng[0] : 0, first = p.drop.below ? p.drop.rng[1] : 0;
+  const uint64_t seed = p.drop.rng[0], first = p.drop.rng[1];
   const int64_t base = static_cast<int64_t>(blockIdx.x) * (DROP_THREADS * DROP_VPT) + threadIdx.x;
-  Raw<T> raw[DROP_VPT];
-  int64_t row[DROP_VPT];
-  int col[DROP_VPT];
+  Raw<T> raw[DROP_VPT] = {};
+  float v[DROP_VPT][GROUP];
+  uint64_t counter[DROP_VPT];
 #pragma unroll
   for (int k = 0; k < DROP_VPT; ++k) {
     const int64_t g = base + k * DROP_THREADS;
-    if (g < p.groups) {
-      row[k] = g / p.row_groups;
-      col[k] = static_cast<int>(g - row[k] * p.row_groups) * GROUP;
-      raw[k] = load_group(static_cast<const T*>(p.x) + row[k] * p.ldx, col[k], p.cols, p.wide);
-    }
+    if (g < p.groups) raw[k] = static_cast<const Raw<T>*>(p.x)[g];
+    counter[k] = first + g;
   }
 #pragma unroll
+  for (int k = 0; k < DROP_VPT; ++k) unpack(raw[k], v[k]);
+  if (ON) drop_groups(p.drop, seed, counter, v);
+#pragma unroll
   for (int k = 0; k < DROP_VPT; ++k) {
     const int64_t g = base + k * DROP_THREADS;
-    if (g < p.groups) {
-      float v[GROUP];
-      unpack(raw[k], v);
-      if (p.drop.below) drop_group(p.drop, seed, first + g, v);
-      store_group(static_cast<T*>(p.y) + row[k] * p.ldy, col[k], p.cols, p.wide, pack<T>(v));
-    }
+    if (g < p.groups) static_cast<Raw<T>*>(p.y)[g] = pack<T>(v[k]);
+  }
+}
+
+// Any rows: row_threads threads walk one, DROP_THREADS / row_threads rows a block.
+template <typename T>
+__global__ void __launch_bounds__(DROP_THREADS) dropout_rows_kernel(const __grid_constant__ DropoutParams p) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const uint64_t seed = p.drop.rng[0], first = p.drop.rng[1];
+  const int per_block = DROP_THREADS / p.row_threads;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / p.row_threads;
+  if (row >= p.rows) return;
+  const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+  T* y = static_cast<T*>(p.y) + row * p.ldy;
+  const int groups = static_cast<int>(p.groups);
+  for (int g = threadIdx.x % p.row_threads; g < groups; g += p.row_threads) {
+    float v[1][GROUP];
+    unpack(load_group<false>(x, g * GROUP, p.cols, p.wide), v[0]);
+    const uint64_t counter[1] = {first + static_cast<uint64_t>(row) * groups + g};
+    if (p.drop.on) drop_groups(p.drop, seed, counter, v);
+    store_group<false>(y, g * GROUP, p.cols, p.wide, pack<T>(v[0]));
   }
 }
 
