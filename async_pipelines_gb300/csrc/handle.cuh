@@ -51,6 +51,8 @@ struct gemm_ws {
 // Sets the shared-memory attributes of the cross entropy's product kernels on
 // the current device; *pair_clusters: how many of its 2-CTA clusters fit at once.
 cudaError_t ce_configure(int num_sms, int* pair_clusters);
+// The same of the norm's gradient.
+cudaError_t norm_configure();
 
 namespace {
 

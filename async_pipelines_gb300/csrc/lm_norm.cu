@@ -135,6 +135,52 @@ int launch_norm(gemm_ws* h, int output, const Team& t, gws::Path path, const gws
 }
 
 template <typename T>
+int launch_dweight(gemm_ws* h, const float* partial, int64_t blocks, int cols, void* dweight,
+                   cudaStream_t s) {
+  gws::DweightParams q;
+  q.partial = partial;
+  q.blocks = static_cast<int>(blocks);
+  q.cols = cols;
+  q.dweight = dweight;
+  return launch(h, gws::dweight_kernel<T>, ceil_div(cols, gws::DW_COLS),
+                gws::DW_COLS * gws::DW_LANES, 0, s, q);
+}
+
+// The ring needs some rows of each SM to be worth its set-up.
+constexpr int64_t kRingRows = 4;
+
+// How the rows pass through the ring: the smallest teams that hold a row, four
+// groups a thread, as long as the ring holds a row for each team and one more;
+// else larger ones. False where two rows do not fit, or a row a team.
+bool plan_ring(int64_t cols, int64_t size, int inputs, gws::NormGradRing* q, int* vpt) {
+  const int64_t groups = cols / gws::GROUP, row = cols * size;
+  const int64_t room = gws::RING_BYTES / (inputs * row);
+  q->stages = static_cast<int>(room < gws::RING_MAX_STAGES ? room : gws::RING_MAX_STAGES);
+  q->row_bytes = static_cast<uint32_t>(row);
+  for (*vpt = 4; *vpt >= 1; *vpt /= 2) {
+    const int64_t warps = ceil_div(groups, 32 * *vpt);
+    if (warps > gws::RING_WARPS) return false;
+    q->teams = static_cast<int>(gws::RING_WARPS / warps);
+    q->p.team = static_cast<int>(32 * warps);
+    if (q->stages > q->teams) return true;
+  }
+  return false;
+}
+
+template <typename T>
+int launch_grad_ring(gemm_ws* h, int vpt, const gws::NormGradRing& q, void* dweight, cudaStream_t s) {
+  const bool on = q.p.drop.on;
+  const auto kernel =
+      vpt == 4   ? (on ? gws::add_rms_norm_grad_ring_kernel<T, true, 4> : gws::add_rms_norm_grad_ring_kernel<T, false, 4>)
+      : vpt == 2 ? (on ? gws::add_rms_norm_grad_ring_kernel<T, true, 2> : gws::add_rms_norm_grad_ring_kernel<T, false, 2>)
+                 : (on ? gws::add_rms_norm_grad_ring_kernel<T, true, 1> : gws::add_rms_norm_grad_ring_kernel<T, false, 1>);
+  const int64_t blocks = h->num_sms;
+  const int rc = launch(h, kernel, blocks, gws::RING_THREADS, gws::RING_BYTES, s, q);
+  if (rc != GEMM_WS_OK || !dweight) return rc;
+  return launch_dweight<T>(h, q.p.partial, blocks, q.p.cols, dweight, s);
+}
+
+template <typename T>
 int launch_grad(gemm_ws* h, const Team& t, gws::Path path, const gws::NormGradParams& p, void* dweight,
                 cudaStream_t s) {
   const auto kernel = path == gws::ANY    ? LM_NORM_INSTANCE(add_rms_norm_grad_kernel, T, gws::ANY)
@@ -151,13 +197,7 @@ int launch_grad(gemm_ws* h, const Team& t, gws::Path path, const gws::NormGradPa
   if (p.partial && blocks > room) blocks = room;
   const int rc = launch(h, kernel, blocks, threads, smem, s, p);
   if (rc != GEMM_WS_OK || !dweight) return rc;
-  gws::DweightParams q;
-  q.partial = p.partial;
-  q.blocks = static_cast<int>(blocks);
-  q.cols = p.cols;
-  q.dweight = dweight;
-  return launch(h, gws::dweight_kernel<T>, ceil_div(p.cols, gws::DW_COLS),
-                gws::DW_COLS * gws::DW_LANES, 0, s, q);
+  return launch_dweight<T>(h, p.partial, blocks, p.cols, dweight, s);
 }
 
 template <typename T>
@@ -170,7 +210,32 @@ int launch_dropout(gemm_ws* h, bool flat, int64_t blocks, const gws::DropoutPara
                 blocks, gws::DROP_THREADS, 0, s, p);
 }
 
+// Sets the shared-memory attribute of the ring kernels on the current device.
+template <typename T>
+cudaError_t configure_ring() {
+  const void* kernels[6] = {
+      reinterpret_cast<const void*>(gws::add_rms_norm_grad_ring_kernel<T, false, 1>),
+      reinterpret_cast<const void*>(gws::add_rms_norm_grad_ring_kernel<T, false, 2>),
+      reinterpret_cast<const void*>(gws::add_rms_norm_grad_ring_kernel<T, false, 4>),
+      reinterpret_cast<const void*>(gws::add_rms_norm_grad_ring_kernel<T, true, 1>),
+      reinterpret_cast<const void*>(gws::add_rms_norm_grad_ring_kernel<T, true, 2>),
+      reinterpret_cast<const void*>(gws::add_rms_norm_grad_ring_kernel<T, true, 4>)};
+  for (const void* k : kernels) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(gws::RING_BYTES));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
 }  // namespace
+
+cudaError_t norm_configure() {
+  cudaError_t e = configure_ring<__nv_bfloat16>();
+  if (e == cudaSuccess) e = configure_ring<__half>();
+  if (e == cudaSuccess) e = configure_ring<float>();
+  return e;
+}
 
 extern "C" {
 
@@ -352,9 +417,23 @@ int gemm_ws_add_rms_norm_backward(gemm_ws_t* h, int dtype, const void* dy, int64
   q.wide = in[0].wide() && (!dhidden || in[1].wide()) && in[2].wide() && out[0].wide() &&
            (!dresidual || out[1].wide()) && reinterpret_cast<uintptr_t>(weight) % 16 == 0;
   const gws::Path path = pick_path(q.wide, cols, q.drop);
+  DeviceGuard guard(h->device);
+  gws::NormGradRing ring;
+  int vpt = 0;
+  if (path != gws::ANY && rows >= kRingRows * h->num_sms) {
+    ring.p = q;
+    ring.status = h->work + 1;
+    ring.timeout_ns = h->timeout_ns;
+    if (plan_ring(cols, size, dhidden ? 3 : 2, &ring, &vpt)) {
+      switch (dtype) {
+        case GEMM_WS_BF16: return launch_grad_ring<__nv_bfloat16>(h, vpt, ring, dweight, s);
+        case GEMM_WS_F16: return launch_grad_ring<__half>(h, vpt, ring, dweight, s);
+        default: return launch_grad_ring<float>(h, vpt, ring, dweight, s);
+      }
+    }
+  }
   const Team t = pick_team(h, rows, cols);
   q.team = t.threads;
-  DeviceGuard guard(h->device);
   switch (dtype) {
     case GEMM_WS_BF16: return launch_grad<__nv_bfloat16>(h, t, path, q, dweight, s);
     case GEMM_WS_F16: return launch_grad<__half>(h, t, path, q, dweight, s);

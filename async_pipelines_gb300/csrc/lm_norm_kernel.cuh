@@ -22,6 +22,7 @@
 #include <stdint.h>
 
 #include "ptx.cuh"
+#include "watchdog.cuh"
 
 namespace gws {
 
@@ -529,6 +530,193 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) add_rms_norm_grad_kernel(co
     }
   }
   __syncthreads();
+  for (int c = threadIdx.x; c < cols; c += blockDim.x) out[c] = share[c];
+}
+
+// The same for many rows that lie FAST: the rows come through a ring in shared
+// memory, filled by one warp's bulk copies, so that the next rows are on their
+// way while a team waits for its row's sum. (Loaded straight into registers the
+// rows of an SM stop at each such wait: 8192 x 8192 bf16 took 124 us, with
+// dropout 171.) RING_WARPS warps form teams of `team` threads; the CTA's k-th row goes
+// to team k % teams through stage k % stages.
+constexpr int RING_WARPS = 16;
+constexpr int RING_THREADS = (RING_WARPS + 1) * 32;
+constexpr int RING_MAX_STAGES = 16;
+constexpr uint32_t RING_BYTES = 208 * 1024;
+
+struct NormGradRing {
+  NormGradParams p;
+  int stages, teams;
+  uint32_t row_bytes;   // of one matrix
+  uint32_t* status;
+  unsigned long long timeout_ns;
+};
+
+// Barrier `id` of `threads` threads; whether `ok` holds for all of them.
+__device__ __forceinline__ bool team_sync(int id, int threads, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "barrier.cta.red.and.pred p, %2, %3, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(all)
+      : "r"(static_cast<uint32_t>(ok)), "r"(id), "r"(threads)
+      : "memory");
+  return all != 0;
+}
+
+template <typename T, bool ON, int VPT>
+__global__ void __launch_bounds__(RING_THREADS, 1)
+    add_rms_norm_grad_ring_kernel(const __grid_constant__ NormGradRing q) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ __align__(8) uint64_t bars[2 * RING_MAX_STAGES];
+  __shared__ float box[2][RING_WARPS];
+  __shared__ uint32_t aborted;
+  const NormGradParams& p = q.p;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int cols = p.cols, groups = cols / GROUP, team = p.team, warps = team / 32;
+  const int inputs = p.dh ? 3 : 2;
+  const uint32_t stage_bytes = inputs * q.row_bytes;
+  auto full = [&](int s) { return smem_addr(&bars[s]); };
+  auto empty = [&](int s) { return smem_addr(&bars[RING_MAX_STAGES + s]); };
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < q.stages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), warps);
+    }
+    aborted = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const Watchdog wd{&aborted, q.status, q.timeout_ns};
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t step = gridDim.x;
+  const int64_t mine = (p.rows - blockIdx.x + step - 1) / step;   // this CTA's rows
+
+  float acc[VPT][GROUP];
+#pragma unroll
+  for (int k = 0; k < VPT; ++k)
+#pragma unroll
+    for (int i = 0; i < GROUP; ++i) acc[k][i] = 0.0f;
+  const int t = threadIdx.x % team, which = threadIdx.x / team;   // of a consumer
+
+  if (warp == RING_WARPS) {
+    if (lane == 0) {
+      int s = 0, ph = 0;
+      int64_t k = 0;
+      for (; k < mine; ++k) {
+        if (!wait_bounded<false>(empty(s), ph ^ 1, wd)) break;
+        const int64_t row = blockIdx.x + k * step;
+        const uint32_t dst = smem_addr(ring) + s * stage_bytes;
+        mbar_arrive_expect_tx(full(s), stage_bytes);
+        bulk_load_1d(dst, static_cast<const T*>(p.dy) + row * p.lddy, q.row_bytes, full(s));
+        bulk_load_1d(dst + q.row_bytes, static_cast<const T*>(p.h) + row * p.ldh, q.row_bytes, full(s));
+        if (p.dh)
+          bulk_load_1d(dst + 2 * q.row_bytes, static_cast<const T*>(p.dh) + row * p.lddh,
+                       q.row_bytes, full(s));
+        if (++s == q.stages) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+      if (k < mine)   // given up: the copies under way land before the CTA ends
+        for (int64_t j = k > q.stages ? k - q.stages : 0; j < k; ++j)
+          wait_drain(full(static_cast<int>(j % q.stages)), static_cast<uint32_t>(j / q.stages) & 1);
+    }
+  } else if (which < q.teams) {
+    Raw<T> wr[VPT] = {};
+#pragma unroll
+    for (int k = 0; k < VPT; ++k)
+      if (k * team + t < groups) wr[k] = static_cast<const Raw<T>*>(p.weight)[k * team + t];
+    const uint64_t seed = p.drop.rng[0], first = p.drop.rng[1];
+    int s = which % q.stages, turn = 0;
+    uint32_t ph = which / q.stages;
+    for (int64_t k = which; k < mine; k += q.teams, turn ^= 1) {
+      const int64_t row = blockIdx.x + k * step;
+      const float r = p.rstd[row];
+      bool ok = warp_wait_spin(full(s), ph & 1, wd);
+      const Raw<T>* dy = reinterpret_cast<const Raw<T>*>(ring + s * stage_bytes);
+      const Raw<T>* h = reinterpret_cast<const Raw<T>*>(ring + s * stage_bytes + q.row_bytes);
+      const Raw<T>* dh = reinterpret_cast<const Raw<T>*>(ring + s * stage_bytes + 2 * q.row_bytes);
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const int g = j * team + t;
+        if (g < groups) {
+          float a[GROUP], n[GROUP], w[GROUP];
+          unpack(dy[g], a);
+          unpack(h[g], n);
+          unpack(wr[j], w);
+#pragma unroll
+          for (int i = 0; i < GROUP; ++i) {
+            const float ni = n[i] * r;
+            acc[j][i] = fmaf(a[i], ni, acc[j][i]);
+            sum = fmaf(a[i] * w[i], ni, sum);
+          }
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (warps > 1) {
+        if (lane == 0) box[turn][warp] = sum;
+        ok = team_sync(1 + which, team, ok);   // the team's warps give up together
+        sum = 0.0f;
+        for (int v = 0; v < warps; ++v) sum += box[turn][which * warps + v];
+      }
+      if (!ok) break;
+      const float rc = r * (sum / static_cast<float>(cols));
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const int g = j * team + t;
+        if (g < groups) {
+          float a[GROUP], n[GROUP], w[GROUP], d[1][GROUP];
+          unpack(dy[g], a);
+          unpack(h[g], n);
+          unpack(wr[j], w);
+          Raw<T> dr = {};
+          if (p.dh) dr = dh[g];
+          unpack(dr, d[0]);
+#pragma unroll
+          for (int i = 0; i < GROUP; ++i) d[0][i] = fmaf(r, a[i] * w[i] - n[i] * rc, d[0][i]);
+          if (p.dres) reinterpret_cast<Raw<T>*>(static_cast<T*>(p.dres) + row * p.lddres)[g] = pack<T>(d[0]);
+          if (ON) {
+            const uint64_t counter[1] = {first + static_cast<uint64_t>(row) * groups + g};
+            drop_groups(p.drop, seed, counter, d);
+          }
+          reinterpret_cast<Raw<T>*>(static_cast<T*>(p.dx) + row * p.lddx)[g] = pack<T>(d[0]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(s));
+      s += q.teams;
+      while (s >= q.stages) {
+        s -= q.stages;
+        ++ph;
+      }
+    }
+  }
+  if (!p.partial) return;
+  // The teams' shares of dweight, added in the teams' order.
+  __syncthreads();
+  float* share = reinterpret_cast<float*>(ring);
+  for (int c = threadIdx.x; c < cols; c += blockDim.x) share[c] = 0.0f;
+  for (int v = 0; v < q.teams; ++v) {
+    __syncthreads();
+    if (warp < RING_WARPS && which == v) {
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        const int g = k * team + t;
+        if (g < groups) {
+#pragma unroll
+          for (int i = 0; i < GROUP; ++i) share[g * GROUP + i] += acc[k][i];
+        }
+      }
+    }
+  }
+  __syncthreads();
+  float* out = p.partial + static_cast<size_t>(blockIdx.x) * cols;
   for (int c = threadIdx.x; c < cols; c += blockDim.x) out[c] = share[c];
 }
 
