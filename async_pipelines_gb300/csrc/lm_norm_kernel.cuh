@@ -186,6 +186,38 @@ struct Bits<2> { using type = uint16_t; };
 template <>
 struct Bits<4> { using type = uint32_t; };
 
+// Two fp32 values in a register pair, for the instructions that take two at
+// once: the gradient's arithmetic would else need as many issue slots as its
+// memory traffic leaves.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair_of(float lo, float hi) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 values_of(Pair p) {
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void unpack(const Raw<T>& raw, Pair (&v)[GROUP / 2]) {
+  float f[GROUP];
+  unpack(raw, f);
+#pragma unroll
+  for (int i = 0; i < GROUP / 2; ++i) v[i] = pair_of(f[2 * i], f[2 * i + 1]);
+}
+
 // How a kernel's rows lie, and whether values are dropped. FAST: every row of
 // every matrix starts on a 16-byte boundary and ends with a whole group. DROP
 // is FAST with dropout: the generator's rounds only overlap the loads around
@@ -535,14 +567,18 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) add_rms_norm_grad_kernel(co
 
 // The same for many rows that lie FAST: the rows come through a ring in shared
 // memory, filled by one warp's bulk copies, so that the next rows are on their
-// way while a team waits for its row's sum. (Loaded straight into registers the
-// rows of an SM stop at each such wait: 8192 x 8192 bf16 took 124 us, with
-// dropout 171.) RING_WARPS warps form teams of `team` threads; the CTA's k-th row goes
-// to team k % teams through stage k % stages.
+// way while a team waits for its row's sum (loaded straight into registers the
+// rows of an SM stop at each such wait: 8192 x 8192 bf16 took 124 us, with dropout
+// 171, against 86 and 127: 0.92 and 0.78 of the copy rate). Both passes over a
+// row read it from the ring: holding it in registers in between cost more
+// (130 us) than the second reading, with one CTA's warps waiting together.
+// RING_WARPS warps form teams of `team` threads; the CTA's k-th row goes to
+// team k % teams through stage k % stages.
 constexpr int RING_WARPS = 16;
 constexpr int RING_THREADS = (RING_WARPS + 1) * 32;
-constexpr int RING_MAX_STAGES = 16;
-constexpr uint32_t RING_BYTES = 208 * 1024;
+constexpr int RING_MAX_STAGES = 32;
+// Shared memory of the ring with 1 or 2 CTAs on an SM.
+__host__ __device__ constexpr uint32_t ring_bytes(int ctas) { return (ctas == 2 ? 104 : 208) * 1024; }
 
 struct NormGradRing {
   NormGradParams p;
@@ -551,6 +587,23 @@ struct NormGradRing {
   uint32_t* status;
   unsigned long long timeout_ns;
 };
+
+// A bounded wait without a call (a call's conventions would spill the sums that
+// live across it) and, at first, without the slow global timer.
+__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, const Watchdog& wd) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1; !mbar_test_wait(bar, parity); ++it) {
+    if (it & 1023) continue;
+    if (*wd.abort) return false;
+    if (t0 == 0) t0 = global_timer_ns();
+    if (global_timer_ns() - t0 > wd.limit_ns) {
+      *wd.abort = 1;
+      atomicExch(wd.status, STATUS_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
 
 // Barrier `id` of `threads` threads; whether `ok` holds for all of them.
 __device__ __forceinline__ bool team_sync(int id, int threads, bool ok) {
@@ -566,8 +619,8 @@ __device__ __forceinline__ bool team_sync(int id, int threads, bool ok) {
   return all != 0;
 }
 
-template <typename T, bool ON, int VPT>
-__global__ void __launch_bounds__(RING_THREADS, 1)
+template <typename T, bool ON, int VPT, int CTAS>
+__global__ void __launch_bounds__(RING_THREADS, CTAS)
     add_rms_norm_grad_ring_kernel(const __grid_constant__ NormGradRing q) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ __align__(8) uint64_t bars[2 * RING_MAX_STAGES];
@@ -595,105 +648,121 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
   const int64_t step = gridDim.x;
   const int64_t mine = (p.rows - blockIdx.x + step - 1) / step;   // this CTA's rows
 
-  float acc[VPT][GROUP];
+  Pair acc[VPT][GROUP / 2];
 #pragma unroll
   for (int k = 0; k < VPT; ++k)
 #pragma unroll
-    for (int i = 0; i < GROUP; ++i) acc[k][i] = 0.0f;
+    for (int i = 0; i < GROUP / 2; ++i) acc[k][i] = 0;
   const int t = threadIdx.x % team, which = threadIdx.x / team;   // of a consumer
 
   if (warp == RING_WARPS) {
-    if (lane == 0) {
-      int s = 0, ph = 0;
-      int64_t k = 0;
-      for (; k < mine; ++k) {
-        if (!wait_bounded<false>(empty(s), ph ^ 1, wd)) break;
-        const int64_t row = blockIdx.x + k * step;
-        const uint32_t dst = smem_addr(ring) + s * stage_bytes;
-        mbar_arrive_expect_tx(full(s), stage_bytes);
-        bulk_load_1d(dst, static_cast<const T*>(p.dy) + row * p.lddy, q.row_bytes, full(s));
-        bulk_load_1d(dst + q.row_bytes, static_cast<const T*>(p.h) + row * p.ldh, q.row_bytes, full(s));
-        if (p.dh)
-          bulk_load_1d(dst + 2 * q.row_bytes, static_cast<const T*>(p.dh) + row * p.lddh,
-                       q.row_bytes, full(s));
-        if (++s == q.stages) {
-          s = 0;
-          ph ^= 1;
-        }
+    // A lane for each matrix: one thread's copies of 2 KiB would come too slowly.
+    int s = 0;
+    uint32_t ph = 0;
+    int64_t k = 0;
+    const T* src = static_cast<const T*>(lane == 0 ? p.dy : lane == 1 ? p.h : p.dh);
+    const int64_t ld = lane == 0 ? p.lddy : lane == 1 ? p.ldh : p.lddh;
+    for (; k < mine; ++k) {
+      if (!__all_sync(0xffffffffu, ring_wait(empty(s), ph ^ 1, wd))) break;
+      if (lane == 0) mbar_arrive_expect_tx(full(s), stage_bytes);
+      __syncwarp();
+      if (lane < inputs)
+        bulk_load_1d(smem_addr(ring) + s * stage_bytes + lane * q.row_bytes,
+                     src + (blockIdx.x + k * step) * ld, q.row_bytes, full(s));
+      if (++s == q.stages) {
+        s = 0;
+        ph ^= 1;
       }
-      if (k < mine)   // given up: the copies under way land before the CTA ends
-        for (int64_t j = k > q.stages ? k - q.stages : 0; j < k; ++j)
-          wait_drain(full(static_cast<int>(j % q.stages)), static_cast<uint32_t>(j / q.stages) & 1);
     }
+    if (k < mine)   // given up: the copies under way land before the CTA ends
+      for (int64_t j = k > q.stages ? k - q.stages : 0; j < k; ++j)
+        wait_drain(full(static_cast<int>(j % q.stages)), static_cast<uint32_t>(j / q.stages) & 1);
   } else if (which < q.teams) {
+    const uint64_t seed = p.drop.rng[0], first = p.drop.rng[1];
+    int s = which, turn = 0;
+    uint32_t ph = 0;
     Raw<T> wr[VPT] = {};
 #pragma unroll
-    for (int k = 0; k < VPT; ++k)
-      if (k * team + t < groups) wr[k] = static_cast<const Raw<T>*>(p.weight)[k * team + t];
-    const uint64_t seed = p.drop.rng[0], first = p.drop.rng[1];
-    int s = which % q.stages, turn = 0;
-    uint32_t ph = which / q.stages;
+    for (int j = 0; j < VPT; ++j)
+      if (j * team + t < groups) wr[j] = static_cast<const Raw<T>*>(p.weight)[j * team + t];
+    float next_r = which < mine ? p.rstd[blockIdx.x + which * step] : 0.0f;
     for (int64_t k = which; k < mine; k += q.teams, turn ^= 1) {
       const int64_t row = blockIdx.x + k * step;
-      const float r = p.rstd[row];
-      bool ok = warp_wait_spin(full(s), ph & 1, wd);
-      const Raw<T>* dy = reinterpret_cast<const Raw<T>*>(ring + s * stage_bytes);
-      const Raw<T>* h = reinterpret_cast<const Raw<T>*>(ring + s * stage_bytes + q.row_bytes);
-      const Raw<T>* dh = reinterpret_cast<const Raw<T>*>(ring + s * stage_bytes + 2 * q.row_bytes);
-      float sum = 0.0f;
+      const float r = next_r;
+      if (k + q.teams < mine) next_r = p.rstd[row + q.teams * step];
+      bool ok = __all_sync(0xffffffffu, ring_wait(full(s), ph, wd));
+      const Raw<T>* dy = reinterpret_cast<const Raw<T>*>(ring + s * stage_bytes) + t;
+      const Raw<T>* h = reinterpret_cast<const Raw<T>*>(ring + s * stage_bytes + q.row_bytes) + t;
+      const Raw<T>* dh = reinterpret_cast<const Raw<T>*>(ring + s * stage_bytes + 2 * q.row_bytes) + t;
+      // acc += dy h r, and the sum of dy weight h
+      const Pair r2 = pair_of(r, r);
+      Pair sums = 0;
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
-        const int g = j * team + t;
-        if (g < groups) {
-          float a[GROUP], n[GROUP], w[GROUP];
-          unpack(dy[g], a);
-          unpack(h[g], n);
+        if (j * team + t < groups) {
+          Pair a[GROUP / 2], n[GROUP / 2], w[GROUP / 2];
+          unpack(dy[j * team], a);
+          unpack(h[j * team], n);
           unpack(wr[j], w);
 #pragma unroll
-          for (int i = 0; i < GROUP; ++i) {
-            const float ni = n[i] * r;
-            acc[j][i] = fmaf(a[i], ni, acc[j][i]);
-            sum = fmaf(a[i] * w[i], ni, sum);
+          for (int i = 0; i < GROUP / 2; ++i) {
+            const Pair an = mul2(a[i], n[i]);
+            acc[j][i] = fma2(an, r2, acc[j][i]);
+            sums = fma2(an, w[i], sums);
           }
         }
       }
+      float sum = values_of(sums).x + values_of(sums).y;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       if (warps > 1) {
         if (lane == 0) box[turn][warp] = sum;
         ok = team_sync(1 + which, team, ok);   // the team's warps give up together
-        sum = 0.0f;
-        for (int v = 0; v < warps; ++v) sum += box[turn][which * warps + v];
+        sum = (lane & 15) < warps ? box[turn][which * warps + (lane & 15)] : 0.0f;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       }
       if (!ok) break;
-      const float rc = r * (sum / static_cast<float>(cols));
+      // dres = dh + r dy weight - h r^2 mean(dy weight h r)
+      const float m = -r * r * (r * sum / static_cast<float>(cols));
+      const Pair m2 = pair_of(m, m);
+      Raw<T>* dres = reinterpret_cast<Raw<T>*>(static_cast<T*>(p.dres) + row * p.lddres) + t;
+      Raw<T>* dx = reinterpret_cast<Raw<T>*>(static_cast<T*>(p.dx) + row * p.lddx) + t;
+      float d[VPT][GROUP];
+      uint64_t counter[VPT];
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
-        const int g = j * team + t;
-        if (g < groups) {
-          float a[GROUP], n[GROUP], w[GROUP], d[1][GROUP];
-          unpack(dy[g], a);
-          unpack(h[g], n);
+        counter[j] = first + static_cast<uint64_t>(row) * groups + j * team + t;
+        if (j * team + t < groups) {
+          Pair a[GROUP / 2], n[GROUP / 2], w[GROUP / 2], e[GROUP / 2];
+          unpack(dy[j * team], a);
+          unpack(h[j * team], n);
           unpack(wr[j], w);
           Raw<T> dr = {};
-          if (p.dh) dr = dh[g];
-          unpack(dr, d[0]);
+          if (p.dh) dr = dh[j * team];
+          unpack(dr, e);
 #pragma unroll
-          for (int i = 0; i < GROUP; ++i) d[0][i] = fmaf(r, a[i] * w[i] - n[i] * rc, d[0][i]);
-          if (p.dres) reinterpret_cast<Raw<T>*>(static_cast<T*>(p.dres) + row * p.lddres)[g] = pack<T>(d[0]);
-          if (ON) {
-            const uint64_t counter[1] = {first + static_cast<uint64_t>(row) * groups + g};
-            drop_groups(p.drop, seed, counter, d);
+          for (int i = 0; i < GROUP / 2; ++i) {
+            e[i] = fma2(n[i], m2, fma2(mul2(a[i], w[i]), r2, e[i]));
+            d[j][2 * i] = values_of(e[i]).x;
+            d[j][2 * i + 1] = values_of(e[i]).y;
           }
-          reinterpret_cast<Raw<T>*>(static_cast<T*>(p.dx) + row * p.lddx)[g] = pack<T>(d[0]);
+          if (p.dres) dres[j * team] = pack<T>(d[j]);
+          if (!ON) dx[j * team] = pack<T>(d[j]);
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty(s));
       s += q.teams;
-      while (s >= q.stages) {
+      if (s >= q.stages) {
         s -= q.stages;
-        ++ph;
+        ph ^= 1;
+      }
+      if (ON) {
+        drop_groups(p.drop, seed, counter, d);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+          if (j * team + t < groups) dx[j * team] = pack<T>(d[j]);
       }
     }
   }
@@ -710,7 +779,10 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
         const int g = k * team + t;
         if (g < groups) {
 #pragma unroll
-          for (int i = 0; i < GROUP; ++i) share[g * GROUP + i] += acc[k][i];
+          for (int i = 0; i < GROUP / 2; ++i) {
+            share[g * GROUP + 2 * i] += values_of(acc[k][i]).x;
+            share[g * GROUP + 2 * i + 1] += values_of(acc[k][i]).y;
+          }
         }
       }
     }

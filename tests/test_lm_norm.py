@@ -180,6 +180,37 @@ def test_norm_and_gradients(g, dtype, T, H, form):
 
 
 @gpu
+@pytest.mark.parametrize("T,H,dtype", [
+    (608, 8, torch.bfloat16), (650, 8192, torch.bfloat16), (700, 4104, torch.float16),
+    (1400, 2048, torch.float32), (615, 16384, torch.bfloat16), (640, 8192, torch.float32),
+    (620, 16384, torch.float32), (609, 10008, torch.float16), (4000, 264, torch.bfloat16)])
+@pytest.mark.parametrize("dropout", [False, True])
+def test_gradients_of_many_rows(g, T, H, dtype, dropout):
+    """Enough rows for several on each SM; strides between rows, with and without dh."""
+    gen = torch.Generator().manual_seed(T + H)
+    dy, h, dh = (rows(T, H, dtype, gen, 8, 0, s) for s in (1.0, 2.0, 0.5))
+    w = rows(1, H, dtype, gen)[0]
+    rstd = (0.1 + torch.rand(T, generator=gen)).cuda()
+    p, words = (0.25, rng_words(7, 11)) if dropout else (0.0, None)
+    dx, dres, dw = (torch.empty(T, H, dtype=dtype, device="cuda"), rows(T, H, dtype, gen, 16),
+                    torch.empty_like(w))
+    for given in (dh, None):
+        g.add_rms_norm_backward(dy, h, w, rstd, dx, dw, dh=given, dresidual=dres, p=p, rng=words)
+        want = ref.add_rms_norm_backward(dy.cpu(), h.cpu(), w.cpu(), rstd.cpu(),
+                                         None if given is None else given.cpu())
+        close(dres, want[1], dtype, want[3], what="dres")
+        close(dw, want[2], dtype, want[4], what="dw")
+        if dropout:
+            # the mask of a plain call on ones, which its own test checks
+            keep = torch.empty(T, H, device="cuda")
+            g.dropout(torch.ones_like(keep), keep, p, words)
+            keep = keep.cpu().double()
+            close(dx, ref.apply_keep(want[1], keep), dtype, want[3] * 2, what="dx")
+        else:
+            assert torch.equal(dx, dres)
+
+
+@gpu
 def test_norm_without_residual_and_in_place(g):
     gen = torch.Generator().manual_seed(8)
     x, res = rows(33, 520, torch.bfloat16, gen), rows(33, 520, torch.bfloat16, gen)
