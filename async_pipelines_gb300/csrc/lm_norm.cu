@@ -91,17 +91,19 @@ struct Team {
 // Longer rows take a block. With few rows (less than two for each SM) every
 // thread takes one group, for the shortest row; with many, two (up to 512
 // threads), so that more than one row is in flight on an SM; beyond 8192
-// columns four.
-Team pick_team(const gemm_ws* h, int64_t rows, int64_t cols) {
+// columns four. On the general path, whose groups move element by element, a
+// thread takes one group wherever a block can hold the row so.
+Team pick_team(const gemm_ws* h, int64_t rows, int64_t cols, gws::Path path) {
   const int64_t groups = ceil_div(cols, gws::GROUP);
+  const bool any = path == gws::ANY;
   Team t;
-  if (groups <= 128) {
+  if (groups <= (any ? 32 : 128)) {
     t.vpt = groups <= 32 ? 1 : groups <= 64 ? 2 : 4;
     t.threads = 32;
     t.rows = rows >= 8 * h->num_sms ? 8 : rows >= 2 * h->num_sms ? 4 : 1;
     return t;
   }
-  t.vpt = rows < 2 * h->num_sms && groups <= 1024 ? 1 : groups <= 1024 ? 2 : 4;
+  t.vpt = groups > 1024 ? 4 : any || rows < 2 * h->num_sms ? 1 : 2;
   t.threads = static_cast<int>(ceil_div(ceil_div(groups, t.vpt), 32) * 32);
   t.rows = 1;
   return t;
@@ -350,7 +352,7 @@ int gemm_ws_add_rms_norm(gemm_ws_t* h, int dtype, const void* x, int64_t ldx,
   q.wide = in[0].wide() && (!residual || in[1].wide()) &&
            reinterpret_cast<uintptr_t>(weight) % 16 == 0 && (!hidden || mh.wide()) && my.wide();
   const gws::Path path = pick_path(q.wide, cols, q.drop);
-  const Team t = pick_team(h, rows, cols);
+  const Team t = pick_team(h, rows, cols, path);
   q.team = t.threads;
   DeviceGuard guard(h->device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -442,7 +444,7 @@ int gemm_ws_add_rms_norm_backward(gemm_ws_t* h, int dtype, const void* dy, int64
       }
     }
   }
-  const Team t = pick_team(h, rows, cols);
+  const Team t = pick_team(h, rows, cols, path);
   q.team = t.threads;
   switch (dtype) {
     case GEMM_WS_BF16: return launch_grad<__nv_bfloat16>(h, t, path, q, dweight, s);

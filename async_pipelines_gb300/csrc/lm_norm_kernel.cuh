@@ -792,7 +792,7 @@ __global__ void __launch_bounds__(RING_THREADS, CTAS)
   for (int c = threadIdx.x; c < cols; c += blockDim.x) out[c] = share[c];
 }
 
-constexpr int DW_COLS = 32, DW_LANES = 8;   // a block's columns, and partial rows in flight
+constexpr int DW_COLS = 32, DW_LANES = 32;  // a block's columns, and partial rows in flight
 
 struct DweightParams {
   const float* partial;

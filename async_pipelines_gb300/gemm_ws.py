@@ -221,6 +221,7 @@ class GemmWS(_lm.LmOps):
 
     def __init__(self, device: int = 0, lib=None):
         self.device = int(device)
+        self._ce_need = {}   # workspace bytes of the cross entropy, by sizes
         self.lib = lib or load_library()
         h = ctypes.c_void_p()
         rc = self.lib.gemm_ws_create(ctypes.byref(h), self.device)
@@ -238,8 +239,6 @@ class GemmWS(_lm.LmOps):
             self.close()
         except Exception:
             pass
-
-    _stream_of = staticmethod(_stream_handle)
 
     def _raise(self, rc, what):
         if rc != OK:

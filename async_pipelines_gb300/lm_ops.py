@@ -50,10 +50,12 @@ def _rows(name, t, shape, dtype):
         raise ValueError(f"{name} must be a {tuple(shape)} {dtype} CUDA tensor, got "
                          f"{tuple(t.shape)} {t.dtype} on {t.device}")
     step, inner = t.stride()
-    rows, cols = shape
-    if (inner != 1 and cols > 1) or (step < cols and rows > 1):
-        raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    return t.data_ptr(), step if step > cols else cols
+    cols = shape[1]
+    if inner != 1 or step < cols:   # of one column, or one row, a stride says nothing
+        if (inner != 1 and cols > 1) or (step < cols and shape[0] > 1):
+            raise ValueError(f"{name} must have contiguous rows that do not overlap")
+        step = max(step, cols)
+    return t.data_ptr(), step
 
 
 def _flat(name, t, n, dtype):
@@ -67,10 +69,10 @@ def _flat(name, t, n, dtype):
 
 def _mask(p, rng):
     """The pointer of the generator's words; None where nothing is dropped."""
-    if not 0.0 <= p <= 1.0:
-        raise ValueError("p must be in [0, 1]")
     if p == 0.0:
         return None
+    if not 0.0 <= p <= 1.0:
+        raise ValueError("p must be in [0, 1]")
     if rng is None:
         raise ValueError("dropout needs rng: an int64 CUDA tensor (seed, first counter)")
     return _flat("rng", rng, 2, torch.int64)
@@ -83,8 +85,22 @@ def _type_of(x):
     return code
 
 
+# torch.cuda.current_stream() builds an object, which takes as long as a launch.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 class LmOps:
-    """The operators' methods, on an object with `lib` and `handle`."""
+    """The operators' methods, on an object with `lib`, `handle` and `device`."""
+
+    def _stream_of(self, stream) -> int:
+        """The raw cudaStream_t of `stream` (default: the device's current torch stream)."""
+        if stream is None:
+            if _raw_stream is not None:
+                return _raw_stream(self.device)
+            return torch.cuda.current_stream(self.device).cuda_stream
+        if isinstance(stream, torch.cuda.Stream):
+            return stream.cuda_stream
+        return int(stream)
 
     def dropout(self, x, y, p, rng, stream=None):
         """y = keep * x / (1 - p); x, y: (rows, cols) of one type; y may be x.
@@ -166,10 +182,17 @@ class LmOps:
 
     def linear_cross_entropy_workspace(self, tokens, hidden, vocab, backward=False) -> int:
         """Bytes of workspace that one call needs."""
+        sizes = (tokens, hidden, vocab, bool(backward))
+        n = self._ce_need.get(sizes)
+        if n is not None:
+            return n
         n = self.lib.gemm_ws_linear_ce_workspace(self.handle, tokens, hidden, vocab,
                                                  int(bool(backward)))
         if n < 0:
             self._raise(-n, "gemm_ws_linear_ce_workspace")
+        if len(self._ce_need) >= 1024:
+            self._ce_need.clear()
+        self._ce_need[sizes] = n
         return n
 
     def _workspace(self, workspace, need, x, stream):
