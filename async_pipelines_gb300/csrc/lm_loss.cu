@@ -133,6 +133,11 @@ bool operand(gemm_ws* h, CUtensorMap* m, const void* ptr, int64_t inner, int64_t
   return encode(h, m, ptr, false, inner, rows, 1, ld, ld * rows, 64, mn ? 64 : box_rows);
 }
 
+// Rows of x in a box: fewer than 128 tokens come in a box of their own size. The
+// TMA fills rows that are not there more slowly than it fetches rows that are: one
+// token over 131072 x 4096 took 238 us with boxes of 128 rows, 61 tokens 173.
+int box_rows(int64_t T) { return static_cast<int>(T < ce::BM ? T : ce::BM); }
+
 template <typename P>
 int launch(gemm_ws* h, void (*kernel)(P), int64_t blocks, int threads, size_t smem, int cluster,
            cudaStream_t s, const P& params) {
@@ -247,6 +252,7 @@ ce::Params product_params(const gemm_ws* h, const Plan& q, uint8_t* ws, const Ti
   p.jobs = 1;
   p.bn = t.bn;
   p.stages = ring_stages(t);
+  p.a_rows = ce::BM;
   p.count = reinterpret_cast<const int*>(ws + q.count);
   p.target = reinterpret_cast<const int*>(ws + q.target);
   p.part_stride = T;
@@ -328,11 +334,12 @@ int gemm_ws_linear_ce(gemm_ws_t* h, const uint16_t* x, int64_t ldx, const uint16
   job.k = static_cast<int>(H);
   job.splits = 1;
   job.out = ce::OUT_LSE;
+  p.a_rows = box_rows(T);
   p.cols = static_cast<int>(V);
   p.target_logit = pack.target_logit;
   p.part = reinterpret_cast<float2*>(ws + q.part);
   p.carry = q.carry;
-  if (!operand(h, &job.tmA, pack.packed, H, T, H, false, ce::BM) ||
+  if (!operand(h, &job.tmA, pack.packed, H, T, H, false, p.a_rows) ||
       !operand(h, &job.tmB, weight, H, V, ldw, false, q.logits.bn / q.logits.cg))
     return GEMM_WS_ERR_CUDA;
 
@@ -407,6 +414,7 @@ int gemm_ws_linear_ce_backward(gemm_ws_t* h, const uint16_t* x, int64_t ldx,
 
   // The products of a piece; what changes from piece to piece is set below.
   ce::Params pg = product_params(h, q, ws, q.logits, T);
+  pg.a_rows = box_rows(T);
   pg.lse = pack.lse_out;
   pg.grad = pack.grad_out;
   ce::Job& jg = pg.job[0];
@@ -419,7 +427,7 @@ int gemm_ws_linear_ce_backward(gemm_ws_t* h, const uint16_t* x, int64_t ldx,
   const int b_rows = q.sums.bn / q.sums.cg;
   ce::Job* jx = dx ? &ps.job[ps.jobs++] : nullptr;
   ce::Job* jw = dweight ? &ps.job[ps.jobs++] : nullptr;
-  bool ok = operand(h, &jg.tmA, pack.packed, H, T, H, false, ce::BM) &&
+  bool ok = operand(h, &jg.tmA, pack.packed, H, T, H, false, pg.a_rows) &&
             operand(h, &jg.tmB, weight, H, V, ldw, false, q.logits.bn / q.logits.cg);
   if (jx) {
     jx->m = -1;

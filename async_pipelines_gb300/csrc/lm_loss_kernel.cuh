@@ -91,6 +91,8 @@ struct Params {
   Job job[2];
   int jobs;
   int bn, stages;            // tile columns; ring stages
+  int a_rows;                // rows of A that a box brings: 128, or all there are if fewer (what
+                             // lies below them in a stage is never looked at)
   const int* count;          // counted rows
   // LSE and GRAD: the logits' rows and columns
   int cols;                  // valid columns of the launch (its piece of the vocabulary)
@@ -158,8 +160,9 @@ __device__ __forceinline__ void producer(const Params& p, uint32_t sbase, uint32
   auto empty = [&](uint32_t s) { return sbase + OFF_BAR + 8 * (BAR_EMPTY + s); };
   const int cluster = blockIdx.x / CG, clusters = gridDim.x / CG;
   const bool leader = a_part && rank == 0;   // arms full[s] for the pair
-  const uint32_t stages = p.stages, sbytes = stage_bytes<CG>(p.bn), tx = CG * sbytes;
+  const uint32_t stages = p.stages, sbytes = stage_bytes<CG>(p.bn);
   const uint32_t b_block = static_cast<uint32_t>(p.bn / CG) * BK * 2;
+  const uint32_t tx = CG * ksub<CG>() * (p.a_rows * BK * 2 + b_block);
   uint32_t s = 0, ph = 0, g = 0;
   bool ok = true;
   Unit w;
