@@ -55,6 +55,7 @@ struct Plan {
   int64_t slots;      // partial maxima and sums a row
   int64_t piece, pieces;
   int64_t cuts;
+  int64_t pitch;      // of the packed rows of x
   int64_t blocks;     // of the joining kernel
   // byte offsets in the workspace
   int64_t packed, place, target, count, logit, part, block_sum, lse, grad, g, sums_at, bytes;
@@ -69,7 +70,8 @@ Plan make_plan(const gemm_ws* h, int64_t T, int64_t H, int64_t V, bool backward)
     at += round_up(bytes, 256);
     return here;
   };
-  q.packed = take(T * H * 2);
+  q.pitch = round_up(H, 64);   // whole 128-byte lines: x's boxes never straddle one
+  q.packed = take(T * q.pitch * 2);
   q.place = take(T * 4);
   q.target = take(T * 4);
   q.count = take(4);
@@ -240,6 +242,7 @@ ce::PackParams pack_params(const Plan& q, uint8_t* ws, const uint16_t* x, int64_
   int64_t chunk = ceil_div(T, int64_t{8} * num_sms);
   p.chunk = static_cast<int>(chunk < ce::PACK_THREADS ? chunk : ce::PACK_THREADS);
   p.packed = reinterpret_cast<uint16_t*>(ws + q.packed);
+  p.pitch = q.pitch;
   p.place = reinterpret_cast<int*>(ws + q.place);
   p.target_out = reinterpret_cast<int*>(ws + q.target);
   p.count = reinterpret_cast<int*>(ws + q.count);
@@ -339,7 +342,7 @@ int gemm_ws_linear_ce(gemm_ws_t* h, const uint16_t* x, int64_t ldx, const uint16
   p.target_logit = pack.target_logit;
   p.part = reinterpret_cast<float2*>(ws + q.part);
   p.carry = q.carry;
-  if (!operand(h, &job.tmA, pack.packed, H, T, H, false, p.a_rows) ||
+  if (!operand(h, &job.tmA, pack.packed, H, T, q.pitch, false, p.a_rows) ||
       !operand(h, &job.tmB, weight, H, V, ldw, false, q.logits.bn / q.logits.cg))
     return GEMM_WS_ERR_CUDA;
 
@@ -427,7 +430,7 @@ int gemm_ws_linear_ce_backward(gemm_ws_t* h, const uint16_t* x, int64_t ldx,
   const int b_rows = q.sums.bn / q.sums.cg;
   ce::Job* jx = dx ? &ps.job[ps.jobs++] : nullptr;
   ce::Job* jw = dweight ? &ps.job[ps.jobs++] : nullptr;
-  bool ok = operand(h, &jg.tmA, pack.packed, H, T, H, false, pg.a_rows) &&
+  bool ok = operand(h, &jg.tmA, pack.packed, H, T, q.pitch, false, pg.a_rows) &&
             operand(h, &jg.tmB, weight, H, V, ldw, false, q.logits.bn / q.logits.cg);
   if (jx) {
     jx->m = -1;
@@ -444,7 +447,7 @@ int gemm_ws_linear_ce_backward(gemm_ws_t* h, const uint16_t* x, int64_t ldx,
     jw->a_mn = jw->b_mn = 1;
     jw->splits = 1;
     jw->out = ce::OUT_BF16;
-    ok = ok && operand(h, &jw->tmB, pack.packed, H, T, H, true, b_rows) &&
+    ok = ok && operand(h, &jw->tmB, pack.packed, H, T, q.pitch, true, b_rows) &&
          encode(h, &jw->tmD, dweight, false, H, V, 1, lddw, lddw * V, 64, 32);
   }
   if (!ok) return GEMM_WS_ERR_CUDA;

@@ -60,6 +60,12 @@ constexpr uint32_t OFF_TMEM = OFF_BAR + NUM_BARS * 8;
 constexpr uint32_t OFF_ABORT = OFF_TMEM + 4;
 constexpr uint32_t SMEM_BYTES = OFF_ABORT + 4 + 1024;   // + slack to align the base
 static_assert(SMEM_BYTES <= 232448, "exceeds the 227 KiB per-CTA shared memory");
+// The tensor cores cut off what an addition to the accumulator shifts out, so a
+// logit that grows over a long K ends too near to zero: by 5e-6 of lse with 8192
+// hidden, 20 times fp32 sums' error. So the logits' sums are cut into 512 of K
+// each, which the epilogue adds in registers with rounding. (The gradients'
+// products, which end in bf16, need none of it.)
+constexpr int CHUNK_K = 512;
 constexpr float LOG2E = 1.4426950408889634f;
 
 enum Mode { LSE = 0, GRAD = 1, SUMS = 2 };
@@ -118,37 +124,101 @@ struct Unit {
 
 constexpr int GROUP_M = 8;   // tiles walk 8 rows of tiles down, then step a column (L2 reuse)
 
-// The i-th unit of cluster c of `clusters`: units c, c + clusters, ... of the
-// jobs' units one after the other.
+// Tiles, and ring stages of K, of a job.
 template <int CG>
-__device__ __forceinline__ bool next_unit(const Params& p, int count, int c, int clusters, int i,
-                                          Unit& w) {
-  int u = c + i * clusters;
-  for (int j = 0; j < p.jobs; ++j) {
-    const Job& job = p.job[j];
-    const int m = job.m < 0 ? count : job.m;
-    const int tm = (m + BM * CG - 1) / (BM * CG), tn = (job.n + p.bn - 1) / p.bn;
-    const int tiles = tm * tn;
-    if (u >= tiles * job.splits) {
-      u -= tiles * job.splits;
-      continue;
-    }
-    w.job = &job;
-    w.cut = u / tiles;
-    const int t = u - w.cut * tiles;
-    const int g = t / (GROUP_M * tn), first = g * GROUP_M;
-    const int gm = tm - first < GROUP_M ? tm - first : GROUP_M;
-    const int r = t - g * GROUP_M * tn;
-    w.m0 = (first + r % gm) * BM * CG;
-    w.nb = r / gm;
-    w.n0 = w.nb * p.bn;
-    const int k = job.k < 0 ? count : job.k;
-    const int ns = (k + BK * ksub<CG>() - 1) / (BK * ksub<CG>());
-    w.s0 = static_cast<int>(static_cast<int64_t>(w.cut) * ns / job.splits);
-    w.s1 = static_cast<int>(static_cast<int64_t>(w.cut + 1) * ns / job.splits);
-    return true;
+__device__ __forceinline__ int job_tiles(const Params& p, const Job& job, int count, int* tm, int* tn) {
+  const int m = job.m < 0 ? count : job.m;
+  *tm = (m + BM * CG - 1) / (BM * CG);
+  *tn = (job.n + p.bn - 1) / p.bn;
+  return *tm * *tn;
+}
+template <int CG>
+__device__ __forceinline__ int job_stages(const Job& job, int count) {
+  const int k = job.k < 0 ? count : job.k;
+  return (k + BK * ksub<CG>() - 1) / (BK * ksub<CG>());
+}
+
+// What every role of a cluster walks: units first, first + clusters, ... of
+// the jobs' units one after the other. With two jobs, the first one's units
+// (dx's, usually the longer) leave the clusters from `heavy` on with one unit
+// less; those then take `extra` units of the second job before all go on in
+// turn, so that no cluster ends more than about one of the shorter units
+// after the others. (Without it dx's quarter-full last wave of long units
+// held the launch up: 4096 x 4096 over 131072, both gradients of a piece,
+// 1378 us.)
+struct Walk {
+  int cluster, clusters;
+  int units0;   // of the first job
+  int heavy, extra;
+};
+
+template <int CG>
+__device__ __forceinline__ Walk make_walk(const Params& p, int count) {
+  Walk k;
+  k.cluster = blockIdx.x / CG;
+  k.clusters = gridDim.x / CG;
+  k.units0 = k.heavy = k.extra = 0;
+  if (p.jobs == 2) {
+    int tm, tn;
+    k.units0 = job_tiles<CG>(p, p.job[0], count, &tm, &tn) * p.job[0].splits;
+    k.heavy = k.units0 % k.clusters;
+    const int s0 = job_stages<CG>(p.job[0], count) / p.job[0].splits;
+    const int s1 = job_stages<CG>(p.job[1], count);
+    if (k.heavy && s1 > 0) k.extra = s0 / s1;
   }
-  return false;
+  return k;
+}
+
+// The i-th unit of the walk.
+template <int CG>
+__device__ __forceinline__ bool next_unit(const Params& p, int count, const Walk& k, int i, Unit& w) {
+  int u = k.cluster + i * k.clusters;
+  int j = 0;
+  if (p.jobs == 2 && u >= k.units0) {
+    j = 1;
+    if (k.extra == 0) {
+      u -= k.units0;
+    } else {
+      // i counts on from this cluster's units of the first job
+      const bool light = k.cluster >= k.heavy;
+      const int lights = k.clusters - k.heavy;
+      const int t = i - k.units0 / k.clusters - (light ? 0 : 1);
+      const int rank = light ? k.cluster - k.heavy : k.cluster + lights;
+      if (light && t < k.extra)
+        u = t * lights + rank;
+      else
+        u = k.extra * lights + (light ? t - k.extra : t) * k.clusters + rank;
+    }
+  }
+  const Job& job = p.job[j];
+  int tm, tn;
+  const int tiles = job_tiles<CG>(p, job, count, &tm, &tn);
+  if (u >= tiles * job.splits) return false;
+  w.job = &job;
+  w.cut = u / tiles;
+  const int t = u - w.cut * tiles;
+  const int g = t / (GROUP_M * tn), first = g * GROUP_M;
+  const int gm = tm - first < GROUP_M ? tm - first : GROUP_M;
+  const int r = t - g * GROUP_M * tn;
+  w.m0 = (first + r % gm) * BM * CG;
+  w.nb = r / gm;
+  w.n0 = w.nb * p.bn;
+  const int ns = job_stages<CG>(job, count);
+  w.s0 = static_cast<int>(static_cast<int64_t>(w.cut) * ns / job.splits);
+  w.s1 = static_cast<int>(static_cast<int64_t>(w.cut + 1) * ns / job.splits);
+  return true;
+}
+
+// Ring stages that one accumulator takes before it is handed over, and how often
+// a unit's is.
+template <int CG, int MODE>
+__device__ __forceinline__ int chunk_stages(const Unit& w) {
+  return MODE == SUMS ? max(w.s1 - w.s0, 1) : CHUNK_K / (BK * ksub<CG>());
+}
+template <int CG, int MODE>
+__device__ __forceinline__ int chunks(const Unit& w) {
+  if (MODE == SUMS) return 1;
+  return (w.s1 - w.s0 + chunk_stages<CG, MODE>(w) - 1) / chunk_stages<CG, MODE>(w);
 }
 
 // ------------------------------------------------------------ producers
@@ -158,7 +228,7 @@ __device__ __forceinline__ void producer(const Params& p, uint32_t sbase, uint32
                                          int count, const Watchdog& wd) {
   auto full = [&](uint32_t s) { return sbase + OFF_BAR + 8 * (BAR_FULL + s); };
   auto empty = [&](uint32_t s) { return sbase + OFF_BAR + 8 * (BAR_EMPTY + s); };
-  const int cluster = blockIdx.x / CG, clusters = gridDim.x / CG;
+  const Walk walk = make_walk<CG>(p, count);
   const bool leader = a_part && rank == 0;   // arms full[s] for the pair
   const uint32_t stages = p.stages, sbytes = stage_bytes<CG>(p.bn);
   const uint32_t b_block = static_cast<uint32_t>(p.bn / CG) * BK * 2;
@@ -166,7 +236,7 @@ __device__ __forceinline__ void producer(const Params& p, uint32_t sbase, uint32
   uint32_t s = 0, ph = 0, g = 0;
   bool ok = true;
   Unit w;
-  for (int i = 0; ok && next_unit<CG>(p, count, cluster, clusters, i, w); ++i) {
+  for (int i = 0; ok && next_unit<CG>(p, count, walk, i, w); ++i) {
     const Job& job = *w.job;
     const CUtensorMap* map = a_part ? &job.tmA : &job.tmB;
     const bool mn = a_part ? job.a_mn : job.b_mn;
@@ -220,7 +290,7 @@ __device__ __forceinline__ void producer(const Params& p, uint32_t sbase, uint32
 
 // ------------------------------------------------------------ MMA issuer
 
-template <int CG>
+template <int CG, int MODE>
 __device__ __forceinline__ void mma_issuer(const Params& p, uint32_t sbase, uint32_t tmem,
                                            uint32_t rank, int count, const Watchdog& wd) {
   auto bar = [&](int i) { return sbase + OFF_BAR + 8 * i; };
@@ -230,61 +300,70 @@ __device__ __forceinline__ void mma_issuer(const Params& p, uint32_t sbase, uint
     else
       umma_commit_pair(b, static_cast<uint16_t>(0x3u));
   };
-  const int cluster = blockIdx.x / CG, clusters = gridDim.x / CG;
+  const Walk walk = make_walk<CG>(p, count);
   const uint32_t stages = p.stages, sbytes = stage_bytes<CG>(p.bn);
   const uint32_t b_block = static_cast<uint32_t>(p.bn / CG) * BK * 2;
   uint32_t s = 0, ph = 0;
+  uint32_t handed = 0;   // accumulators handed over so far
   bool issued = false;
   Unit w;
-  for (int i = 0; next_unit<CG>(p, count, cluster, clusters, i, w); ++i) {
+  for (int i = 0; next_unit<CG>(p, count, walk, i, w); ++i) {
     const Job& job = *w.job;
     const bool a_mn = job.a_mn, b_mn = job.b_mn;
     const uint32_t idesc = idesc_bf16_f32(BM * CG, p.bn, a_mn, b_mn);
     // 16 of K: 32 bytes along a K-major row, or 16 rows of 128 bytes
     const uint32_t a_step = a_mn ? UMMA_K * 128 : UMMA_K * 2;
     const uint32_t b_step = b_mn ? UMMA_K * 128 : UMMA_K * 2;
-    const uint32_t b = i & 1, aph = (i >> 1) & 1;
-    if (!wait_spin<true>(bar(BAR_ACC_EMPTY + b), aph ^ 1, wd)) break;
-    tc_fence_after_sync();
-    const uint32_t d = tmem + b * BN_MAX;
     bool ok = true;
-    for (int st = w.s0; st < w.s1; ++st) {
-      if (!wait_spin<true>(bar(BAR_FULL + s), ph, wd)) {
+    const int n = chunks<CG, MODE>(w), len = chunk_stages<CG, MODE>(w);
+    for (int c = 0; ok && c < n; ++c, ++handed) {
+      const uint32_t b = handed & 1, aph = (handed >> 1) & 1;
+      if (!wait_spin<true>(bar(BAR_ACC_EMPTY + b), aph ^ 1, wd)) {
         ok = false;
         break;
       }
-      const uint32_t a_addr = sbase + s * sbytes, b_addr = a_addr + ksub<CG>() * A_BLOCK;
+      tc_fence_after_sync();
+      const uint32_t d = tmem + b * BN_MAX;
+      const int first = w.s0 + c * len, end = min(first + len, w.s1);
+      for (int st = first; st < end; ++st) {
+        if (!wait_spin<true>(bar(BAR_FULL + s), ph, wd)) {
+          ok = false;
+          break;
+        }
+        const uint32_t a_addr = sbase + s * sbytes, b_addr = a_addr + ksub<CG>() * A_BLOCK;
 #pragma unroll
-      for (int kk = 0; kk < ksub<CG>() * (BK / UMMA_K); ++kk) {
-        const int blk = kk / (BK / UMMA_K), kin = kk % (BK / UMMA_K);
-        const uint32_t aa = a_addr + blk * A_BLOCK + kin * a_step;
-        const uint32_t bb = b_addr + blk * b_block + kin * b_step;
-        const uint64_t ad = a_mn ? sdesc_mnmajor_sw128(aa) : sdesc_kmajor_sw128(aa);
-        const uint64_t bd = b_mn ? sdesc_mnmajor_sw128(bb) : sdesc_kmajor_sw128(bb);
-        const uint32_t acc = (st != w.s0 || kk != 0) ? 1u : 0u;
-        if constexpr (CG == 1)
-          umma_bf16(d, ad, bd, idesc, acc);
-        else
-          umma_bf16_pair(d, ad, bd, idesc, acc);
+        for (int kk = 0; kk < ksub<CG>() * (BK / UMMA_K); ++kk) {
+          const int blk = kk / (BK / UMMA_K), kin = kk % (BK / UMMA_K);
+          const uint32_t aa = a_addr + blk * A_BLOCK + kin * a_step;
+          const uint32_t bb = b_addr + blk * b_block + kin * b_step;
+          const uint64_t ad = a_mn ? sdesc_mnmajor_sw128(aa) : sdesc_kmajor_sw128(aa);
+          const uint64_t bd = b_mn ? sdesc_mnmajor_sw128(bb) : sdesc_kmajor_sw128(bb);
+          const uint32_t acc = (st != first || kk != 0) ? 1u : 0u;
+          if constexpr (CG == 1)
+            umma_bf16(d, ad, bd, idesc, acc);
+          else
+            umma_bf16_pair(d, ad, bd, idesc, acc);
+        }
+        issued = true;
+        commit(bar(BAR_EMPTY + s));
+        if (++s == stages) {
+          s = 0;
+          ph ^= 1;
+        }
       }
-      issued = true;
-      commit(bar(BAR_EMPTY + s));
-      if (++s == stages) {
-        s = 0;
-        ph ^= 1;
+      if (!ok) break;
+      if (end > first) {
+        commit(bar(BAR_ACC_FULL + b));
+      } else {   // nothing to sum: signal the accumulator barriers directly
+        for (int r = 0; r < CG; ++r) {
+          if constexpr (CG == 1)
+            mbar_arrive(bar(BAR_ACC_FULL + b));
+          else
+            mbar_arrive_cluster(mapa_shared(bar(BAR_ACC_FULL + b), r));
+        }
       }
     }
     if (!ok) break;
-    if (w.s1 > w.s0) {
-      commit(bar(BAR_ACC_FULL + b));
-    } else {   // nothing to sum: signal the accumulator barriers directly
-      for (int r = 0; r < CG; ++r) {
-        if constexpr (CG == 1)
-          mbar_arrive(bar(BAR_ACC_FULL + b));
-        else
-          mbar_arrive_cluster(mapa_shared(bar(BAR_ACC_FULL + b), r));
-      }
-    }
   }
   if (issued) {
     // Every MMA issued has finished once this arrives (also after an abort).
@@ -307,159 +386,236 @@ __device__ __forceinline__ float exp_diff(float x, float y) {
   return r;
 }
 
+// What an epilogue warp knows of its place, and its side of the hand-overs.
+template <int CG>
+struct Epilogue {
+  uint32_t sbase, tmem, rank;
+  int lane;
+  int e;        // 0 .. 7
+  int q;        // the TMEM lane quarter that the warp may read
+  int hf;       // it takes the unit's column blocks of 64 (or 32) b with b % 2 == hf
+  uint8_t* out;
+  uint32_t handed;
+
+  __device__ __forceinline__ Epilogue(uint32_t sbase_, uint8_t* smem, uint32_t tmem_, uint32_t rank_,
+                                      int warp)
+      : sbase(sbase_), tmem(tmem_), rank(rank_), lane(threadIdx.x & 31), e(warp - WARP_EPI0),
+        q(warp & 3), hf((warp - WARP_EPI0) / 4), out(smem + OFF_OUT + (warp - WARP_EPI0) * OUT_BYTES),
+        handed(0) {}
+  __device__ __forceinline__ uint32_t bar(int i) const { return sbase + OFF_BAR + 8 * i; }
+  // Waits for the next accumulator; its address for this warp's lanes.
+  __device__ __forceinline__ bool take(const Watchdog& wd, uint32_t* tacc) const {
+    if (!warp_wait_spin(bar(BAR_ACC_FULL + (handed & 1)), (handed >> 1) & 1, wd)) return false;
+    tc_fence_after_sync();
+    *tacc = tmem + (static_cast<uint32_t>(32 * q) << 16) + (handed & 1) * BN_MAX;
+    return true;
+  }
+  // Gives it back to the MMA thread (of the pair's even CTA).
+  __device__ __forceinline__ void release() {
+    tc_fence_before_sync();
+    __syncwarp();
+    if (lane == 0) {
+      const uint32_t b = bar(BAR_ACC_EMPTY + (handed & 1));
+      if (CG == 1 || rank == 0)
+        mbar_arrive(b);
+      else
+        mbar_arrive_cluster(mapa_shared(b, 0));
+    }
+    ++handed;
+  }
+  // Rows of 128 bytes with the TMA's 128-byte swizzle: 16-byte piece c of this lane's row.
+  __device__ __forceinline__ uint4* piece(int c) const {
+    return reinterpret_cast<uint4*>(out + lane * 128 + ((c ^ (lane & 7)) << 4));
+  }
+  // The warp's block may be written again: its last store has read it.
+  __device__ __forceinline__ void reuse() const {
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+  }
+  __device__ __forceinline__ void store(const CUtensorMap* map, int x, int y, int z, bool add) const {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      if (add)
+        tma_add_3d(map, smem_addr(out), x, y, z);
+      else
+        tma_store_3d(map, smem_addr(out), x, y, z);
+      bulk_commit();
+    }
+  }
+};
+
+// 64 fp32 values of a row in bf16 to the warp's block.
+template <int CG>
+__device__ __forceinline__ void put_bf16(const Epilogue<CG>& w, const float (&lo)[32],
+                                         const float (&hi)[32]) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const float* a = c < 4 ? lo : hi;
+    const int o = 8 * (c & 3);
+    *w.piece(c) = make_uint4(pack_bf16x2(a[o], a[o + 1]), pack_bf16x2(a[o + 2], a[o + 3]),
+                             pack_bf16x2(a[o + 4], a[o + 5]), pack_bf16x2(a[o + 6], a[o + 7]));
+  }
+}
+
+// LSE and GRAD: a thread has one row and, in registers, the logits of its warp's
+// column blocks, two of 64.
 template <int CG, int MODE>
-__device__ __forceinline__ void epilogue(const Params& p, uint32_t sbase, uint8_t* smem,
-                                         uint32_t tmem, uint32_t rank, int warp, int count,
-                                         const Watchdog& wd) {
-  const int lane = threadIdx.x & 31;
-  const int e = warp - WARP_EPI0;
-  const int q = warp & 3;         // the TMEM lane quarter that this warp may read
-  const int hf = e / 4;           // it takes the unit's column blocks b with b % 2 == hf
-  auto bar = [&](int i) { return sbase + OFF_BAR + 8 * i; };
-  const int cluster = blockIdx.x / CG, clusters = gridDim.x / CG;
-  uint8_t* out = smem + OFF_OUT + e * OUT_BYTES;
-  const uint32_t out_row = lane * 128, swz = lane & 7;   // 128-byte swizzle, as the TMA reads it
-  float top = -INFINITY, sum = 0.0f;                     // LSE
+__device__ __forceinline__ void epilogue_logits(const Params& p, uint32_t sbase, uint8_t* smem,
+                                                uint32_t tmem, uint32_t rank, int warp, int count,
+                                                const Watchdog& wd) {
+  Epilogue<CG> me(sbase, smem, tmem, rank, warp);
+  const Walk walk = make_walk<CG>(p, count);
+  float top = -INFINITY, sum = 0.0f;
   int row = 0;
+  bool any = false;
   auto flush = [&](int slot) {
     if (row < count) p.part[static_cast<int64_t>(slot) * p.part_stride + row] = make_float2(top, sum);
     top = -INFINITY;
     sum = 0.0f;
   };
-  bool any = false;
   Unit w;
-  for (int i = 0; next_unit<CG>(p, count, cluster, clusters, i, w); ++i) {
-    const Job& job = *w.job;
+  for (int i = 0; next_unit<CG>(p, count, walk, i, w); ++i) {
     any = true;
     const int part0 = w.m0 + static_cast<int>(rank) * BM;   // this CTA's first row
-    row = part0 + 32 * q + lane;
-    const int m = job.m < 0 ? count : job.m;
-    const int width = min(p.bn, (MODE == SUMS ? job.n : p.cols) - w.n0);   // valid columns
-    const int step = MODE == LSE || job.out == OUT_ADD ? EPI_N : 2 * EPI_N;   // columns of a block
-    const int blocks = part0 < m ? (width + step - 1) / step : 0;
-    int target = -1;
+    row = part0 + 32 * me.q + me.lane;
+    const int width = part0 < count ? min(p.bn, p.cols - w.n0) : 0;   // valid columns
+    int target = -1;   // the target's column in this tile, if in it
     float lse = 0.0f, grad = 0.0f;
-    if (MODE != SUMS && row < count) {
-      target = p.target[row] - p.col0 - w.n0;   // the target's column in this tile, if in it
+    if (row < count) {
+      target = p.target[row] - p.col0 - w.n0;
       if (MODE == GRAD) {
         lse = p.lse[row];
         grad = p.grad[row];
       }
     }
-    const uint32_t b = i & 1, aph = (i >> 1) & 1;
-    auto release = [&]() {
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) {
-        if (CG == 1 || rank == 0)
-          mbar_arrive(bar(BAR_ACC_EMPTY + b));
-        else
-          mbar_arrive_cluster(mapa_shared(bar(BAR_ACC_EMPTY + b), 0));
+    // block k of 32 columns: the halves of the warp's 64-column blocks
+    auto column = [&](int k) { return 128 * (k / 2) + 64 * me.hf + 32 * (k % 2); };
+    float z[4][32];
+    bool ok = true;
+    const int n = chunks<CG, MODE>(w);
+    for (int c = 0; c < n; ++c) {
+      uint32_t tacc;
+      if (!me.take(wd, &tacc)) {
+        ok = false;
+        break;
       }
-    };
-    if (!warp_wait_spin(bar(BAR_ACC_FULL + b), aph, wd)) break;
-    tc_fence_after_sync();
-    const uint32_t tacc = tmem + (static_cast<uint32_t>(32 * q) << 16) + b * BN_MAX;
-    if (hf >= blocks) release();
-    for (int j = hf; j < blocks; j += 2) {
-      uint32_t a0[32];
-      if constexpr (MODE == LSE) {
-        tmem_ld_32x32b_x32(tacc + j * EPI_N, a0);
-        tmem_wait_ld();
-        if (j + 2 >= blocks) release();
-        const int valid = width - j * EPI_N;
-        float most = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (column(k) >= width) continue;
+#pragma unroll
+        for (int x0 = 0; x0 < 32; x0 += 16) {
+          uint32_t part[16];
+          tmem_ld_32x32b_x16(tacc + column(k) + x0, part);
+          tmem_wait_ld();
+#pragma unroll
+          for (int x = 0; x < 16; ++x)
+            z[k][x0 + x] = c == 0 ? __uint_as_float(part[x]) : z[k][x0 + x] + __uint_as_float(part[x]);
+        }
+      }
+      me.release();
+    }
+    if (!ok) break;
+    if constexpr (MODE == LSE) {
+      float next = top;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (column(k) >= width) continue;
+        const int valid = width - column(k);
+        const int hit = target - column(k);
+        if (hit >= 0 && hit < 32) {
+          float at = 0.0f;
+#pragma unroll
+          for (int x = 0; x < 32; ++x) at = x == hit ? z[k][x] : at;
+          p.target_logit[row] = at;
+        }
 #pragma unroll
         for (int x = 0; x < 32; ++x) {
-          const float z = x < valid ? __uint_as_float(a0[x]) : -INFINITY;
-          if (target == j * EPI_N + x) p.target_logit[row] = __uint_as_float(a0[x]);
-          a0[x] = __float_as_uint(z);
-          most = fmaxf(most, z);
+          if (x >= valid) z[k][x] = -INFINITY;
+          next = fmaxf(next, z[k][x]);
         }
-        const float next = fmaxf(top, most);
-        const float base = next == -INFINITY ? 0.0f : next;   // nothing finite yet: all terms 0
+      }
+      const float base = next == -INFINITY ? 0.0f : next;   // nothing finite yet: all terms 0
+      sum *= exp_diff(top, base);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (column(k) >= width) continue;
         float add = 0.0f;
 #pragma unroll
-        for (int x = 0; x < 32; ++x) add += exp_diff(__uint_as_float(a0[x]), base);
-        sum = fmaf(sum, exp_diff(top, base), add);
-        top = next;
-        continue;
+        for (int x = 0; x < 32; ++x) add += exp_diff(z[k][x], base);
+        sum += add;
       }
-      const bool has_acc = w.s1 > w.s0;
-      if (MODE == SUMS && job.out == OUT_ADD) {
-        if (has_acc) {
-          tmem_ld_32x32b_x32(tacc + j * EPI_N, a0);
-          tmem_wait_ld();
-        } else {
+      top = next;
+      if (!p.carry) flush(2 * w.nb + me.hf);
+    } else {
 #pragma unroll
-          for (int x = 0; x < 32; ++x) a0[x] = 0u;
+      for (int k = 0; k < 4; k += 2) {
+        if (column(k) >= width) continue;
+        // Rows that are not there (or have no gradient) and columns past the
+        // vocabulary are 0: the products after this one run over them.
+        const int valid = grad != 0.0f ? width - column(k) : 0;
+        const int hit = target - column(k);
+        auto gradient = [&](float logit, int x) {
+          float pr = exp_diff(logit, lse);
+          if (x == hit) pr -= 1.0f;
+          return x < valid ? pr * grad : 0.0f;
+        };
+        const bool second = column(k + 1) < width;   // else its z holds nothing
+#pragma unroll
+        for (int x = 0; x < 32; ++x) {
+          z[k][x] = gradient(z[k][x], x);
+          z[k + 1][x] = second ? gradient(z[k + 1][x], 32 + x) : 0.0f;
         }
-        if (j + 2 >= blocks) release();
-        if (lane == 0) bulk_wait_read<0>();
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(out + out_row + ((c ^ swz) << 4)) =
-              make_uint4(a0[4 * c], a0[4 * c + 1], a0[4 * c + 2], a0[4 * c + 3]);
-      } else {
-        uint32_t a1[32];
-        if (has_acc) {
-          tmem_ld_32x32b_x32(tacc + 2 * j * EPI_N, a0);
-          tmem_ld_32x32b_x32(tacc + (2 * j + 1) * EPI_N, a1);
-          tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int x = 0; x < 32; ++x) a0[x] = a1[x] = 0u;
-        }
-        if (j + 2 >= blocks) release();
-        if constexpr (MODE == GRAD) {
-          // Rows that are not there (or have no gradient) and columns past
-          // the vocabulary are 0: the products after this one run over them.
-          const int valid = grad != 0.0f ? width - 2 * j * EPI_N : 0;
-          const int hit = target - 2 * j * EPI_N;
-          auto gradient = [&](uint32_t acc, int x) {
-            float pr = exp_diff(__uint_as_float(acc), lse);
-            if (x == hit) pr -= 1.0f;
-            return x < valid ? pr * grad : 0.0f;
-          };
-#pragma unroll
-          for (int x = 0; x < 32; ++x) {
-            a0[x] = __float_as_uint(gradient(a0[x], x));
-            a1[x] = __float_as_uint(gradient(a1[x], 32 + x));
-          }
-        }
-        if (lane == 0) bulk_wait_read<0>();   // this warp's previous block has been read
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint32_t* a = c < 4 ? a0 : a1;
-          const int o = 8 * (c & 3);
-          uint4 v;
-          v.x = pack_bf16x2(__uint_as_float(a[o]), __uint_as_float(a[o + 1]));
-          v.y = pack_bf16x2(__uint_as_float(a[o + 2]), __uint_as_float(a[o + 3]));
-          v.z = pack_bf16x2(__uint_as_float(a[o + 4]), __uint_as_float(a[o + 5]));
-          v.w = pack_bf16x2(__uint_as_float(a[o + 6]), __uint_as_float(a[o + 7]));
-          *reinterpret_cast<uint4*>(out + out_row + ((c ^ swz) << 4)) = v;
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        const int x = w.n0 + j * step, y = job.d_row0 + part0 + 32 * q;
-        if (MODE == SUMS && job.add)
-          tma_add_3d(&job.tmD, smem_addr(out), x, y, w.cut);
-        else
-          tma_store_3d(&job.tmD, smem_addr(out), x, y, w.cut);
-        bulk_commit();
+        me.reuse();
+        put_bf16(me, z[k], z[k + 1]);
+        me.store(&w.job->tmD, w.n0 + column(k), part0 + 32 * me.q, 0, false);
       }
     }
-    if (MODE == LSE && !p.carry) flush(2 * w.nb + hf);
   }
-  if (MODE == LSE && p.carry && any) flush(2 * cluster + hf);
-  if (MODE != LSE) {
-    if (lane == 0) bulk_wait_read<0>();
-    __syncwarp();
+  if (MODE == LSE && p.carry && any) flush(2 * walk.cluster + me.hf);
+  if (MODE == GRAD) me.reuse();
+}
+
+// SUMS: dx's tiles leave in fp32 (stored, or added to the pieces before), dweight's
+// in bf16.
+template <int CG>
+__device__ __forceinline__ void epilogue_sums(const Params& p, uint32_t sbase, uint8_t* smem,
+                                              uint32_t tmem, uint32_t rank, int warp, int count,
+                                              const Watchdog& wd) {
+  Epilogue<CG> me(sbase, smem, tmem, rank, warp);
+  const Walk walk = make_walk<CG>(p, count);
+  Unit w;
+  for (int i = 0; next_unit<CG>(p, count, walk, i, w); ++i) {
+    const Job& job = *w.job;
+    const int part0 = w.m0 + static_cast<int>(rank) * BM;   // this CTA's first row
+    const bool f32 = job.out == OUT_ADD;
+    const int step = f32 ? EPI_N : 2 * EPI_N;   // columns of a block
+    const int blocks = part0 < (job.m < 0 ? count : job.m)
+                           ? (min(p.bn, job.n - w.n0) + step - 1) / step : 0;
+    const bool has_acc = w.s1 > w.s0;
+    uint32_t tacc;
+    if (!me.take(wd, &tacc)) break;
+    if (me.hf >= blocks) me.release();
+    for (int j = me.hf; j < blocks; j += 2) {
+      uint32_t a0[32] = {}, a1[32] = {};
+      if (has_acc) {
+        tmem_ld_32x32b_x32(tacc + j * step, a0);
+        if (!f32) tmem_ld_32x32b_x32(tacc + j * step + EPI_N, a1);
+        tmem_wait_ld();
+      }
+      if (j + 2 >= blocks) me.release();
+      me.reuse();
+      if (f32) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *me.piece(c) = make_uint4(a0[4 * c], a0[4 * c + 1], a0[4 * c + 2], a0[4 * c + 3]);
+      } else {
+        put_bf16(me, reinterpret_cast<const float(&)[32]>(a0), reinterpret_cast<const float(&)[32]>(a1));
+      }
+      me.store(&job.tmD, w.n0 + j * step, job.d_row0 + part0 + 32 * me.q, w.cut, job.add);
+    }
   }
+  me.reuse();
 }
 
 // ------------------------------------------------------------ product kernel
@@ -518,9 +674,12 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
   if (warp == WARP_A || warp == WARP_B) {
     if (lane == 0) producer<CG>(p, sbase, rank, warp == WARP_A, count, wd);
   } else if (warp == WARP_MMA) {
-    if (lane == 0 && rank == 0) mma_issuer<CG>(p, sbase, tmem, rank, count, wd);
+    if (lane == 0 && rank == 0) mma_issuer<CG, MODE>(p, sbase, tmem, rank, count, wd);
   } else {
-    epilogue<CG, MODE>(p, sbase, smem, tmem, rank, warp, count, wd);
+    if constexpr (MODE == SUMS)
+      epilogue_sums<CG>(p, sbase, smem, tmem, rank, warp, count, wd);
+    else
+      epilogue_logits<CG, MODE>(p, sbase, smem, tmem, rank, warp, count, wd);
   }
   __syncwarp();
   tc_fence_before_sync();
@@ -546,7 +705,8 @@ struct PackParams {
   int rows, cols, vocab;
   int wide;                   // x's rows allow 16-byte accesses
   int chunk;                  // rows of a block, at most PACK_THREADS
-  uint16_t* packed;           // T x H
+  uint16_t* packed;           // T x H, `pitch` elements between rows
+  int64_t pitch;
   int* place;                 // [row]: its packed row, -1 if not counted
   int* target_out;            // [packed row]
   int* count;
@@ -638,7 +798,7 @@ __global__ void __launch_bounds__(PACK_THREADS) pack_kernel(const __grid_constan
         w.w = src[6] | static_cast<uint32_t>(src[7]) << 16;
       }
     }
-    *reinterpret_cast<uint4*>(p.packed + static_cast<int64_t>(to >= 0 ? to : -1 - to) * p.cols + c) = w;
+    *reinterpret_cast<uint4*>(p.packed + static_cast<int64_t>(to >= 0 ? to : -1 - to) * p.pitch + c) = w;
   }
 }
 
@@ -659,68 +819,107 @@ struct JoinParams {
 
 constexpr int JOIN_ROWS = 32, JOIN_LANES = 32;
 
-// lse and loss of 32 rows a block, from the partial maxima and sums in slot
-// order; the block that finishes last adds the blocks' loss sums in block
-// order, so the mean's bits do not depend on which one that is.
+// (top, sum) and (v.x, v.y) as one maximum and sum.
+__device__ __forceinline__ void join_pair(float& top, float& sum, float2 v) {
+  const float next = fmaxf(top, v.x), base = next == -INFINITY ? 0.0f : next;
+  sum = sum * exp_diff(top, base) + v.y * exp_diff(v.x, base);
+  top = next;
+}
+
+// lse and loss of 32 rows a block, from the partial maxima and sums: a warp
+// reads a slot's 32 rows at once, JOIN_LANES slots apart; then a warp joins the
+// lanes of one row. The order is fixed. The block that finishes last adds the
+// blocks' loss sums in block order, so the mean's bits do not depend on which
+// one that is.
 __global__ void __launch_bounds__(JOIN_ROWS* JOIN_LANES)
     join_kernel(const __grid_constant__ JoinParams p) {
-  __shared__ float2 box[JOIN_LANES][JOIN_ROWS];
-  __shared__ float sums[JOIN_LANES];
-  __shared__ bool last;
+  __shared__ float2 box[JOIN_LANES][JOIN_ROWS + 1];
+  __shared__ float sums[JOIN_LANES], logit[JOIN_ROWS];
+  __shared__ bool last, counted[JOIN_ROWS];
   grid_dependency_wait();
   grid_launch_dependents();
   const int x = threadIdx.x % JOIN_ROWS, lane = threadIdx.x / JOIN_ROWS;
-  const int row = blockIdx.x * JOIN_ROWS + x;
-  const int at = row < p.rows ? p.place[row] : -1;
-  float top = -INFINITY, sum = 0.0f;
-  if (at >= 0) {
-#pragma unroll 4
-    for (int s = lane; s < p.slots; s += JOIN_LANES) {
-      const float2 v = p.part[s * p.part_stride + at];
-      const float next = fmaxf(top, v.x), base = next == -INFINITY ? 0.0f : next;
-      sum = sum * exp_diff(top, base) + v.y * exp_diff(v.x, base);
-      top = next;
+  {
+    const int row = blockIdx.x * JOIN_ROWS + x;
+    const int at = row < p.rows ? p.place[row] : -1;
+    float top = -INFINITY, sum = 0.0f;
+    if (lane == 0) {
+      counted[x] = at >= 0;
+      logit[x] = at >= 0 ? p.target_logit[at] : 0.0f;
     }
+    if (at >= 0) {
+      constexpr int AHEAD = 8;   // loads in flight
+      for (int s0 = lane; s0 < p.slots; s0 += AHEAD * JOIN_LANES) {
+        float2 v[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+          const int s = s0 + k * JOIN_LANES;
+          v[k] = s < p.slots ? p.part[s * p.part_stride + at] : make_float2(-INFINITY, 0.0f);
+        }
+        float next = top;
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) next = fmaxf(next, v[k].x);
+        const float base = next == -INFINITY ? 0.0f : next;
+        sum *= exp_diff(top, base);
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) sum = fmaf(v[k].y, exp_diff(v[k].x, base), sum);
+        top = next;
+      }
+    }
+    box[lane][x] = make_float2(top, sum);
   }
-  box[lane][x] = make_float2(top, sum);
   __syncthreads();
-  float loss = 0.0f;
-  if (lane == 0) {
-    for (int l = 1; l < JOIN_LANES; ++l) {
-      const float2 v = box[l][x];
-      const float next = fmaxf(top, v.x), base = next == -INFINITY ? 0.0f : next;
-      sum = sum * exp_diff(top, base) + v.y * exp_diff(v.x, base);
-      top = next;
-    }
+  const int row = blockIdx.x * JOIN_ROWS + lane;   // this warp's row
+  const float2 mine = box[x][lane];
+  float top = mine.x, sum = mine.y, loss = 0.0f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    // the lower lane's pair first, on both sides, so that both get the same bits
+    float2 a = make_float2(top, sum);
+    float2 b = make_float2(__shfl_xor_sync(0xffffffffu, top, o), __shfl_xor_sync(0xffffffffu, sum, o));
+    const bool low = (x & o) == 0;
+    top = low ? a.x : b.x;
+    sum = low ? a.y : b.y;
+    join_pair(top, sum, low ? b : a);
+  }
+  if (x == 0) {
     if (row < p.rows) {
-      const float rest = at >= 0 ? logf(sum) : 0.0f;
-      loss = at >= 0 ? (top - p.target_logit[at]) + rest : 0.0f;
-      p.lse[row] = at >= 0 ? top + rest : 0.0f;
+      const float rest = counted[lane] ? logf(sum) : 0.0f;
+      loss = counted[lane] ? (top - logit[lane]) + rest : 0.0f;
+      p.lse[row] = counted[lane] ? top + rest : 0.0f;
       p.loss[row] = loss;
     }
+    sums[lane] = loss;
+  }
+  __syncthreads();
+  if (lane == 0) {
+    loss = sums[x];
+#pragma unroll
     for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
   }
   if (!p.mean) return;
-  if (threadIdx.x == 0) {
-    p.block_sum[blockIdx.x] = loss;
+  if (gridDim.x > 1) {
+    if (threadIdx.x == 0) {
+      p.block_sum[blockIdx.x] = loss;
+      __threadfence();
+      last = atomicAdd(p.done, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!last) return;
     __threadfence();
-    last = atomicAdd(p.done, 1u) == gridDim.x - 1;
+    loss = 0.0f;
+    for (int b = threadIdx.x; b < static_cast<int>(gridDim.x); b += blockDim.x)
+      loss += __ldcg(p.block_sum + b);
+    for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
+    if (x == 0) sums[lane] = loss;
+    __syncthreads();
+    loss = 0.0f;
+    for (int l = 0; l < JOIN_LANES; ++l) loss += sums[l];
   }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  float s = 0.0f;
-  for (int b = threadIdx.x; b < static_cast<int>(gridDim.x); b += blockDim.x)
-    s += __ldcg(p.block_sum + b);
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (x == 0) sums[lane] = s;
-  __syncthreads();
   if (threadIdx.x == 0) {
-    s = 0.0f;
-    for (int l = 0; l < JOIN_LANES; ++l) s += sums[l];
     const int n = *p.count;
     const float share = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
-    p.mean[0] = s * share;
+    p.mean[0] = loss * share;
     p.mean[1] = share;
     *p.done = 0u;
   }
