@@ -256,6 +256,7 @@ ce::Params product_params(const gemm_ws* h, const Plan& q, uint8_t* ws, const Ti
   p.bn = t.bn;
   p.stages = ring_stages(t);
   p.a_rows = ce::BM;
+  p.cut_k = T <= ce::BM ? ce::CUT_K_FEW : ce::CUT_K;
   p.count = reinterpret_cast<const int*>(ws + q.count);
   p.target = reinterpret_cast<const int*>(ws + q.target);
   p.part_stride = T;

@@ -62,10 +62,14 @@ constexpr uint32_t SMEM_BYTES = OFF_ABORT + 4 + 1024;   // + slack to align the 
 static_assert(SMEM_BYTES <= 232448, "exceeds the 227 KiB per-CTA shared memory");
 // The tensor cores cut off what an addition to the accumulator shifts out, so a
 // logit that grows over a long K ends too near to zero: by 5e-6 of lse with 8192
-// hidden, 20 times fp32 sums' error. So the logits' sums are cut into 512 of K
-// each, which the epilogue adds in registers with rounding. (The gradients'
-// products, which end in bf16, need none of it.)
-constexpr int CHUNK_K = 512;
+// hidden, and the loss of a token that the model is nearly sure of by more than
+// that. So the logits' sums are cut, and the epilogue adds the cuts in registers
+// with rounding. Each cut costs the tensor cores the time in which the accumulator is
+// read (0.28 us for 256 x 256: 4096 x 4096 over 131072 takes 2.36 ms in one cut,
+// 2.44 in cuts of 1024, 2.58 in cuts of 512), so it is 1024 of K, an error below
+// 1e-6; and 256 where few tokens leave them waiting for memory anyway. (The
+// gradients' products, which end in bf16, need none of it.)
+constexpr int CUT_K = 1024, CUT_K_FEW = 256;
 constexpr float LOG2E = 1.4426950408889634f;
 
 enum Mode { LSE = 0, GRAD = 1, SUMS = 2 };
@@ -107,6 +111,7 @@ struct Params {
   float* target_logit;       // [row]
   float2* part;              // [slot][row]: maximum and sum of exponentials
   int64_t part_stride;
+  int cut_k;                 // K of one accumulator, a multiple of 128 (the same in both)
   int carry;                 // one row of tiles: a CTA keeps its sums over its tiles
   const float *lse, *grad;   // [row]: lse, and g
   uint32_t* status;
@@ -212,13 +217,14 @@ __device__ __forceinline__ bool next_unit(const Params& p, int count, const Walk
 // Ring stages that one accumulator takes before it is handed over, and how often
 // a unit's is.
 template <int CG, int MODE>
-__device__ __forceinline__ int chunk_stages(const Unit& w) {
-  return MODE == SUMS ? max(w.s1 - w.s0, 1) : CHUNK_K / (BK * ksub<CG>());
+__device__ __forceinline__ int cut_stages(const Params& p, const Unit& w) {
+  return MODE == SUMS ? max(w.s1 - w.s0, 1) : p.cut_k / (BK * ksub<CG>());
 }
 template <int CG, int MODE>
-__device__ __forceinline__ int chunks(const Unit& w) {
+__device__ __forceinline__ int cuts(const Params& p, const Unit& w) {
   if (MODE == SUMS) return 1;
-  return (w.s1 - w.s0 + chunk_stages<CG, MODE>(w) - 1) / chunk_stages<CG, MODE>(w);
+  const int n = cut_stages<CG, MODE>(p, w);
+  return (w.s1 - w.s0 + n - 1) / n;
 }
 
 // ------------------------------------------------------------ producers
@@ -315,7 +321,7 @@ __device__ __forceinline__ void mma_issuer(const Params& p, uint32_t sbase, uint
     const uint32_t a_step = a_mn ? UMMA_K * 128 : UMMA_K * 2;
     const uint32_t b_step = b_mn ? UMMA_K * 128 : UMMA_K * 2;
     bool ok = true;
-    const int n = chunks<CG, MODE>(w), len = chunk_stages<CG, MODE>(w);
+    const int n = cuts<CG, MODE>(p, w), len = cut_stages<CG, MODE>(p, w);
     for (int c = 0; ok && c < n; ++c, ++handed) {
       const uint32_t b = handed & 1, aph = (handed >> 1) & 1;
       if (!wait_spin<true>(bar(BAR_ACC_EMPTY + b), aph ^ 1, wd)) {
@@ -493,7 +499,7 @@ __device__ __forceinline__ void epilogue_logits(const Params& p, uint32_t sbase,
     auto column = [&](int k) { return 128 * (k / 2) + 64 * me.hf + 32 * (k % 2); };
     float z[4][32];
     bool ok = true;
-    const int n = chunks<CG, MODE>(w);
+    const int n = cuts<CG, MODE>(p, w);
     for (int c = 0; c < n; ++c) {
       uint32_t tacc;
       if (!me.take(wd, &tacc)) {
