@@ -55,7 +55,7 @@ struct Plan {
   int64_t slots;      // partial maxima and sums a row
   int64_t piece, pieces;
   int64_t cuts;
-  int64_t pitch;      // of the packed rows of x
+  int64_t pitch, rows;   // of the packed rows of x; rows of G, too
   int64_t blocks;     // of the joining kernel
   // byte offsets in the workspace
   int64_t packed, place, target, count, logit, part, block_sum, lse, grad, g, sums_at, bytes;
@@ -71,7 +71,10 @@ Plan make_plan(const gemm_ws* h, int64_t T, int64_t H, int64_t V, bool backward)
     return here;
   };
   q.pitch = round_up(H, 64);   // whole 128-byte lines: x's boxes never straddle one
-  q.packed = take(T * q.pitch * 2);
+  // Whole tiles of rows (they may hold anything past the counted ones): the TMA
+  // fills rows that are not there more slowly than it fetches rows that are.
+  q.rows = T > ce::BM ? round_up(T, 2 * ce::BM) : ce::BM;
+  q.packed = take(q.rows * q.pitch * 2);
   q.place = take(T * 4);
   q.target = take(T * 4);
   q.count = take(4);
@@ -103,7 +106,7 @@ Plan make_plan(const gemm_ws* h, int64_t T, int64_t H, int64_t V, bool backward)
     if (q.cuts > kMaxCuts) q.cuts = kMaxCuts;
     q.lse = take(T * 4);
     q.grad = take(T * 4);
-    q.g = take(T * q.piece * 2);
+    q.g = take(q.rows * q.piece * 2);
     q.sums_at = take(q.cuts * T * H * 4);
   }
   q.bytes = at;
@@ -135,9 +138,9 @@ bool operand(gemm_ws* h, CUtensorMap* m, const void* ptr, int64_t inner, int64_t
   return encode(h, m, ptr, false, inner, rows, 1, ld, ld * rows, 64, mn ? 64 : box_rows);
 }
 
-// Rows of x in a box: fewer than 128 tokens come in a box of their own size. The
-// TMA fills rows that are not there more slowly than it fetches rows that are: one
-// token over 131072 x 4096 took 238 us with boxes of 128 rows, 61 tokens 173.
+// Rows of x in a box: fewer than 128 tokens come in a box of their own size. (One
+// token over 131072 x 4096 took 238 us with boxes of 128 rows, of which 127 were
+// not there; now 172.)
 int box_rows(int64_t T) { return static_cast<int>(T < ce::BM ? T : ce::BM); }
 
 template <typename P>
@@ -239,7 +242,8 @@ ce::PackParams pack_params(const Plan& q, uint8_t* ws, const uint16_t* x, int64_
   p.cols = static_cast<int>(H);
   p.vocab = static_cast<int>(V);
   p.wide = !odd(x, 16) && ldx % 8 == 0;
-  int64_t chunk = ceil_div(T, int64_t{8} * num_sms);
+  p.padded = static_cast<int>(round_up(T, 128));
+  int64_t chunk = ceil_div(p.padded, int64_t{8} * num_sms);
   p.chunk = static_cast<int>(chunk < ce::PACK_THREADS ? chunk : ce::PACK_THREADS);
   p.packed = reinterpret_cast<uint16_t*>(ws + q.packed);
   p.pitch = q.pitch;
@@ -343,7 +347,7 @@ int gemm_ws_linear_ce(gemm_ws_t* h, const uint16_t* x, int64_t ldx, const uint16
   p.target_logit = pack.target_logit;
   p.part = reinterpret_cast<float2*>(ws + q.part);
   p.carry = q.carry;
-  if (!operand(h, &job.tmA, pack.packed, H, T, q.pitch, false, p.a_rows) ||
+  if (!operand(h, &job.tmA, pack.packed, H, q.rows, q.pitch, false, p.a_rows) ||
       !operand(h, &job.tmB, weight, H, V, ldw, false, q.logits.bn / q.logits.cg))
     return GEMM_WS_ERR_CUDA;
 
@@ -363,7 +367,7 @@ int gemm_ws_linear_ce(gemm_ws_t* h, const uint16_t* x, int64_t ldx, const uint16
   join.done = h->work + 3;
 
   DeviceGuard guard(h->device);
-  rc = launch(h, ce::pack_kernel, ceil_div(T, pack.chunk), ce::PACK_THREADS, 0, 1, s, pack);
+  rc = launch(h, ce::pack_kernel, ceil_div(pack.padded, pack.chunk), ce::PACK_THREADS, 0, 1, s, pack);
   if (rc == GEMM_WS_OK)
     rc = launch_product<ce::LSE>(
         h, q.logits, ceil_div(T, ce::BM * q.logits.cg) * ceil_div(V, q.logits.bn), p, s);
@@ -431,7 +435,7 @@ int gemm_ws_linear_ce_backward(gemm_ws_t* h, const uint16_t* x, int64_t ldx,
   const int b_rows = q.sums.bn / q.sums.cg;
   ce::Job* jx = dx ? &ps.job[ps.jobs++] : nullptr;
   ce::Job* jw = dweight ? &ps.job[ps.jobs++] : nullptr;
-  bool ok = operand(h, &jg.tmA, pack.packed, H, T, q.pitch, false, pg.a_rows) &&
+  bool ok = operand(h, &jg.tmA, pack.packed, H, q.rows, q.pitch, false, pg.a_rows) &&
             operand(h, &jg.tmB, weight, H, V, ldw, false, q.logits.bn / q.logits.cg);
   if (jx) {
     jx->m = -1;
@@ -448,13 +452,13 @@ int gemm_ws_linear_ce_backward(gemm_ws_t* h, const uint16_t* x, int64_t ldx,
     jw->a_mn = jw->b_mn = 1;
     jw->splits = 1;
     jw->out = ce::OUT_BF16;
-    ok = ok && operand(h, &jw->tmB, pack.packed, H, T, q.pitch, true, b_rows) &&
+    ok = ok && operand(h, &jw->tmB, pack.packed, H, q.rows, q.pitch, true, b_rows) &&
          encode(h, &jw->tmD, dweight, false, H, V, 1, lddw, lddw * V, 64, 32);
   }
   if (!ok) return GEMM_WS_ERR_CUDA;
 
   DeviceGuard guard(h->device);
-  rc = launch(h, ce::pack_kernel, ceil_div(T, pack.chunk), ce::PACK_THREADS, 0, 1, s, pack);
+  rc = launch(h, ce::pack_kernel, ceil_div(pack.padded, pack.chunk), ce::PACK_THREADS, 0, 1, s, pack);
   for (int64_t i = 0; i < q.pieces && rc == GEMM_WS_OK; ++i) {
     const int64_t c0 = i * q.piece, cols = V - c0 < q.piece ? V - c0 : q.piece;
     const int64_t held = round_up(cols, 8);   // G's columns of this piece; the last few may be zeros
@@ -462,20 +466,20 @@ int gemm_ws_linear_ce_backward(gemm_ws_t* h, const uint16_t* x, int64_t ldx,
     jg.b_row0 = static_cast<int>(c0);
     pg.cols = static_cast<int>(cols);
     pg.col0 = static_cast<int>(c0);
-    ok = encode(h, &jg.tmD, g, false, held, T, 1, q.piece, q.piece * T, 64, 32);
+    ok = encode(h, &jg.tmD, g, false, held, q.rows, 1, q.piece, q.piece * q.rows, 64, 32);
     int64_t units = 0;
     if (jx) {
       jx->k = static_cast<int>(cols);
       jx->b_row0 = static_cast<int>(c0);
       jx->add = i > 0;
       units += ceil_div(T, ce::BM * q.sums.cg) * ceil_div(H, q.sums.bn) * q.cuts;
-      ok = ok && operand(h, &jx->tmA, g, held, T, q.piece, false, ce::BM);
+      ok = ok && operand(h, &jx->tmA, g, held, q.rows, q.piece, false, ce::BM);
     }
     if (jw) {
       jw->m = static_cast<int>(cols);
       jw->d_row0 = static_cast<int>(c0);
       units += ceil_div(cols, ce::BM * q.sums.cg) * ceil_div(H, q.sums.bn);
-      ok = ok && operand(h, &jw->tmA, g, held, T, q.piece, true, ce::BM);
+      ok = ok && operand(h, &jw->tmA, g, held, q.rows, q.piece, true, ce::BM);
     }
     if (!ok) return GEMM_WS_ERR_CUDA;
     rc = launch_product<ce::GRAD>(

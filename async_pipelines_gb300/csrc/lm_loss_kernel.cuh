@@ -709,6 +709,7 @@ struct PackParams {
   int wide_target;            // int64
   int64_t ignore;
   int rows, cols, vocab;
+  int padded;                 // rows, rounded up to a multiple of 128
   int wide;                   // x's rows allow 16-byte accesses
   int chunk;                  // rows of a block, at most PACK_THREADS
   uint16_t* packed;           // T x H, `pitch` elements between rows
@@ -745,13 +746,14 @@ __device__ __forceinline__ int block_sum(int v, int* box) {
 // counts all targets itself (8 bytes a row, from L2 after the first block), which
 // saves a scan of its own before it. The rows that follow the last counted
 // one up to a multiple of 128 are zeroed, since dweight's product sums over
-// them; the uncounted rows' blocks do that.
+// them; the uncounted rows' blocks do that, and rows that are there only to make up
+// the 128 count as uncounted.
 __global__ void __launch_bounds__(PACK_THREADS) pack_kernel(const __grid_constant__ PackParams p) {
   __shared__ int box[PACK_THREADS / 32];
   __shared__ int dst_row[PACK_THREADS];   // [row of the chunk]: packed row; -1 - packed row: zeros; NO_ROW
   grid_dependency_wait();
   grid_launch_dependents();
-  const int r0 = blockIdx.x * p.chunk, r1 = min(p.rows, r0 + p.chunk);
+  const int r0 = blockIdx.x * p.chunk, r1 = min(p.padded, r0 + p.chunk);
   int before = 0, all = 0;
 #pragma unroll 4
   for (int r = threadIdx.x; r < p.rows; r += PACK_THREADS) {
@@ -764,7 +766,7 @@ __global__ void __launch_bounds__(PACK_THREADS) pack_kernel(const __grid_constan
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.count = all;
   const int row = r0 + threadIdx.x;
   const bool mine = threadIdx.x < p.chunk && row < r1;
-  const int64_t t = mine ? target_of(p, row) : p.ignore;
+  const int64_t t = mine && row < p.rows ? target_of(p, row) : p.ignore;
   const bool counted = mine && t != p.ignore;
   const unsigned vote = __ballot_sync(0xffffffffu, counted);
   if ((threadIdx.x & 31) == 0) box[threadIdx.x >> 5] = __popc(vote);
@@ -772,7 +774,7 @@ __global__ void __launch_bounds__(PACK_THREADS) pack_kernel(const __grid_constan
   int rank = before + __popc(vote & ((1u << (threadIdx.x & 31)) - 1u));
   for (int w = 0; w < static_cast<int>(threadIdx.x >> 5); ++w) rank += box[w];
   if (mine) {
-    p.place[row] = counted ? rank : -1;
+    if (row < p.rows) p.place[row] = counted ? rank : -1;
     if (counted) {
       const bool inside = t >= 0 && t < p.vocab;
       p.target_out[rank] = inside ? static_cast<int>(t) : -1;
