@@ -348,10 +348,14 @@ __global__ void __launch_bounds__(MOST) add_rms_norm_kernel(const __grid_constan
 #pragma unroll
   for (int k = 0; k < VPT; ++k) unpack(xr[k], v[k]);
   if (PATH == DROP || (PATH == ANY && p.drop.on)) {
-    uint64_t counter[VPT];
+    constexpr int PAIR = VPT < 2 ? VPT : 2;   // generators side by side; more would cost registers
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) counter[k] = first + k * team + t;
-    drop_groups(p.drop, seed, counter, v);
+    for (int k = 0; k < VPT; k += PAIR) {
+      uint64_t counter[PAIR];
+#pragma unroll
+      for (int j = 0; j < PAIR; ++j) counter[j] = first + (k + j) * team + t;
+      drop_groups(p.drop, seed, counter, reinterpret_cast<float(&)[PAIR][GROUP]>(v[k]));
+    }
   }
   SumMax s = {0.0f, 0.0f};
 #pragma unroll
