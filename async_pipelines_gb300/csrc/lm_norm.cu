@@ -151,46 +151,38 @@ int launch_dweight(gemm_ws* h, const float* partial, int64_t blocks, int cols, v
 // The ring needs some rows of each SM to be worth its set-up.
 constexpr int64_t kRingRows = 4;
 
-// How the rows pass through the ring: groups a thread holds, CTAs of an SM.
-struct Ring {
-  int vpt, ctas;
-};
-
-// Up to 2048 columns one group a thread and two CTAs, whose rows' waits overlap
-// (16384 x 1024 bf16: 31 us; one CTA with two groups 39); up to 8192 two groups
-// and one CTA (8192 x 8192: 86 us; two CTAs 103, four groups 94); beyond, four,
-// or a team would be more than a CTA.
-Ring pick_ring(int64_t cols) {
-  if (cols <= 2048) return {1, 2};
-  return {cols <= 8192 ? 2 : 4, 1};
-}
-
-// The ring's teams and stages; false where a team's row and one more do not fit.
-bool plan_ring(int64_t cols, int64_t size, int inputs, const Ring& r, gws::NormGradRing* q) {
-  const int64_t row = cols * size, warps = ceil_div(cols / gws::GROUP, 32 * r.vpt);
-  const int64_t room = gws::ring_bytes(r.ctas) / (inputs * row);
-  if (warps > gws::RING_WARPS || room < 2) return false;
-  q->row_bytes = static_cast<uint32_t>(row);
-  q->stages = static_cast<int>(room < gws::RING_MAX_STAGES ? room : gws::RING_MAX_STAGES);
-  q->teams = static_cast<int>(gws::RING_WARPS / warps);
-  if (q->teams >= q->stages) q->teams = q->stages - 1;
-  q->p.team = static_cast<int>(32 * warps);
-  return true;
+// How the rows pass through the ring: four groups a thread, the smallest teams
+// that hold a row, and two rows at least for each team; two groups and larger teams
+// where the ring has not that many rows (8192 fp32 columns). *vpt: which. False
+// where two rows do not fit, or a row is more than a CTA's warps hold.
+bool plan_ring(int64_t cols, int64_t size, int inputs, gws::NormGradRing* q, int* vpt) {
+  const int64_t row = cols * size, groups = cols / gws::GROUP;
+  int64_t room = gws::RING_BYTES / (inputs * row);
+  if (room > gws::RING_MAX_STAGES) room = gws::RING_MAX_STAGES;
+  for (*vpt = 4; *vpt >= 2; *vpt /= 2) {
+    const int64_t warps = ceil_div(groups, 32 * *vpt);
+    if (warps > gws::RING_WARPS) return false;
+    q->row_bytes = static_cast<uint32_t>(row);
+    q->p.team = static_cast<int>(32 * warps);
+    q->teams = static_cast<int>(gws::RING_WARPS / warps);
+    q->stages = static_cast<int>(room / q->teams);
+    if (q->stages >= 2) return true;
+  }
+  return false;
 }
 
 template <typename T, bool ON>
-auto ring_kernel(const Ring& r) {
-  return r.vpt == 4   ? gws::add_rms_norm_grad_ring_kernel<T, ON, 4, 1>
-         : r.vpt == 2 ? gws::add_rms_norm_grad_ring_kernel<T, ON, 2, 1>
-                      : gws::add_rms_norm_grad_ring_kernel<T, ON, 1, 2>;
+auto ring_kernel(int vpt) {
+  return vpt == 4 ? gws::add_rms_norm_grad_ring_kernel<T, ON, 4>
+                  : gws::add_rms_norm_grad_ring_kernel<T, ON, 2>;
 }
 
 template <typename T>
-int launch_grad_ring(gemm_ws* h, const Ring& r, const gws::NormGradRing& q, void* dweight,
+int launch_grad_ring(gemm_ws* h, int vpt, const gws::NormGradRing& q, void* dweight,
                      cudaStream_t s) {
-  const int64_t blocks = static_cast<int64_t>(r.ctas) * h->num_sms;
-  const int rc = launch(h, q.p.drop.on ? ring_kernel<T, true>(r) : ring_kernel<T, false>(r), blocks,
-                        gws::RING_THREADS, gws::ring_bytes(r.ctas), s, q);
+  const int64_t blocks = h->num_sms;
+  const int rc = launch(h, q.p.drop.on ? ring_kernel<T, true>(vpt) : ring_kernel<T, false>(vpt),
+                        blocks, gws::RING_THREADS, gws::RING_BYTES, s, q);
   if (rc != GEMM_WS_OK || !dweight) return rc;
   return launch_dweight<T>(h, q.p.partial, blocks, q.p.cols, dweight, s);
 }
@@ -228,15 +220,13 @@ int launch_dropout(gemm_ws* h, bool flat, int64_t blocks, const gws::DropoutPara
 // Sets the shared-memory attribute of the ring kernels on the current device.
 template <typename T>
 cudaError_t configure_ring() {
-  for (const Ring& r : {Ring{1, 2}, Ring{2, 1}, Ring{4, 1}}) {
-    const int bytes = static_cast<int>(gws::ring_bytes(r.ctas));
-    cudaError_t e = cudaFuncSetAttribute(ring_kernel<T, true>(r),
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(ring_kernel<T, false>(r),
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-  }
+  const int bytes = static_cast<int>(gws::RING_BYTES);
+  for (int vpt : {2, 4})
+    for (auto kernel : {ring_kernel<T, true>(vpt), ring_kernel<T, false>(vpt)}) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      if (e != cudaSuccess) return e;
+    }
   return cudaSuccess;
 }
 
@@ -431,16 +421,16 @@ int gemm_ws_add_rms_norm_backward(gemm_ws_t* h, int dtype, const void* dy, int64
   const gws::Path path = pick_path(q.wide, cols, q.drop);
   DeviceGuard guard(h->device);
   gws::NormGradRing ring;
-  const Ring shape = pick_ring(cols);
+  int vpt = 0;
   if (path != gws::ANY && rows >= kRingRows * h->num_sms) {
     ring.p = q;
     ring.status = h->work + 1;
     ring.timeout_ns = h->timeout_ns;
-    if (plan_ring(cols, size, dhidden ? 3 : 2, shape, &ring)) {
+    if (plan_ring(cols, size, dhidden ? 3 : 2, &ring, &vpt)) {
       switch (dtype) {
-        case GEMM_WS_BF16: return launch_grad_ring<__nv_bfloat16>(h, shape, ring, dweight, s);
-        case GEMM_WS_F16: return launch_grad_ring<__half>(h, shape, ring, dweight, s);
-        default: return launch_grad_ring<float>(h, shape, ring, dweight, s);
+        case GEMM_WS_BF16: return launch_grad_ring<__nv_bfloat16>(h, vpt, ring, dweight, s);
+        case GEMM_WS_F16: return launch_grad_ring<__half>(h, vpt, ring, dweight, s);
+        default: return launch_grad_ring<float>(h, vpt, ring, dweight, s);
       }
     }
   }

@@ -78,14 +78,12 @@ struct Dropout {
   float scale;           // 65536 / (65536 - round(65536 p)); 0 where all is dropped
 };
 
-// v = d(v) for N groups at their counters. A dropped value is 0 whatever it was.
+// v = d(v) for N groups by their words. A dropped value is 0 whatever it was.
 // Words are compared in the upper half of a register: the high one as it
 // stands (what is below it cannot change the verdict), the low one shifted up.
 template <int N>
-__device__ __forceinline__ void drop_groups(const Dropout& d, uint64_t seed,
-                                            const uint64_t (&counter)[N], float (&v)[N][GROUP]) {
-  uint32_t words[N][4];
-  philox(counter, seed, words);
+__device__ __forceinline__ void drop_by(const Dropout& d, const uint32_t (&words)[N][4],
+                                        float (&v)[N][GROUP]) {
 #pragma unroll
   for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -93,6 +91,15 @@ __device__ __forceinline__ void drop_groups(const Dropout& d, uint64_t seed,
       v[n][2 * i] = (words[n][i] << 16) > d.limit ? v[n][2 * i] * d.scale : 0.0f;
       v[n][2 * i + 1] = words[n][i] > d.limit ? v[n][2 * i + 1] * d.scale : 0.0f;
     }
+}
+
+// v = d(v) for N groups at their counters.
+template <int N>
+__device__ __forceinline__ void drop_groups(const Dropout& d, uint64_t seed,
+                                            const uint64_t (&counter)[N], float (&v)[N][GROUP]) {
+  uint32_t words[N][4];
+  philox(counter, seed, words);
+  drop_by(d, words, v);
 }
 
 // ------------------------------------------------------------ groups
@@ -570,23 +577,25 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) add_rms_norm_grad_kernel(co
 }
 
 // The same for many rows that lie FAST: the rows come through a ring in shared
-// memory, filled by one warp's bulk copies, so that the next rows are on their
-// way while a team waits for its row's sum (loaded straight into registers the
-// rows of an SM stop at each such wait: 8192 x 8192 bf16 took 124 us, with dropout
-// 171, against 86 and 127: 0.92 and 0.78 of the copy rate). Both passes over a
-// row read it from the ring: holding it in registers in between cost more
-// (130 us) than the second reading, with one CTA's warps waiting together.
-// RING_WARPS warps form teams of `team` threads; the CTA's k-th row goes to
-// team k % teams through stage k % stages.
+// memory by bulk copies, so that the next rows are on their way while a team
+// waits for its row's sum (loaded straight into registers the rows of an SM stop
+// at each such wait: 8192 x 8192 bf16 took 124 us, with dropout 171, against 87
+// and 107: 0.91 and 0.93 of the copy rate). RING_WARPS warps form teams of `team`
+// threads; row k of a CTA goes to its team k % teams, each of which has its own
+// stages. There is no producer warp: a team's barrier of a row says that all of it
+// is done with the row before, whose stage one thread then fills again. (With such
+// a warp the CTA's 17 warps count as 20, which leaves 96 registers a thread instead
+// of 128, and four groups a thread spill.) Both passes over a row read it from the
+// ring: holding it in registers in between cost more (130 us) than the second
+// reading.
 constexpr int RING_WARPS = 16;
-constexpr int RING_THREADS = (RING_WARPS + 1) * 32;
-constexpr int RING_MAX_STAGES = 32;
-// Shared memory of the ring with 1 or 2 CTAs on an SM.
-__host__ __device__ constexpr uint32_t ring_bytes(int ctas) { return (ctas == 2 ? 104 : 208) * 1024; }
+constexpr int RING_THREADS = RING_WARPS * 32;
+constexpr int RING_MAX_STAGES = 32;   // of all teams
+constexpr uint32_t RING_BYTES = 208 * 1024;
 
 struct NormGradRing {
   NormGradParams p;
-  int stages, teams;
+  int stages, teams;    // stages of a team
   uint32_t row_bytes;   // of one matrix
   uint32_t* status;
   unsigned long long timeout_ns;
@@ -623,11 +632,11 @@ __device__ __forceinline__ bool team_sync(int id, int threads, bool ok) {
   return all != 0;
 }
 
-template <typename T, bool ON, int VPT, int CTAS>
-__global__ void __launch_bounds__(RING_THREADS, CTAS)
+template <typename T, bool ON, int VPT>
+__global__ void __launch_bounds__(RING_THREADS, 1)
     add_rms_norm_grad_ring_kernel(const __grid_constant__ NormGradRing q) {
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ __align__(8) uint64_t bars[2 * RING_MAX_STAGES];
+  __shared__ __align__(8) uint64_t bars[RING_MAX_STAGES];
   __shared__ float box[2][RING_WARPS];
   __shared__ uint32_t aborted;
   const NormGradParams& p = q.p;
@@ -635,13 +644,8 @@ __global__ void __launch_bounds__(RING_THREADS, CTAS)
   const int cols = p.cols, groups = cols / GROUP, team = p.team, warps = team / 32;
   const int inputs = p.dh ? 3 : 2;
   const uint32_t stage_bytes = inputs * q.row_bytes;
-  auto full = [&](int s) { return smem_addr(&bars[s]); };
-  auto empty = [&](int s) { return smem_addr(&bars[RING_MAX_STAGES + s]); };
   if (threadIdx.x == 0) {
-    for (int s = 0; s < q.stages; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), warps);
-    }
+    for (int s = 0; s < q.teams * q.stages; ++s) mbar_init(smem_addr(&bars[s]), 1);
     aborted = 0;
     fence_mbar_init();
   }
@@ -649,55 +653,62 @@ __global__ void __launch_bounds__(RING_THREADS, CTAS)
   const Watchdog wd{&aborted, q.status, q.timeout_ns};
   grid_dependency_wait();
   grid_launch_dependents();
-  const int64_t step = gridDim.x;
-  const int64_t mine = (p.rows - blockIdx.x + step - 1) / step;   // this CTA's rows
+  const int t = threadIdx.x % team, which = threadIdx.x / team;
+  // The team's rows are first_row, + row_step, ...; `mine` of them.
+  const int64_t row_step = static_cast<int64_t>(gridDim.x) * q.teams;
+  const int64_t first_row = blockIdx.x + static_cast<int64_t>(which) * gridDim.x;
+  const int64_t mine =
+      which < q.teams && first_row < p.rows ? (p.rows - first_row + row_step - 1) / row_step : 0;
 
   Pair acc[VPT][GROUP / 2];
 #pragma unroll
   for (int k = 0; k < VPT; ++k)
 #pragma unroll
     for (int i = 0; i < GROUP / 2; ++i) acc[k][i] = 0;
-  const int t = threadIdx.x % team, which = threadIdx.x / team;   // of a consumer
 
-  if (warp == RING_WARPS) {
-    // A lane for each matrix: one thread's copies of 2 KiB would come too slowly.
-    int s = 0;
-    uint32_t ph = 0;
-    int64_t k = 0;
-    const T* src = static_cast<const T*>(lane == 0 ? p.dy : lane == 1 ? p.h : p.dh);
-    const int64_t ld = lane == 0 ? p.lddy : lane == 1 ? p.ldh : p.lddh;
-    for (; k < mine; ++k) {
-      if (!__all_sync(0xffffffffu, ring_wait(empty(s), ph ^ 1, wd))) break;
-      if (lane == 0) mbar_arrive_expect_tx(full(s), stage_bytes);
-      __syncwarp();
-      if (lane < inputs)
-        bulk_load_1d(smem_addr(ring) + s * stage_bytes + lane * q.row_bytes,
-                     src + (blockIdx.x + k * step) * ld, q.row_bytes, full(s));
-      if (++s == q.stages) {
-        s = 0;
-        ph ^= 1;
-      }
-    }
-    if (k < mine)   // given up: the copies under way land before the CTA ends
-      for (int64_t j = k > q.stages ? k - q.stages : 0; j < k; ++j)
-        wait_drain(full(static_cast<int>(j % q.stages)), static_cast<uint32_t>(j / q.stages) & 1);
-  } else if (which < q.teams) {
+  if (mine > 0) {
+    const uint32_t stage0 = smem_addr(ring) + which * q.stages * stage_bytes;
+    auto full = [&](int s) { return smem_addr(&bars[which * q.stages + s]); };
+    // One thread of the team fetches row k into stage s.
+    auto fetch = [&](int64_t k, int s) {
+      const int64_t row = first_row + k * row_step;
+      const uint32_t dst = stage0 + s * stage_bytes;
+      mbar_arrive_expect_tx(full(s), stage_bytes);
+      bulk_load_1d(dst, static_cast<const T*>(p.dy) + row * p.lddy, q.row_bytes, full(s));
+      bulk_load_1d(dst + q.row_bytes, static_cast<const T*>(p.h) + row * p.ldh, q.row_bytes, full(s));
+      if (p.dh)
+        bulk_load_1d(dst + 2 * q.row_bytes, static_cast<const T*>(p.dh) + row * p.lddh, q.row_bytes,
+                     full(s));
+    };
+    if (t == 0)
+      for (int k = 0; k < q.stages && k < mine; ++k) fetch(k, k);
     const uint64_t seed = p.drop.rng[0], first = p.drop.rng[1];
-    int s = which, turn = 0;
-    uint32_t ph = 0;
     Raw<T> wr[VPT] = {};
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
       if (j * team + t < groups) wr[j] = static_cast<const Raw<T>*>(p.weight)[j * team + t];
-    float next_r = which < mine ? p.rstd[blockIdx.x + which * step] : 0.0f;
-    for (int64_t k = which; k < mine; k += q.teams, turn ^= 1) {
-      const int64_t row = blockIdx.x + k * step;
+    int s = 0, turn = 0, before = q.stages - 1;   // this row's stage, and the one before's
+    uint32_t ph = 0;
+    float next_r = p.rstd[first_row];
+    int64_t k = 0;
+    for (; k < mine; ++k, turn ^= 1) {
+      const int64_t row = first_row + k * row_step;
       const float r = next_r;
-      if (k + q.teams < mine) next_r = p.rstd[row + q.teams * step];
+      if (k + 1 < mine) next_r = p.rstd[row + row_step];
+      // The mask needs nothing of the row: its rounds fill the wait for it.
+      uint32_t words[VPT][4];
+      if (ON) {
+        uint64_t counter[VPT];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+          counter[j] = first + static_cast<uint64_t>(row) * groups + j * team + t;
+        philox(counter, seed, words);
+      }
       bool ok = __all_sync(0xffffffffu, ring_wait(full(s), ph, wd));
-      const Raw<T>* dy = reinterpret_cast<const Raw<T>*>(ring + s * stage_bytes) + t;
-      const Raw<T>* h = reinterpret_cast<const Raw<T>*>(ring + s * stage_bytes + q.row_bytes) + t;
-      const Raw<T>* dh = reinterpret_cast<const Raw<T>*>(ring + s * stage_bytes + 2 * q.row_bytes) + t;
+      const uint8_t* stage = ring + (which * q.stages + s) * stage_bytes;
+      const Raw<T>* dy = reinterpret_cast<const Raw<T>*>(stage) + t;
+      const Raw<T>* h = reinterpret_cast<const Raw<T>*>(stage + q.row_bytes) + t;
+      const Raw<T>* dh = reinterpret_cast<const Raw<T>*>(stage + 2 * q.row_bytes) + t;
       // acc += dy h r, and the sum of dy weight h
       const Pair r2 = pair_of(r, r);
       Pair sums = 0;
@@ -727,16 +738,15 @@ __global__ void __launch_bounds__(RING_THREADS, CTAS)
         for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       }
       if (!ok) break;
+      // The whole team is here, so it has done with the row before.
+      if (t == 0 && k > 0 && k - 1 + q.stages < mine) fetch(k - 1 + q.stages, before);
       // dres = dh + r dy weight - h r^2 mean(dy weight h r)
       const float m = -r * r * (r * sum / static_cast<float>(cols));
       const Pair m2 = pair_of(m, m);
       Raw<T>* dres = reinterpret_cast<Raw<T>*>(static_cast<T*>(p.dres) + row * p.lddres) + t;
       Raw<T>* dx = reinterpret_cast<Raw<T>*>(static_cast<T*>(p.dx) + row * p.lddx) + t;
-      float d[VPT][GROUP];
-      uint64_t counter[VPT];
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
-        counter[j] = first + static_cast<uint64_t>(row) * groups + j * team + t;
         if (j * team + t < groups) {
           Pair a[GROUP / 2], n[GROUP / 2], w[GROUP / 2], e[GROUP / 2];
           unpack(dy[j * team], a);
@@ -745,30 +755,28 @@ __global__ void __launch_bounds__(RING_THREADS, CTAS)
           Raw<T> dr = {};
           if (p.dh) dr = dh[j * team];
           unpack(dr, e);
+          float d[1][GROUP];
 #pragma unroll
           for (int i = 0; i < GROUP / 2; ++i) {
             e[i] = fma2(n[i], m2, fma2(mul2(a[i], w[i]), r2, e[i]));
-            d[j][2 * i] = values_of(e[i]).x;
-            d[j][2 * i + 1] = values_of(e[i]).y;
+            d[0][2 * i] = values_of(e[i]).x;
+            d[0][2 * i + 1] = values_of(e[i]).y;
           }
-          if (p.dres) dres[j * team] = pack<T>(d[j]);
-          if (!ON) dx[j * team] = pack<T>(d[j]);
+          if (p.dres) dres[j * team] = pack<T>(d[0]);
+          if (ON) drop_by(p.drop, reinterpret_cast<const uint32_t(&)[1][4]>(words[j]), d);
+          dx[j * team] = pack<T>(d[0]);
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty(s));
-      s += q.teams;
-      if (s >= q.stages) {
-        s -= q.stages;
+      before = s;
+      if (++s == q.stages) {
+        s = 0;
         ph ^= 1;
       }
-      if (ON) {
-        drop_groups(p.drop, seed, counter, d);
-#pragma unroll
-        for (int j = 0; j < VPT; ++j)
-          if (j * team + t < groups) dx[j * team] = pack<T>(d[j]);
-      }
     }
+    // Given up: the copies under way land before the CTA ends.
+    if (k < mine && t == 0)
+      for (int64_t j = k; j < mine && j < k + q.stages - (k > 0); ++j)
+        wait_drain(full(static_cast<int>(j % q.stages)), static_cast<uint32_t>(j / q.stages) & 1);
   }
   if (!p.partial) return;
   // The teams' shares of dweight, added in the teams' order.
@@ -777,7 +785,7 @@ __global__ void __launch_bounds__(RING_THREADS, CTAS)
   for (int c = threadIdx.x; c < cols; c += blockDim.x) share[c] = 0.0f;
   for (int v = 0; v < q.teams; ++v) {
     __syncthreads();
-    if (warp < RING_WARPS && which == v) {
+    if (which == v) {
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
         const int g = k * team + t;
