@@ -109,6 +109,30 @@ Team pick_team(const gemm_ws* h, int64_t rows, int64_t cols, gws::Path path) {
   return t;
 }
 
+// The ring needs some rows of each SM to be worth its set-up.
+constexpr int64_t kRingRows = 4;
+
+// How the rows pass through the ring: four groups a thread, the smallest teams
+// that hold a row, and two rows at least for each team; two groups and larger teams
+// where the ring has not that many rows (8192 fp32 columns). *vpt: which. False
+// where two rows do not fit, or a row is more than a CTA's warps hold.
+template <typename Q>
+bool plan_ring(int64_t cols, int64_t size, int inputs, Q* q, int* vpt) {
+  const int64_t row = cols * size, groups = cols / gws::GROUP;
+  int64_t room = gws::RING_BYTES / (inputs * row);
+  if (room > gws::RING_MAX_STAGES) room = gws::RING_MAX_STAGES;
+  for (*vpt = 4; *vpt >= 2; *vpt /= 2) {
+    const int64_t warps = ceil_div(groups, 32 * *vpt);
+    if (warps > gws::RING_WARPS) return false;
+    q->row_bytes = static_cast<uint32_t>(row);
+    q->p.team = static_cast<int>(32 * warps);
+    q->teams = static_cast<int>(gws::RING_WARPS / warps);
+    q->stages = static_cast<int>(room / q->teams);
+    if (q->stages >= 2) return true;
+  }
+  return false;
+}
+
 // The kernel instance for a team and a path. Fewer threads a block leave each
 // more registers: 64 with 1024, 128 with 512.
 #define LM_NORM_INSTANCE(KERNEL, T, PATH, ...)                                     \
@@ -124,6 +148,11 @@ int launch_norm(gemm_ws* h, const Team& t, gws::Path path, const gws::NormParams
   if constexpr (Q == 0)   // 8 bits are for serving: with dropout they take the general path
     if (path == gws::DROP) kernel = LM_NORM_INSTANCE(add_rms_norm_kernel, T, gws::DROP, Q);
   return launch(h, kernel, ceil_div(p.rows, t.rows), t.threads * t.rows, 0, s, p);
+}
+
+template <typename T>
+auto forward_ring_kernel(int vpt) {
+  return vpt == 4 ? gws::add_rms_norm_ring_kernel<T, 4> : gws::add_rms_norm_ring_kernel<T, 2>;
 }
 
 template <typename T>
@@ -146,29 +175,6 @@ int launch_dweight(gemm_ws* h, const float* partial, int64_t blocks, int cols, v
   q.dweight = dweight;
   return launch(h, gws::dweight_kernel<T>, ceil_div(cols, gws::DW_COLS),
                 gws::DW_COLS * gws::DW_LANES, 0, s, q);
-}
-
-// The ring needs some rows of each SM to be worth its set-up.
-constexpr int64_t kRingRows = 4;
-
-// How the rows pass through the ring: four groups a thread, the smallest teams
-// that hold a row, and two rows at least for each team; two groups and larger teams
-// where the ring has not that many rows (8192 fp32 columns). *vpt: which. False
-// where two rows do not fit, or a row is more than a CTA's warps hold.
-bool plan_ring(int64_t cols, int64_t size, int inputs, gws::NormGradRing* q, int* vpt) {
-  const int64_t row = cols * size, groups = cols / gws::GROUP;
-  int64_t room = gws::RING_BYTES / (inputs * row);
-  if (room > gws::RING_MAX_STAGES) room = gws::RING_MAX_STAGES;
-  for (*vpt = 4; *vpt >= 2; *vpt /= 2) {
-    const int64_t warps = ceil_div(groups, 32 * *vpt);
-    if (warps > gws::RING_WARPS) return false;
-    q->row_bytes = static_cast<uint32_t>(row);
-    q->p.team = static_cast<int>(32 * warps);
-    q->teams = static_cast<int>(gws::RING_WARPS / warps);
-    q->stages = static_cast<int>(room / q->teams);
-    if (q->stages >= 2) return true;
-  }
-  return false;
 }
 
 template <typename T, bool ON>
@@ -222,7 +228,11 @@ template <typename T>
 cudaError_t configure_ring() {
   const int bytes = static_cast<int>(gws::RING_BYTES);
   for (int vpt : {2, 4})
-    for (auto kernel : {ring_kernel<T, true>(vpt), ring_kernel<T, false>(vpt)}) {
+    for (int k = 0; k < 3; ++k) {
+      const void* kernel = reinterpret_cast<const void*>(ring_kernel<T, false>(vpt));
+      if (k == 1) kernel = reinterpret_cast<const void*>(ring_kernel<T, true>(vpt));
+      if constexpr (sizeof(T) == 2)
+        if (k == 2) kernel = reinterpret_cast<const void*>(forward_ring_kernel<T>(vpt));
       const cudaError_t e =
           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
       if (e != cudaSuccess) return e;
@@ -342,10 +352,23 @@ int gemm_ws_add_rms_norm(gemm_ws_t* h, int dtype, const void* x, int64_t ldx,
   q.wide = in[0].wide() && (!residual || in[1].wide()) &&
            reinterpret_cast<uintptr_t>(weight) % 16 == 0 && (!hidden || mh.wide()) && my.wide();
   const gws::Path path = pick_path(q.wide, cols, q.drop);
-  const Team t = pick_team(h, rows, cols, path);
-  q.team = t.threads;
   DeviceGuard guard(h->device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  gws::NormRing ring;
+  int vpt = 0;
+  if (path == gws::DROP && same && size == 2 && rows >= kRingRows * h->num_sms) {
+    ring.p = q;
+    ring.status = h->work + 1;
+    ring.timeout_ns = h->timeout_ns;
+    if (plan_ring(cols, size, residual ? 2 : 1, &ring, &vpt)) {
+      return launch(h,
+                    dtype == GEMM_WS_BF16 ? forward_ring_kernel<__nv_bfloat16>(vpt)
+                                          : forward_ring_kernel<__half>(vpt),
+                    h->num_sms, gws::RING_THREADS, gws::RING_BYTES, s, ring);
+    }
+  }
+  const Team t = pick_team(h, rows, cols, path);
+  q.team = t.threads;
   switch (dtype) {
     case GEMM_WS_BF16: return launch_norm<__nv_bfloat16>(h, output, t, path, q, s);
     case GEMM_WS_F16: return launch_norm<__half>(h, output, t, path, q, s);

@@ -307,6 +307,73 @@ __device__ __forceinline__ SumMax reduce_team(SumMax v, int warps, SumMax* box) 
   return all;
 }
 
+// ------------------------------------------------------------ rows through shared memory
+
+constexpr int RING_WARPS = 16;
+constexpr int RING_THREADS = RING_WARPS * 32;
+constexpr int RING_MAX_STAGES = 32;   // of all teams
+constexpr uint32_t RING_BYTES = 208 * 1024;
+
+// Where a team stands in its rows: those of a CTA go to its teams in turn.
+struct RingRows {
+  int64_t first, step, count;
+};
+__device__ __forceinline__ RingRows ring_rows(int64_t rows, int teams, int which) {
+  RingRows r;
+  r.step = static_cast<int64_t>(gridDim.x) * teams;
+  r.first = blockIdx.x + static_cast<int64_t>(which) * gridDim.x;
+  r.count = which < teams && r.first < rows ? (rows - r.first + r.step - 1) / r.step : 0;
+  return r;
+}
+
+// A bounded wait without a call (a call's conventions would spill the sums that
+// live across it) and, at first, without the slow global timer.
+__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, const Watchdog& wd) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1; !mbar_test_wait(bar, parity); ++it) {
+    if (it & 1023) continue;
+    if (*wd.abort) return false;
+    if (t0 == 0) t0 = global_timer_ns();
+    if (global_timer_ns() - t0 > wd.limit_ns) {
+      *wd.abort = 1;
+      atomicExch(wd.status, STATUS_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+// Barrier `id` of `threads` threads; whether `ok` holds for all of them.
+__device__ __forceinline__ bool team_sync(int id, int threads, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "barrier.cta.red.and.pred p, %2, %3, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(all)
+      : "r"(static_cast<uint32_t>(ok)), "r"(id), "r"(threads)
+      : "memory");
+  return all != 0;
+}
+
+// The sum over a team of a value a thread, in every thread, in a fixed order.
+// `ok` is false after it unless it was true in all of them: the team's warps give
+// up together. `box`: a slot for each warp of the CTA, not used again before the
+// next sum but one.
+__device__ __forceinline__ float ring_sum(float sum, int which, int team, float* box, bool* ok) {
+  const int warps = team / 32, lane = threadIdx.x % 32;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (warps == 1) return sum;
+  if (lane == 0) box[threadIdx.x / 32] = sum;
+  *ok = team_sync(1 + which, team, *ok);
+  sum = (lane & 15) < warps ? box[which * warps + (lane & 15)] : 0.0f;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
 // ------------------------------------------------------------ forward
 
 struct NormParams {
@@ -443,6 +510,124 @@ __global__ void __launch_bounds__(MOST) add_rms_norm_kernel(const __grid_constan
       }
     }
   }
+}
+
+struct NormRing {
+  NormParams p;
+  int stages, teams;    // stages of a team
+  uint32_t row_bytes;   // of one matrix
+  uint32_t* status;
+  unsigned long long timeout_ns;
+};
+
+// The forward pass with dropout for many rows of a 16-bit type that lie FAST: as
+// the gradient's ring (see there), since the generator's rounds leave the plain
+// kernel too few threads on an SM to cover a row's wait (8192 x 8192 bf16: 100 us,
+// here 95, 0.84 of the copy rate; 4096 x 8192 fp32, with half the rounds a byte,
+// is faster without: 82 against 97). A team has its row in registers at its
+// barrier, so the row's own stage is free then.
+template <typename T, int VPT>
+__global__ void __launch_bounds__(RING_THREADS, 1)
+    add_rms_norm_ring_kernel(const __grid_constant__ NormRing q) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ __align__(8) uint64_t bars[RING_MAX_STAGES];
+  __shared__ float box[2][RING_WARPS];
+  __shared__ uint32_t aborted;
+  const NormParams& p = q.p;
+  const int cols = p.cols, groups = cols / GROUP, team = p.team;
+  const int inputs = p.residual ? 2 : 1;
+  const uint32_t stage_bytes = inputs * q.row_bytes;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < q.teams * q.stages; ++s) mbar_init(smem_addr(&bars[s]), 1);
+    aborted = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const Watchdog wd{&aborted, q.status, q.timeout_ns};
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int t = threadIdx.x % team, which = threadIdx.x / team;
+  const RingRows rows = ring_rows(p.rows, q.teams, which);
+  if (rows.count == 0) return;
+  const uint32_t stage0 = smem_addr(ring) + which * q.stages * stage_bytes;
+  auto full = [&](int s) { return smem_addr(&bars[which * q.stages + s]); };
+  auto fetch = [&](int64_t k, int s) {
+    const int64_t row = rows.first + k * rows.step;
+    const uint32_t dst = stage0 + s * stage_bytes;
+    mbar_arrive_expect_tx(full(s), stage_bytes);
+    bulk_load_1d(dst, static_cast<const T*>(p.x) + row * p.ldx, q.row_bytes, full(s));
+    if (p.residual)
+      bulk_load_1d(dst + q.row_bytes, static_cast<const T*>(p.residual) + row * p.ldr, q.row_bytes,
+                   full(s));
+  };
+  if (t == 0)
+    for (int k = 0; k < q.stages && k < rows.count; ++k) fetch(k, k);
+  const uint64_t seed = p.drop.rng[0], first = p.drop.rng[1];
+  Raw<T> wr[VPT] = {};
+#pragma unroll
+  for (int j = 0; j < VPT; ++j)
+    if (j * team + t < groups) wr[j] = static_cast<const Raw<T>*>(p.weight)[j * team + t];
+  int s = 0, turn = 0;
+  uint32_t ph = 0;
+  int64_t k = 0;
+  for (; k < rows.count; ++k, turn ^= 1) {
+    const int64_t row = rows.first + k * rows.step;
+    uint64_t counter[VPT];
+    uint32_t words[VPT][4];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+      counter[j] = first + static_cast<uint64_t>(row) * groups + j * team + t;
+    philox(counter, seed, words);
+    bool ok = __all_sync(0xffffffffu, ring_wait(full(s), ph, wd));
+    const uint8_t* stage = ring + (which * q.stages + s) * stage_bytes;
+    const Raw<T>* x = reinterpret_cast<const Raw<T>*>(stage) + t;
+    const Raw<T>* res = reinterpret_cast<const Raw<T>*>(stage + q.row_bytes) + t;
+    Raw<T>* h = reinterpret_cast<Raw<T>*>(static_cast<T*>(p.h) + row * p.ldh) + t;
+    float v[VPT][GROUP];
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      if (j * team + t < groups) {
+        unpack(x[j * team], v[j]);
+        drop_by(p.drop, reinterpret_cast<const uint32_t(&)[1][4]>(words[j]),
+                reinterpret_cast<float(&)[1][GROUP]>(v[j]));
+        if (p.residual) {
+          float r[GROUP];
+          unpack(res[j * team], r);
+#pragma unroll
+          for (int i = 0; i < GROUP; ++i) v[j][i] += r[i];
+        }
+#pragma unroll
+        for (int i = 0; i < GROUP; ++i) sum = fmaf(v[j][i], v[j][i], sum);
+        if (p.h) h[j * team] = pack<T>(v[j]);
+      }
+    }
+    __syncwarp();
+    sum = ring_sum(sum, which, team, box[turn], &ok);
+    if (!ok) break;
+    if (t == 0 && k + q.stages < rows.count) fetch(k + q.stages, s);   // the row is in registers
+    const float r = rsqrtf(sum / static_cast<float>(cols) + p.eps);
+    if (p.rstd && t == 0) p.rstd[row] = r;
+    Raw<T>* y = reinterpret_cast<Raw<T>*>(static_cast<T*>(p.y) + row * p.ldy) + t;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      if (j * team + t < groups) {
+        float w[GROUP];
+        unpack(wr[j], w);
+#pragma unroll
+        for (int i = 0; i < GROUP; ++i) v[j][i] = v[j][i] * r * w[i];
+        y[j * team] = pack<T>(v[j]);
+      }
+    }
+    if (++s == q.stages) {
+      s = 0;
+      ph ^= 1;
+    }
+  }
+  // Given up: the copies under way land before the CTA ends.
+  if (k < rows.count && t == 0)
+    for (int64_t j = k; j < rows.count && j < k + q.stages; ++j)
+      wait_drain(full(static_cast<int>(j % q.stages)), static_cast<uint32_t>(j / q.stages) & 1);
 }
 
 // ------------------------------------------------------------ backward
@@ -588,11 +773,6 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) add_rms_norm_grad_kernel(co
 // of 128, and four groups a thread spill.) Both passes over a row read it from the
 // ring: holding it in registers in between cost more (130 us) than the second
 // reading.
-constexpr int RING_WARPS = 16;
-constexpr int RING_THREADS = RING_WARPS * 32;
-constexpr int RING_MAX_STAGES = 32;   // of all teams
-constexpr uint32_t RING_BYTES = 208 * 1024;
-
 struct NormGradRing {
   NormGradParams p;
   int stages, teams;    // stages of a team
@@ -600,37 +780,6 @@ struct NormGradRing {
   uint32_t* status;
   unsigned long long timeout_ns;
 };
-
-// A bounded wait without a call (a call's conventions would spill the sums that
-// live across it) and, at first, without the slow global timer.
-__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, const Watchdog& wd) {
-  uint64_t t0 = 0;
-  for (uint32_t it = 1; !mbar_test_wait(bar, parity); ++it) {
-    if (it & 1023) continue;
-    if (*wd.abort) return false;
-    if (t0 == 0) t0 = global_timer_ns();
-    if (global_timer_ns() - t0 > wd.limit_ns) {
-      *wd.abort = 1;
-      atomicExch(wd.status, STATUS_TIMEOUT);
-      return false;
-    }
-  }
-  return true;
-}
-
-// Barrier `id` of `threads` threads; whether `ok` holds for all of them.
-__device__ __forceinline__ bool team_sync(int id, int threads, bool ok) {
-  uint32_t all;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 q, %1, 0;\n\t"
-      "barrier.cta.red.and.pred p, %2, %3, q;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(all)
-      : "r"(static_cast<uint32_t>(ok)), "r"(id), "r"(threads)
-      : "memory");
-  return all != 0;
-}
 
 template <typename T, bool ON, int VPT>
 __global__ void __launch_bounds__(RING_THREADS, 1)
@@ -640,8 +789,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
   __shared__ float box[2][RING_WARPS];
   __shared__ uint32_t aborted;
   const NormGradParams& p = q.p;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int cols = p.cols, groups = cols / GROUP, team = p.team, warps = team / 32;
+  const int cols = p.cols, groups = cols / GROUP, team = p.team;
   const int inputs = p.dh ? 3 : 2;
   const uint32_t stage_bytes = inputs * q.row_bytes;
   if (threadIdx.x == 0) {
@@ -654,11 +802,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
   grid_dependency_wait();
   grid_launch_dependents();
   const int t = threadIdx.x % team, which = threadIdx.x / team;
-  // The team's rows are first_row, + row_step, ...; `mine` of them.
-  const int64_t row_step = static_cast<int64_t>(gridDim.x) * q.teams;
-  const int64_t first_row = blockIdx.x + static_cast<int64_t>(which) * gridDim.x;
-  const int64_t mine =
-      which < q.teams && first_row < p.rows ? (p.rows - first_row + row_step - 1) / row_step : 0;
+  const RingRows rows = ring_rows(p.rows, q.teams, which);
 
   Pair acc[VPT][GROUP / 2];
 #pragma unroll
@@ -666,12 +810,12 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
 #pragma unroll
     for (int i = 0; i < GROUP / 2; ++i) acc[k][i] = 0;
 
-  if (mine > 0) {
+  if (rows.count > 0) {
     const uint32_t stage0 = smem_addr(ring) + which * q.stages * stage_bytes;
     auto full = [&](int s) { return smem_addr(&bars[which * q.stages + s]); };
     // One thread of the team fetches row k into stage s.
     auto fetch = [&](int64_t k, int s) {
-      const int64_t row = first_row + k * row_step;
+      const int64_t row = rows.first + k * rows.step;
       const uint32_t dst = stage0 + s * stage_bytes;
       mbar_arrive_expect_tx(full(s), stage_bytes);
       bulk_load_1d(dst, static_cast<const T*>(p.dy) + row * p.lddy, q.row_bytes, full(s));
@@ -681,7 +825,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
                      full(s));
     };
     if (t == 0)
-      for (int k = 0; k < q.stages && k < mine; ++k) fetch(k, k);
+      for (int k = 0; k < q.stages && k < rows.count; ++k) fetch(k, k);
     const uint64_t seed = p.drop.rng[0], first = p.drop.rng[1];
     Raw<T> wr[VPT] = {};
 #pragma unroll
@@ -689,12 +833,12 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
       if (j * team + t < groups) wr[j] = static_cast<const Raw<T>*>(p.weight)[j * team + t];
     int s = 0, turn = 0, before = q.stages - 1;   // this row's stage, and the one before's
     uint32_t ph = 0;
-    float next_r = p.rstd[first_row];
+    float next_r = p.rstd[rows.first];
     int64_t k = 0;
-    for (; k < mine; ++k, turn ^= 1) {
-      const int64_t row = first_row + k * row_step;
+    for (; k < rows.count; ++k, turn ^= 1) {
+      const int64_t row = rows.first + k * rows.step;
       const float r = next_r;
-      if (k + 1 < mine) next_r = p.rstd[row + row_step];
+      if (k + 1 < rows.count) next_r = p.rstd[row + rows.step];
       // The mask needs nothing of the row: its rounds fill the wait for it.
       uint32_t words[VPT][4];
       if (ON) {
@@ -727,19 +871,11 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
           }
         }
       }
-      float sum = values_of(sums).x + values_of(sums).y;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (warps > 1) {
-        if (lane == 0) box[turn][warp] = sum;
-        ok = team_sync(1 + which, team, ok);   // the team's warps give up together
-        sum = (lane & 15) < warps ? box[turn][which * warps + (lane & 15)] : 0.0f;
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      }
+      const float sum =
+          ring_sum(values_of(sums).x + values_of(sums).y, which, team, box[turn], &ok);
       if (!ok) break;
       // The whole team is here, so it has done with the row before.
-      if (t == 0 && k > 0 && k - 1 + q.stages < mine) fetch(k - 1 + q.stages, before);
+      if (t == 0 && k > 0 && k - 1 + q.stages < rows.count) fetch(k - 1 + q.stages, before);
       // dres = dh + r dy weight - h r^2 mean(dy weight h r)
       const float m = -r * r * (r * sum / static_cast<float>(cols));
       const Pair m2 = pair_of(m, m);
@@ -774,8 +910,8 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
       }
     }
     // Given up: the copies under way land before the CTA ends.
-    if (k < mine && t == 0)
-      for (int64_t j = k; j < mine && j < k + q.stages - (k > 0); ++j)
+    if (k < rows.count && t == 0)
+      for (int64_t j = k; j < rows.count && j < k + q.stages - (k > 0); ++j)
         wait_drain(full(static_cast<int>(j % q.stages)), static_cast<uint32_t>(j / q.stages) & 1);
   }
   if (!p.partial) return;

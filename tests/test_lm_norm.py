@@ -211,6 +211,32 @@ def test_gradients_of_many_rows(g, T, H, dtype, dropout):
 
 
 @gpu
+@pytest.mark.parametrize("T,H,dtype", [
+    (608, 8, torch.bfloat16), (650, 8192, torch.bfloat16), (700, 4104, torch.float16),
+    (1400, 2048, torch.float32), (615, 16384, torch.bfloat16), (640, 8192, torch.float32),
+    (620, 16384, torch.float32), (4000, 264, torch.bfloat16)])
+@pytest.mark.parametrize("given", [True, False])
+def test_norm_with_dropout_of_many_rows(g, T, H, dtype, given):
+    """Enough rows for several on each SM; strides between rows, with and without a residual."""
+    gen = torch.Generator().manual_seed(T + H)
+    x, res = (rows(T, H, dtype, gen, 8, 0, s) for s in (1.0, 3.0))
+    w = rows(1, H, dtype, gen)[0]
+    p, words = 0.25, rng_words(7, 11)
+    h, y = torch.empty(T, H, dtype=dtype, device="cuda"), rows(T, H, dtype, gen, 16)
+    rstd = torch.empty(T, device="cuda")
+    g.add_rms_norm(x, w, y, residual=res if given else None, h=h, rstd=rstd, eps=EPS, p=p, rng=words)
+    # the mask of a plain call on ones, which its own test checks
+    keep = torch.empty(T, H, device="cuda")
+    g.dropout(torch.ones_like(keep), keep, p, words)
+    want_h, want_r, want_y = ref.add_rms_norm(x.cpu(), res.cpu() if given else None, w.cpu(), EPS,
+                                              keep.cpu().double())
+    sizes = x.cpu().double().abs() * 2 + (res.cpu().double().abs() if given else 0.0)
+    close(h, want_h, dtype, sizes, 2.0 ** -22, "h")
+    close(rstd, want_r, torch.float32, what="rstd")
+    close(y, want_y, dtype, sizes * want_r[:, None] * w.cpu().double().abs(), what="y")
+
+
+@gpu
 def test_norm_without_residual_and_in_place(g):
     gen = torch.Generator().manual_seed(8)
     x, res = rows(33, 520, torch.bfloat16, gen), rows(33, 520, torch.bfloat16, gen)
