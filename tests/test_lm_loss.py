@@ -264,6 +264,39 @@ def test_same_bits_on_another_stream_in_a_graph_and_after_other_sizes(g):
 
 
 @gpu
+def test_weight_past_32_bits(g):
+    """A weight of more than 2^32 elements: the last rows of the vocabulary count and get theirs."""
+    T, H, V = 5, 32776, 131100
+    gen = torch.Generator("cuda").manual_seed(12)
+    w = torch.randn(V, H, device="cuda", dtype=torch.bfloat16, generator=gen)
+    w *= 1.5 / math.sqrt(H)
+    t = torch.tensor([V - 1, 0, V - 300, IGNORE, V - 1], device="cuda")
+    x = (torch.randn(T, H, device="cuda", generator=gen) + 3.0 * w[t.clamp(min=0)].float()).bfloat16()
+    loss, lse, mean = forward(g, x, w, t)
+    z = torch.cat([x.double() @ w[a:a + 8192].double().T for a in range(0, V, 8192)], 1)
+    counted = t != IGNORE
+    want = torch.logsumexp(z, 1)
+    at = t.clamp(min=0)
+    rows = torch.arange(T, device="cuda")
+    assert torch.all((lse - want)[counted].abs() <= 1e-4)
+    assert torch.all((loss - (want - z[rows, at]))[counted].abs() <= 2e-4)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    g.linear_cross_entropy_backward(x, w, t, lse, mean[1:], dx, dw)
+    p = torch.softmax(z, 1)
+    p[rows, at] -= 1.0
+    p = torch.where(counted[:, None], p / 4, 0.0)
+    last = V - 400
+    tail = p[:, last:].T @ x.double()
+    assert float((dw[last:].double() - tail).norm() / tail.norm()) < 4e-3
+    head = p[:, :400].T @ x.double()
+    assert float((dw[:400].double() - head).norm() / head.norm()) < 4e-3
+    want_dx = sum(p[:, a:a + 8192] @ w[a:a + 8192].double() for a in range(0, V, 8192))
+    assert float((dx.double() - want_dx).norm() / want_dx.norm()) < 4e-3
+    del w, dw, z, p
+    torch.cuda.empty_cache()
+
+
+@gpu
 def test_refusals(g):
     x, w, t = (v.cuda() for v in make(16, 64, 100, 1))
     loss, lse, mean = (torch.full((n,), 7.0, device="cuda") for n in (16, 16, 2))

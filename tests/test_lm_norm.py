@@ -292,6 +292,40 @@ def test_norm_in_8_bits(g, T, H, form, dtype):
 
 
 @gpu
+def test_norm_past_32_bits(g):
+    """More than 2^32 elements: the last rows, forward and backward, with dropout."""
+    T, H, dt = 2 ** 19 + 5, 8200, torch.bfloat16
+    gen = torch.Generator().manual_seed(77)
+    one = rows(1, H, dt, gen)
+    x = one.repeat(T, 1)
+    x[-3:] = rows(3, H, dt, gen)
+    w = rows(1, H, dt, gen)[0]
+    y, h, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(T, device="cuda")
+    words = (3, 2 ** 34)
+    g.add_rms_norm(x, w, y, h=h, rstd=rstd, eps=EPS, p=0.2, rng=rng_words(*words))
+    groups = H // 8
+    keep = ref.keep_factor(3, H, 0.2, (words[0], words[1] + (T - 3) * groups))
+    tail = x[-3:].cpu()
+    want_h, want_r, want_y = ref.add_rms_norm(tail, None, w.cpu(), EPS, keep)
+    close(h[-3:], want_h, dt, what="h")
+    close(y[-3:], want_y, dt, what="y")
+    dx, dw = y, torch.empty_like(w)
+    g.add_rms_norm_backward(x, h, w, rstd, dx, dw, p=0.2, rng=rng_words(*words))
+    want = ref.add_rms_norm_backward(tail, h[-3:].cpu(), w.cpu(), rstd[-3:].cpu(), None, keep)
+    close(dx[-3:], want[0], dt, want[3] * 2, what="dx")
+    total = torch.zeros(H, dtype=torch.float64, device="cuda")
+    size = torch.zeros_like(total)
+    for a in range(0, T, 2 ** 15):
+        part = x[a:a + 2 ** 15].double() * h[a:a + 2 ** 15].double() * rstd[a:a + 2 ** 15, None].double()
+        total += part.sum(0)
+        size += part.abs().sum(0)
+    # sums of thousands of rows in 32 bits: 2^-24 for each of the about 2^12 additions of a column
+    close(dw, total.cpu(), dt, size.cpu(), 2.0 ** -12, what="dw")
+    del x, y, h, dx
+    torch.cuda.empty_cache()
+
+
+@gpu
 def test_norm_of_infinities_and_nan(g):
     x = torch.randn(4, 512, device="cuda")
     x[1, 3], x[2, 5] = float("inf"), float("nan")
