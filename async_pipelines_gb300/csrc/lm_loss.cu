@@ -228,6 +228,10 @@ int check_common(const gemm_ws* h, const uint16_t* x, int64_t ldx, const uint16_
   return GEMM_WS_OK;
 }
 
+ce::Targets targets(const void* target, int target_bytes, int64_t ignore, int64_t V) {
+  return {target, target_bytes == 8, ignore, static_cast<int>(V)};
+}
+
 ce::PackParams pack_params(const Plan& q, uint8_t* ws, const uint16_t* x, int64_t ldx,
                            const void* target, int target_bytes, int64_t ignore, int64_t T,
                            int64_t H, int64_t V, int num_sms) {
@@ -235,12 +239,9 @@ ce::PackParams pack_params(const Plan& q, uint8_t* ws, const uint16_t* x, int64_
   std::memset(&p, 0, sizeof p);
   p.x = x;
   p.ldx = ldx;
-  p.target = target;
-  p.wide_target = target_bytes == 8;
-  p.ignore = ignore;
+  p.given = targets(target, target_bytes, ignore, V);
   p.rows = static_cast<int>(T);
   p.cols = static_cast<int>(H);
-  p.vocab = static_cast<int>(V);
   p.wide = !odd(x, 16) && ldx % 8 == 0;
   p.padded = static_cast<int>(round_up(T, 128));
   int64_t chunk = ceil_div(p.padded, int64_t{8} * num_sms);
@@ -347,33 +348,44 @@ int gemm_ws_linear_ce(gemm_ws_t* h, const uint16_t* x, int64_t ldx, const uint16
   p.target_logit = pack.target_logit;
   p.part = reinterpret_cast<float2*>(ws + q.part);
   p.carry = q.carry;
-  if (!operand(h, &job.tmA, pack.packed, H, q.rows, q.pitch, false, p.a_rows) ||
-      !operand(h, &job.tmB, weight, H, V, ldw, false, q.logits.bn / q.logits.cg))
+  p.slots = static_cast<int>(q.slots);
+  p.result = {loss, lse, mean};
+  p.done = h->work + 3;
+  const int64_t units = ceil_div(T, ce::BM * q.logits.cg) * ceil_div(V, q.logits.bn);
+  if (!operand(h, &job.tmB, weight, H, V, ldw, false, q.logits.bn / q.logits.cg))
     return GEMM_WS_ERR_CUDA;
+  DeviceGuard guard(h->device);
+
+  // Up to 128 rows that the TMA can read where they lie are not packed: each row
+  // has its own sums, so an uncounted one touches nothing.
+  p.direct = T <= ce::BM && pack.wide;
+  p.join = p.direct && T <= ce::JOIN_FEW;
+  p.rows = static_cast<int>(T);
+  p.given = pack.given;
+  if (!(p.direct ? operand(h, &job.tmA, x, H, T, ldx, false, p.a_rows)
+                 : operand(h, &job.tmA, pack.packed, H, q.rows, q.pitch, false, p.a_rows)))
+    return GEMM_WS_ERR_CUDA;
+  rc = GEMM_WS_OK;
+  if (!p.direct)
+    rc = launch(h, ce::pack_kernel, ceil_div(pack.padded, pack.chunk), ce::PACK_THREADS, 0, 1, s, pack);
+  if (rc == GEMM_WS_OK) rc = launch_product<ce::LSE>(h, q.logits, units, p, s);
+  if (rc != GEMM_WS_OK || p.join) return rc;
 
   ce::JoinParams join;
   std::memset(&join, 0, sizeof join);
   join.part = p.part;
   join.part_stride = T;
-  join.slots = static_cast<int>(q.slots);
+  join.slots = p.slots;
+  join.direct = p.direct;
+  join.given = p.given;
   join.place = pack.place;
   join.count = pack.count;
   join.target_logit = pack.target_logit;
   join.rows = static_cast<int>(T);
-  join.loss = loss;
-  join.lse = lse;
-  join.mean = mean;
+  join.result = p.result;
   join.block_sum = reinterpret_cast<float*>(ws + q.block_sum);
-  join.done = h->work + 3;
-
-  DeviceGuard guard(h->device);
-  rc = launch(h, ce::pack_kernel, ceil_div(pack.padded, pack.chunk), ce::PACK_THREADS, 0, 1, s, pack);
-  if (rc == GEMM_WS_OK)
-    rc = launch_product<ce::LSE>(
-        h, q.logits, ceil_div(T, ce::BM * q.logits.cg) * ceil_div(V, q.logits.bn), p, s);
-  if (rc == GEMM_WS_OK)
-    rc = launch(h, ce::join_kernel, q.blocks, ce::JOIN_ROWS * ce::JOIN_LANES, 0, 1, s, join);
-  return rc;
+  join.done = p.done;
+  return launch(h, ce::join_kernel, q.blocks, ce::JOIN_ROWS * ce::JOIN_LANES, 0, 1, s, join);
 }
 
 int gemm_ws_linear_ce_backward(gemm_ws_t* h, const uint16_t* x, int64_t ldx,

@@ -70,6 +70,7 @@ static_assert(SMEM_BYTES <= 232448, "exceeds the 227 KiB per-CTA shared memory")
 // 1e-6; and 256 where few tokens leave them waiting for memory anyway. (The
 // gradients' products, which end in bf16, need none of it.)
 constexpr int CUT_K = 1024, CUT_K_FEW = 256;
+constexpr int JOIN_FEW = 8;
 constexpr float LOG2E = 1.4426950408889634f;
 
 enum Mode { LSE = 0, GRAD = 1, SUMS = 2 };
@@ -97,6 +98,25 @@ struct Job {
   int out;              // Output
 };
 
+// The targets as the caller gives them.
+struct Targets {
+  const void* at;
+  int wide;         // int64, else int32
+  int64_t ignore;
+  int vocab;
+  __device__ __forceinline__ int64_t raw(int row) const {
+    return wide ? static_cast<const int64_t*>(at)[row]
+                : static_cast<int64_t>(static_cast<const int*>(at)[row]);
+  }
+  __device__ __forceinline__ bool inside(int64_t t) const { return t >= 0 && t < vocab; }
+};
+
+// Where the forward pass's results go.
+struct Results {
+  float *loss, *lse;
+  float* mean;      // two, or NULL
+};
+
 struct Params {
   Job job[2];
   int jobs;
@@ -114,6 +134,16 @@ struct Params {
   int cut_k;                 // K of one accumulator, a multiple of 128 (the same in both)
   int carry;                 // one row of tiles: a CTA keeps its sums over its tiles
   const float *lse, *grad;   // [row]: lse, and g
+  // LSE of at most 128 rows: x itself is A, so nothing is packed; and with at most
+  // JOIN_FEW rows the CTA that ends last joins the sums, so that the pass is one
+  // launch. (It is one SM's work: 61 rows so take 10 us longer than with a launch.)
+  int direct;
+  int join;
+  int rows;
+  int slots;
+  Targets given;
+  Results result;
+  uint32_t* done;            // CTAs that ended; zero at launch, left zero
   uint32_t* status;
   unsigned long long timeout_ns;
 };
@@ -489,7 +519,14 @@ __device__ __forceinline__ void epilogue_logits(const Params& p, uint32_t sbase,
     int target = -1;   // the target's column in this tile, if in it
     float lse = 0.0f, grad = 0.0f;
     if (row < count) {
-      target = p.target[row] - p.col0 - w.n0;
+      int t;
+      if (MODE == LSE && p.direct) {
+        const int64_t raw = p.given.raw(row);
+        t = raw != p.given.ignore && p.given.inside(raw) ? static_cast<int>(raw) : -1;
+      } else {
+        t = p.target[row];
+      }
+      target = t - p.col0 - w.n0;
       if (MODE == GRAD) {
         lse = p.lse[row];
         grad = p.grad[row];
@@ -624,6 +661,86 @@ __device__ __forceinline__ void epilogue_sums(const Params& p, uint32_t sbase, u
   me.reuse();
 }
 
+// ------------------------------------------------------------ joining the sums
+
+// (top, sum) and (v.x, v.y) as one maximum and sum.
+__device__ __forceinline__ void join_pair(float& top, float& sum, float2 v) {
+  const float next = fmaxf(top, v.x), base = next == -INFINITY ? 0.0f : next;
+  sum = sum * exp_diff(top, base) + v.y * exp_diff(v.x, base);
+  top = next;
+}
+
+// The pairs of the lanes that are equal modulo `group`, in each of them. The lower
+// lane's pair comes first on both sides, so that both get the same bits.
+__device__ __forceinline__ void join_lanes(float& top, float& sum, int group) {
+  for (int o = 16; o >= group; o >>= 1) {
+    const float2 a = make_float2(top, sum);
+    const float2 b =
+        make_float2(__shfl_xor_sync(0xffffffffu, top, o), __shfl_xor_sync(0xffffffffu, sum, o));
+    const bool low = (threadIdx.x & o) == 0;
+    top = low ? a.x : b.x;
+    sum = low ? a.y : b.y;
+    join_pair(top, sum, low ? b : a);
+  }
+}
+
+__device__ __forceinline__ void write_mean(const Results& r, float total, int counted) {
+  if (!r.mean) return;
+  const float share = counted > 0 ? 1.0f / static_cast<float>(counted) : 0.0f;
+  r.mean[0] = counted > 0 ? total * share : 0.0f;
+  r.mean[1] = share;
+}
+
+// lse and loss of all rows, at most JOIN_FEW, and the mean, by the CTA that ends
+// last, from the CTAs' partial maxima and sums. A warp's lanes are the rows,
+// rounded up to a power of two, and as many slots side by side as fit; the order in
+// which they are joined is fixed.
+__device__ __forceinline__ void join_last(const Params& p, uint8_t* smem) {
+  constexpr int WARPS = THREADS / 32;
+  float2* box = reinterpret_cast<float2*>(smem);
+  uint32_t* ended = reinterpret_cast<uint32_t*>(smem + WARPS * 32 * sizeof(float2));
+  __threadfence();   // this thread's partial sums, before the count of CTAs
+  __syncthreads();
+  if (threadIdx.x == 0) *ended = atomicAdd(p.done, 1u);
+  __syncthreads();
+  if (*ended != gridDim.x - 1) return;
+  __threadfence();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  int group = 1;
+  while (group < p.rows) group *= 2;
+  const int row = lane % group;
+  float top = -INFINITY, sum = 0.0f;
+  if (row < p.rows) {
+#pragma unroll 8
+    for (int s = warp * (32 / group) + lane / group; s < p.slots; s += WARPS * (32 / group))
+      join_pair(top, sum, __ldcg(p.part + s * p.part_stride + row));
+  }
+  join_lanes(top, sum, group);
+  box[warp * 32 + lane] = make_float2(top, sum);
+  __syncthreads();
+  if (warp > 0) return;
+  for (int w = 1; w < WARPS; ++w) join_pair(top, sum, box[w * 32 + lane]);
+  float loss = 0.0f;
+  int counted = 0;
+  if (lane < p.rows) {
+    const int64_t t = p.given.raw(row);
+    counted = t != p.given.ignore;
+    const float rest = counted ? logf(sum) : 0.0f;
+    const float logit = p.given.inside(t) ? __ldcg(p.target_logit + row) : NAN;
+    loss = counted ? (top - logit) + rest : 0.0f;
+    p.result.lse[row] = counted ? top + rest : 0.0f;
+    p.result.loss[row] = loss;
+  }
+  for (int o = 16; o > 0; o >>= 1) {
+    loss += __shfl_xor_sync(0xffffffffu, loss, o);
+    counted += __shfl_xor_sync(0xffffffffu, counted, o);
+  }
+  if (lane == 0) {
+    write_mean(p.result, loss, counted);
+    *p.done = 0u;
+  }
+}
+
 // ------------------------------------------------------------ product kernel
 
 template <int CG, int MODE>
@@ -675,7 +792,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
   // The set-up above overlaps the previous kernel's end; nothing below does.
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
-  const int count = *p.count;
+  const int count = MODE == LSE && p.direct ? p.rows : *p.count;
 
   if (warp == WARP_A || warp == WARP_B) {
     if (lane == 0) producer<CG>(p, sbase, rank, warp == WARP_A, count, wd);
@@ -698,6 +815,8 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
     else
       tmem_dealloc_pair(tmem, ACC_BUFS * BN_MAX);
   }
+  if constexpr (MODE == LSE && CG == 1)
+    if (p.join) join_last(p, smem);
 }
 
 // ------------------------------------------------------------ packing the counted rows
@@ -705,10 +824,8 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
 struct PackParams {
   const uint16_t* x;          // T x H bf16
   int64_t ldx;
-  const void* target;         // T int64 or int32
-  int wide_target;            // int64
-  int64_t ignore;
-  int rows, cols, vocab;
+  Targets given;
+  int rows, cols;
   int padded;                 // rows, rounded up to a multiple of 128
   int wide;                   // x's rows allow 16-byte accesses
   int chunk;                  // rows of a block, at most PACK_THREADS
@@ -725,11 +842,6 @@ struct PackParams {
 
 constexpr int PACK_THREADS = 256;
 constexpr int NO_ROW = -0x7FFFFFFF - 1;
-
-__device__ __forceinline__ int64_t target_of(const PackParams& p, int row) {
-  return p.wide_target ? static_cast<const int64_t*>(p.target)[row]
-                       : static_cast<int64_t>(static_cast<const int*>(p.target)[row]);
-}
 
 // The sum over the block of a value a thread, in every thread.
 __device__ __forceinline__ int block_sum(int v, int* box) {
@@ -757,7 +869,7 @@ __global__ void __launch_bounds__(PACK_THREADS) pack_kernel(const __grid_constan
   int before = 0, all = 0;
 #pragma unroll 4
   for (int r = threadIdx.x; r < p.rows; r += PACK_THREADS) {
-    const int c = target_of(p, r) != p.ignore;
+    const int c = p.given.raw(r) != p.given.ignore;
     all += c;
     before += r < r0 ? c : 0;
   }
@@ -766,8 +878,8 @@ __global__ void __launch_bounds__(PACK_THREADS) pack_kernel(const __grid_constan
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.count = all;
   const int row = r0 + threadIdx.x;
   const bool mine = threadIdx.x < p.chunk && row < r1;
-  const int64_t t = mine && row < p.rows ? target_of(p, row) : p.ignore;
-  const bool counted = mine && t != p.ignore;
+  const int64_t t = mine && row < p.rows ? p.given.raw(row) : p.given.ignore;
+  const bool counted = mine && t != p.given.ignore;
   const unsigned vote = __ballot_sync(0xffffffffu, counted);
   if ((threadIdx.x & 31) == 0) box[threadIdx.x >> 5] = __popc(vote);
   __syncthreads();
@@ -776,7 +888,7 @@ __global__ void __launch_bounds__(PACK_THREADS) pack_kernel(const __grid_constan
   if (mine) {
     if (row < p.rows) p.place[row] = counted ? rank : -1;
     if (counted) {
-      const bool inside = t >= 0 && t < p.vocab;
+      const bool inside = p.given.inside(t);
       p.target_out[rank] = inside ? static_cast<int>(t) : -1;
       if (p.target_logit) p.target_logit[rank] = inside ? 0.0f : __int_as_float(0x7FC00000);
       if (p.lse_out) {
@@ -816,23 +928,18 @@ struct JoinParams {
   const float2* part;
   int64_t part_stride;
   int slots;
+  int direct;           // the rows are the tokens: `given`; else `place` and `count` say which
+  Targets given;
   const int* place;
   const int* count;
   const float* target_logit;
   int rows;
-  float *loss, *lse, *mean;   // mean may be NULL
-  float* block_sum;           // [block]
-  uint32_t* done;             // blocks finished; zero at launch, left zero
+  Results result;
+  float* block_sum;     // [block]
+  uint32_t* done;       // blocks finished; zero at launch, left zero
 };
 
 constexpr int JOIN_ROWS = 32, JOIN_LANES = 32;
-
-// (top, sum) and (v.x, v.y) as one maximum and sum.
-__device__ __forceinline__ void join_pair(float& top, float& sum, float2 v) {
-  const float next = fmaxf(top, v.x), base = next == -INFINITY ? 0.0f : next;
-  sum = sum * exp_diff(top, base) + v.y * exp_diff(v.x, base);
-  top = next;
-}
 
 // lse and loss of 32 rows a block, from the partial maxima and sums: a warp
 // reads a slot's 32 rows at once, JOIN_LANES slots apart; then a warp joins the
@@ -849,11 +956,21 @@ __global__ void __launch_bounds__(JOIN_ROWS* JOIN_LANES)
   const int x = threadIdx.x % JOIN_ROWS, lane = threadIdx.x / JOIN_ROWS;
   {
     const int row = blockIdx.x * JOIN_ROWS + x;
-    const int at = row < p.rows ? p.place[row] : -1;
+    int at = -1;
+    bool known = true;   // the target is in the vocabulary
+    if (row < p.rows) {
+      if (p.direct) {
+        const int64_t t = p.given.raw(row);
+        at = t != p.given.ignore ? row : -1;
+        known = p.given.inside(t);
+      } else {
+        at = p.place[row];
+      }
+    }
     float top = -INFINITY, sum = 0.0f;
     if (lane == 0) {
       counted[x] = at >= 0;
-      logit[x] = at >= 0 ? p.target_logit[at] : 0.0f;
+      logit[x] = at < 0 ? 0.0f : known ? p.target_logit[at] : NAN;
     }
     if (at >= 0) {
       constexpr int AHEAD = 8;   // loads in flight
@@ -880,22 +997,13 @@ __global__ void __launch_bounds__(JOIN_ROWS* JOIN_LANES)
   const int row = blockIdx.x * JOIN_ROWS + lane;   // this warp's row
   const float2 mine = box[x][lane];
   float top = mine.x, sum = mine.y, loss = 0.0f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    // the lower lane's pair first, on both sides, so that both get the same bits
-    float2 a = make_float2(top, sum);
-    float2 b = make_float2(__shfl_xor_sync(0xffffffffu, top, o), __shfl_xor_sync(0xffffffffu, sum, o));
-    const bool low = (x & o) == 0;
-    top = low ? a.x : b.x;
-    sum = low ? a.y : b.y;
-    join_pair(top, sum, low ? b : a);
-  }
+  join_lanes(top, sum, 1);
   if (x == 0) {
     if (row < p.rows) {
       const float rest = counted[lane] ? logf(sum) : 0.0f;
       loss = counted[lane] ? (top - logit[lane]) + rest : 0.0f;
-      p.lse[row] = counted[lane] ? top + rest : 0.0f;
-      p.loss[row] = loss;
+      p.result.lse[row] = counted[lane] ? top + rest : 0.0f;
+      p.result.loss[row] = loss;
     }
     sums[lane] = loss;
   }
@@ -905,7 +1013,7 @@ __global__ void __launch_bounds__(JOIN_ROWS* JOIN_LANES)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
   }
-  if (!p.mean) return;
+  if (!p.result.mean) return;
   if (gridDim.x > 1) {
     if (threadIdx.x == 0) {
       p.block_sum[blockIdx.x] = loss;
@@ -924,11 +1032,10 @@ __global__ void __launch_bounds__(JOIN_ROWS* JOIN_LANES)
     loss = 0.0f;
     for (int l = 0; l < JOIN_LANES; ++l) loss += sums[l];
   }
+  const int t = threadIdx.x;   // direct: at most 128 rows
+  const int n = p.direct ? __syncthreads_count(t < p.rows && p.given.raw(t) != p.given.ignore) : *p.count;
   if (threadIdx.x == 0) {
-    const int n = *p.count;
-    const float share = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
-    p.mean[0] = loss * share;
-    p.mean[1] = share;
+    write_mean(p.result, loss, n);
     *p.done = 0u;
   }
 }

@@ -228,7 +228,7 @@ class LmOps:
         x: (tokens, hidden), weight: (vocab, hidden), bf16; targets: (tokens,)
         int64 or int32. loss, lse: (tokens,) f32; mean: 2 f32, the mean loss
         over the counted tokens and 1 / their number. A token whose target is
-        ignore_index is not counted: loss and lse 0, its row not read; one
+        ignore_index is not counted: loss and lse 0, its row plays no part; one
         whose target is outside the vocabulary has loss NaN. Without a
         workspace (uint8, linear_cross_entropy_workspace bytes) the call takes
         one from torch's allocator.

@@ -102,7 +102,7 @@ int gemm_ws_add_rms_norm_backward(gemm_ws_t* h, int dtype, const void* dy, int64
  *  - x: tokens x hidden bf16; weight: vocab x hidden bf16; target: tokens
  *    int64 (target_bytes 8) or int32 (4).
  *  - A token whose target is `ignore` is not counted: its loss and lse are 0
- *    and its row of x is not read (it may hold anything). A counted token
+ *    and its row of x plays no part (it may hold anything). A counted token
  *    whose target is outside [0, vocab) has loss NaN, and no gradient.
  *  - loss, lse: tokens fp32; mean: two fp32, the mean loss over the counted
  *    tokens and 1 / their number (both 0 with none), or NULL.
@@ -112,7 +112,8 @@ int gemm_ws_add_rms_norm_backward(gemm_ws_t* h, int dtype, const void* dy, int64
  *    may lie anywhere). 0 <= tokens, 1 <= vocab, 8 <= hidden, each < 2^31,
  *    tokens * hidden, vocab * hidden and tokens * vocab < 2^40.
  * Products in bf16 with fp32 sums in tensor memory; everything after them in
- * fp32. Launches three kernels. */
+ * fp32. Launches three kernels; two for up to 128 tokens whose rows lie on
+ * 16-byte boundaries, one for up to 8 of them. */
 int gemm_ws_linear_ce(gemm_ws_t* h, const uint16_t* x, int64_t ldx, const uint16_t* weight,
                       int64_t ldw, const void* target, int target_bytes, int64_t ignore,
                       float* loss, float* lse, float* mean, int64_t tokens, int64_t hidden,

@@ -137,6 +137,31 @@ def test_loss_and_gradients(g, T, H, V, ignored):
 
 
 @gpu
+@pytest.mark.parametrize("T", [1, 2, 3, 5, 8, 9, 32, 33, 100, 128])
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("V", [37, 70000])
+def test_few_tokens(g, T, shift, V):
+    """Rows read where they lie (or packed, when they are not aligned), joined in one launch or two."""
+    x, w, t = make(T, 520, V, T + shift, 0.3 if T > 2 else 0.0, int32=shift == 1)
+    if T > 3:
+        t[2] = V      # outside the vocabulary: NaN, which the mean shows too
+    got = forward(g, on_gpu(x, 0 if shift else 8, shift), w.cuda(), t.cuda())
+    loss, lse, mean = got
+    if T > 3:
+        assert loss[2].isnan() and torch.isfinite(lse[2]) and mean[0].isnan()
+        keep = torch.arange(T) != 2
+        n = int((t != IGNORE).sum())
+        assert abs(float(mean[1]) - 1.0 / n) <= 2.0 ** -24
+        want = ref.linear_cross_entropy(x[keep], w, t[keep].long(), IGNORE)
+        tol = math.sqrt(520) * 2.0 ** -23 * (x.double().abs() @ w.double().abs().T).amax(1) + \
+            2.0 ** -20 * 20
+        assert torch.all((loss.cpu().double()[keep] - want[0]).abs() <= 2 * tol[keep])
+        assert torch.all((lse.cpu().double()[keep] - want[1]).abs() <= tol[keep])
+    else:
+        check_forward(got, x, w, t)
+
+
+@gpu
 def test_strides_grad_of_each_token_and_one_gradient_only(g):
     T, H, V = 333, 264, 3001
     x, w, t = make(T, H, V, 9, 0.2)
