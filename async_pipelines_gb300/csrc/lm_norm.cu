@@ -91,9 +91,11 @@ struct Team {
 // Longer rows take a block. With few rows (less than two for each SM) every
 // thread takes one group, for the shortest row; with many, two, and from 2048
 // columns four, so that an SM has more bytes in flight for the threads that it
-// can hold (8192 x 8192 bf16: 78 us with four, 86 with two). On the general path, whose groups move element by element, a
-// thread takes one group wherever a block can hold the row so.
-Team pick_team(const gemm_ws* h, int64_t rows, int64_t cols, gws::Path path) {
+// can hold (8192 x 8192 bf16: 78 us with four, 86 with two); beyond 8192 columns
+// always four. On the general path, whose loads take many registers, a row longer
+// than a warp's 32 groups takes a block with `any_vpt` groups a thread (8192 x 8191
+// bf16, forward: 188 us with two, 264 with one; fp32 169 and 152; backward 376 and 286).
+Team pick_team(const gemm_ws* h, int64_t rows, int64_t cols, gws::Path path, int any_vpt) {
   const int64_t groups = ceil_div(cols, gws::GROUP);
   const bool any = path == gws::ANY;
   Team t;
@@ -103,7 +105,8 @@ Team pick_team(const gemm_ws* h, int64_t rows, int64_t cols, gws::Path path) {
     t.rows = rows >= 8 * h->num_sms ? 8 : rows >= 2 * h->num_sms ? 4 : 1;
     return t;
   }
-  t.vpt = groups > 1024 ? 4 : any || rows < 2 * h->num_sms ? 1 : groups >= 256 ? 4 : 2;
+  const bool many = rows >= (any ? 8 : 2) * h->num_sms;
+  t.vpt = groups > 1024 ? 4 : !many ? 1 : any ? any_vpt : groups >= 256 ? 4 : 2;
   t.threads = static_cast<int>(ceil_div(ceil_div(groups, t.vpt), 32) * 32);
   t.rows = 1;
   return t;
@@ -274,10 +277,10 @@ int gemm_ws_dropout(gemm_ws_t* h, int dtype, const void* x, int64_t ldx, void* y
   q.rows = rows;
   q.cols = static_cast<int>(cols);
   q.groups = ceil_div(cols, gws::GROUP);
-  q.wide = mx.wide() && my.wide();
+  const bool wide = mx.wide() && my.wide();
   q.row_threads = 1;
   while (q.row_threads < gws::DROP_THREADS && q.row_threads < q.groups) q.row_threads *= 2;
-  const bool flat = q.wide && cols % gws::GROUP == 0 && (rows == 1 || (ldx == cols && ldy == cols));
+  const bool flat = wide && cols % gws::GROUP == 0 && (rows == 1 || (ldx == cols && ldy == cols));
   int64_t blocks = ceil_div(rows, gws::DROP_THREADS / q.row_threads);
   if (flat) {
     q.groups *= rows;
@@ -349,9 +352,9 @@ int gemm_ws_add_rms_norm(gemm_ws_t* h, int dtype, const void* x, int64_t ldx,
   q.rows = rows;
   q.cols = static_cast<int>(cols);
   q.eps = eps;
-  q.wide = in[0].wide() && (!residual || in[1].wide()) &&
+  const bool wide = in[0].wide() && (!residual || in[1].wide()) &&
            reinterpret_cast<uintptr_t>(weight) % 16 == 0 && (!hidden || mh.wide()) && my.wide();
-  const gws::Path path = pick_path(q.wide, cols, q.drop);
+  const gws::Path path = pick_path(wide, cols, q.drop);
   DeviceGuard guard(h->device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   gws::NormRing ring;
@@ -367,7 +370,7 @@ int gemm_ws_add_rms_norm(gemm_ws_t* h, int dtype, const void* x, int64_t ldx,
                     h->num_sms, gws::RING_THREADS, gws::RING_BYTES, s, ring);
     }
   }
-  const Team t = pick_team(h, rows, cols, path);
+  const Team t = pick_team(h, rows, cols, path, size == 2 ? 2 : 1);
   q.team = t.threads;
   switch (dtype) {
     case GEMM_WS_BF16: return launch_norm<__nv_bfloat16>(h, output, t, path, q, s);
@@ -439,9 +442,9 @@ int gemm_ws_add_rms_norm_backward(gemm_ws_t* h, int dtype, const void* dy, int64
   q.lddres = lddr;
   q.rows = rows;
   q.cols = static_cast<int>(cols);
-  q.wide = in[0].wide() && (!dhidden || in[1].wide()) && in[2].wide() && out[0].wide() &&
+  const bool wide = in[0].wide() && (!dhidden || in[1].wide()) && in[2].wide() && out[0].wide() &&
            (!dresidual || out[1].wide()) && reinterpret_cast<uintptr_t>(weight) % 16 == 0;
-  const gws::Path path = pick_path(q.wide, cols, q.drop);
+  const gws::Path path = pick_path(wide, cols, q.drop);
   DeviceGuard guard(h->device);
   gws::NormGradRing ring;
   int vpt = 0;
@@ -457,7 +460,7 @@ int gemm_ws_add_rms_norm_backward(gemm_ws_t* h, int dtype, const void* dy, int64
       }
     }
   }
-  const Team t = pick_team(h, rows, cols, path);
+  const Team t = pick_team(h, rows, cols, path, 1);
   q.team = t.threads;
   switch (dtype) {
     case GEMM_WS_BF16: return launch_grad<__nv_bfloat16>(h, t, path, q, dweight, s);

@@ -233,42 +233,173 @@ __device__ __forceinline__ void unpack(const Raw<T>& raw, Pair (&v)[GROUP / 2]) 
 // dropout behind a branch.
 enum Path { ANY = 0, FAST = 1, DROP = 2 };
 
-// Columns [c, c + 8) of a row whose end is `cols`; past it zeros. WHOLE: not
-// ANY, so a group moves in 16-byte pieces and nothing is tested. Else `wide` says
-// whether rows start on such a boundary.
-template <bool WHOLE, typename T>
-__device__ __forceinline__ Raw<T> load_group(const T* row, int c, int cols, bool wide) {
-  const auto* src = reinterpret_cast<const typename Bits<sizeof(T)>::type*>(row) + c;
-  if (WHOLE || (wide && c + GROUP <= cols)) {
-    Raw<T> raw;
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) * GROUP / 16); ++i)
-      raw.w[i] = reinterpret_cast<const uint4*>(src)[i];
-    return raw;
-  }
-  if (c + GROUP <= cols) {
-    const uint32_t e[GROUP] = {src[0], src[1], src[2], src[3], src[4], src[5], src[6], src[7]};
-    return from_bits<T>(e);
-  }
-  uint32_t e[GROUP];
-#pragma unroll
-  for (int i = 0; i < GROUP; ++i) e[i] = c + i < cols ? src[i] : 0u;
-  return from_bits<T>(e);
+// Where a matrix lies: what may be read of it.
+struct Span {
+  uintptr_t lo, hi;
+};
+template <typename T>
+__device__ __forceinline__ Span span_of(const void* first, int64_t rows, int64_t ld, int cols) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(first);
+  return {lo, lo + ((rows - 1) * ld + cols) * sizeof(T)};
 }
 
-template <bool WHOLE, typename T>
-__device__ __forceinline__ void store_group(T* row, int c, int cols, bool wide, const Raw<T>& raw) {
-  auto* dst = reinterpret_cast<typename Bits<sizeof(T)>::type*>(row) + c;
-  if (WHOLE || (wide && c + GROUP <= cols)) {
+// out = the bytes [by, by + 4 W) of `in`, by < 16.
+template <int W>
+__device__ __forceinline__ void shift_bytes(uint32_t (&in)[W + 4], int by, uint32_t (&out)[W]) {
+  if (by & 8) {
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) * GROUP / 16); ++i)
-      reinterpret_cast<uint4*>(dst)[i] = raw.w[i];
-    return;
+    for (int i = 0; i < W + 2; ++i) in[i] = in[i + 2];
   }
-  if constexpr (!WHOLE) {
+  if (by & 4) {
 #pragma unroll
-    for (int i = 0; i < GROUP; ++i)
-      if (c + i < cols) dst[i] = static_cast<typename Bits<sizeof(T)>::type>(bits_of(raw, i));
+    for (int i = 0; i < W + 1; ++i) in[i] = in[i + 1];
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) out[i] = __funnelshift_r(in[i], in[i + 1], (by & 3) * 8);
+}
+
+template <typename T>
+constexpr int WORDS = sizeof(T) * GROUP / 4;   // of a group
+
+template <typename T>
+__device__ __forceinline__ void words_of(const Raw<T>& raw, uint32_t (&w)[WORDS<T>]) {
+#pragma unroll
+  for (int i = 0; i < WORDS<T> / 4; ++i) {
+    w[4 * i] = raw.w[i].x;
+    w[4 * i + 1] = raw.w[i].y;
+    w[4 * i + 2] = raw.w[i].z;
+    w[4 * i + 3] = raw.w[i].w;
+  }
+}
+
+// Columns [c, c + 8) of a row whose end is `cols`; past it zeros. WHOLE (not
+// ANY): a group moves in 16-byte pieces and nothing is tested. Else a group that
+// does not start on a 16-byte boundary is cut out of the 16-byte pieces around it,
+// where those lie within the matrix; at its two ends and the row's, single
+// elements. (8192 x 8191 bf16, forward: 398 us with single elements, 186 so.)
+template <bool WHOLE, typename T>
+__device__ __forceinline__ Raw<T> load_group(const T* row, int c, int cols, const Span& span) {
+  const auto* src = reinterpret_cast<const typename Bits<sizeof(T)>::type*>(row) + c;
+  constexpr int PIECES = WORDS<T> / 4;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(src);
+  const int off = static_cast<int>(at & 15);
+  const bool whole = c + GROUP <= cols;
+  Raw<T> raw;
+  if (WHOLE || (whole && off == 0)) {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) raw.w[i] = reinterpret_cast<const uint4*>(src)[i];
+  } else if (whole && at - off >= span.lo && at - off + 16 * (PIECES + 1) <= span.hi) {
+    uint32_t in[WORDS<T> + 4], out[WORDS<T>];
+#pragma unroll
+    for (int i = 0; i <= PIECES; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(at - off)[i];
+      in[4 * i] = v.x;
+      in[4 * i + 1] = v.y;
+      in[4 * i + 2] = v.z;
+      in[4 * i + 3] = v.w;
+    }
+    shift_bytes<WORDS<T>>(in, off, out);
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+      raw.w[i] = make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+  } else {
+    uint32_t e[GROUP];
+#pragma unroll
+    for (int i = 0; i < GROUP; ++i) e[i] = c + i < cols ? src[i] : 0u;
+    raw = from_bits<T>(e);
+  }
+  return raw;
+}
+
+// Stores columns [c, c + 8) (as many as there are) of thread t's group of a row of
+// `team` threads; WHOLE needs no other thread. Else the whole warp has to call it,
+// threads without a group with c >= cols: neighbouring threads hold neighbouring
+// groups, and where these do not start on a 16-byte boundary each thread stores the
+// 16-byte pieces that end in its group, with the rest of its left neighbour's; the
+// pieces at a warp's and the row's ends go as single elements. (Two bytes a store,
+// 8192 x 8191 bf16 took five times as long as 8192 x 8192.)
+template <bool WHOLE, typename T>
+__device__ __forceinline__ void store_group(T* row, int c, int cols, int t, int team,
+                                            const Raw<T>& raw) {
+  auto* dst = reinterpret_cast<typename Bits<sizeof(T)>::type*>(row) + c;
+  constexpr int PIECES = WORDS<T> / 4;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(dst);
+  const int off = static_cast<int>(at & 15);   // the same for all groups of the row
+  if constexpr (WHOLE) {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) reinterpret_cast<uint4*>(dst)[i] = raw.w[i];
+  } else {
+    uint32_t own[WORDS<T>], in[WORDS<T> + 4], out[WORDS<T>];
+    words_of(raw, own);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) in[i] = __shfl_up_sync(0xffffffffu, own[WORDS<T> - 4 + i], 1);
+    if (off == 0 && c + GROUP <= cols) {
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) reinterpret_cast<uint4*>(dst)[i] = raw.w[i];
+      return;
+    }
+    unsigned stored = 0;   // bit k: the k-th piece that touches the group is stored
+    if (off != 0) {
+#pragma unroll
+      for (int i = 0; i < WORDS<T>; ++i) in[4 + i] = own[i];
+      shift_bytes<WORDS<T>>(in, 16 - off, out);
+      // elements of the group in the piece that its left neighbour begins
+      const int lead = (16 - off) / static_cast<int>(sizeof(T));
+      const int lane = threadIdx.x & 31;
+#pragma unroll
+      for (int k = 0; k < PIECES; ++k) {
+        const int end = lead + k * 16 / static_cast<int>(sizeof(T));
+        if ((k > 0 || (lane > 0 && t > 0)) && c + end <= cols) {
+          reinterpret_cast<uint4*>(at - off)[k] =
+              make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]);
+          stored |= 1u << k;
+        }
+      }
+      // the right neighbour stores the piece that it ends
+      if (lane < 31 && t + 1 < team && c + GROUP + lead <= cols) stored |= 1u << PIECES;
+    }
+    if (stored != (2u << PIECES) - 1) {
+#pragma unroll
+      for (int i = 0; i < GROUP; ++i) {
+        const int piece = (off + i * static_cast<int>(sizeof(T))) / 16;
+        if (c + i < cols && !(off != 0 && (stored >> piece & 1)))
+          dst[i] = static_cast<typename Bits<sizeof(T)>::type>(bits_of(raw, i));
+      }
+    }
+  }
+}
+
+// The same for the 8 bytes of an e4m3 group.
+template <bool WHOLE>
+__device__ __forceinline__ void store_bytes(uint8_t* row, int c, int cols, int t, int team,
+                                            uint2 raw) {
+  uint8_t* dst = row + c;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(dst);
+  const int off = static_cast<int>(at & 7);
+  if constexpr (WHOLE) {
+    *reinterpret_cast<uint2*>(dst) = raw;
+  } else {
+    const unsigned long long own = raw.x | static_cast<unsigned long long>(raw.y) << 32;
+    const unsigned long long left = __shfl_up_sync(0xffffffffu, own, 1);
+    if (off == 0 && c + GROUP <= cols) {
+      *reinterpret_cast<uint2*>(dst) = raw;
+      return;
+    }
+    unsigned stored = 0;
+    if (off != 0) {
+      const int lane = threadIdx.x & 31, lead = 8 - off;
+      if (lane > 0 && t > 0 && c + lead <= cols) {
+        *reinterpret_cast<unsigned long long*>(at - off) = own << (8 * off) | left >> (8 * lead);
+        stored |= 1;
+      }
+      if (lane < 31 && t + 1 < team && c + GROUP + lead <= cols) stored |= 2;
+    }
+    if (stored != 3) {
+#pragma unroll
+      for (int i = 0; i < GROUP; ++i)
+        if (c + i < cols && !(off != 0 && (stored >> ((off + i) / 8) & 1)))
+          dst[i] = static_cast<uint8_t>((i < 4 ? raw.x : raw.y) >> (8 * (i % 4)));
+    }
   }
 }
 
@@ -385,8 +516,6 @@ struct NormParams {
   int cols;
   int team;                            // threads a row: 32 (blockDim / 32 rows a block), or all
   float eps;
-  int wide;                            // ANY: rows of x, residual, h, y and weight start on
-                                       // 16-byte boundaries
   Dropout drop;
 };
 
@@ -404,16 +533,18 @@ __global__ void __launch_bounds__(MOST) add_rms_norm_kernel(const __grid_constan
   const T* res = p.residual ? static_cast<const T*>(p.residual) + row * p.ldr : nullptr;
   const T* weight = static_cast<const T*>(p.weight);
   const int cols = p.cols, groups = (cols + GROUP - 1) / GROUP;
-  const bool wide = p.wide;
+  constexpr bool WHOLE = PATH != ANY;
+  const Span sx = span_of<T>(p.x, p.rows, p.ldx, cols), sr = span_of<T>(p.residual, p.rows, p.ldr, cols),
+             sw = span_of<T>(weight, 1, cols, cols);
 
   Raw<T> xr[VPT] = {}, rr[VPT], wr[VPT];
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
     const int g = k * team + t;
     if (g < groups) {
-      xr[k] = load_group<PATH != ANY>(x, g * GROUP, cols, wide);
-      if (res) rr[k] = load_group<PATH != ANY>(res, g * GROUP, cols, wide);
-      wr[k] = load_group<PATH != ANY>(weight, g * GROUP, cols, wide);
+      xr[k] = load_group<WHOLE>(x, g * GROUP, cols, sx);
+      if (res) rr[k] = load_group<WHOLE>(res, g * GROUP, cols, sr);
+      wr[k] = load_group<WHOLE>(weight, g * GROUP, cols, sw);
     }
   }
   const uint64_t seed = p.drop.rng[0];
@@ -437,7 +568,7 @@ __global__ void __launch_bounds__(MOST) add_rms_norm_kernel(const __grid_constan
     const int g = k * team + t;
     if (g < groups) {
       float w[GROUP];
-      unpack(wr[k], w);
+      if (Q == 1) unpack(wr[k], w);
       if (res) {
         float r[GROUP];
         unpack(rr[k], r);
@@ -449,8 +580,9 @@ __global__ void __launch_bounds__(MOST) add_rms_norm_kernel(const __grid_constan
         s.sum = fmaf(v[k][i], v[k][i], s.sum);
         if (Q == 1) s.max = max_nan(s.max, fabsf(v[k][i] * w[i]));
       }
-      if (p.h) store_group<PATH != ANY>(static_cast<T*>(p.h) + row * p.ldh, g * GROUP, cols, wide, pack<T>(v[k]));
     }
+    if (p.h && (PATH == ANY || g < groups))
+      store_group<WHOLE>(static_cast<T*>(p.h) + row * p.ldh, g * GROUP, cols, t, team, pack<T>(v[k]));
   }
   s = reduce_team<Q == 1>(s, team / 32, box);
   // r of the unrounded h, in 32 bits
@@ -472,8 +604,8 @@ __global__ void __launch_bounds__(MOST) add_rms_norm_kernel(const __grid_constan
       for (int i = 0; i < GROUP; ++i) v[k][i] = v[k][i] * r * w[i];
     }
     if (Q == 0) {
-      if (g < groups)
-        store_group<PATH != ANY>(static_cast<T*>(p.y) + row * p.ldy, g * GROUP, cols, wide, pack<T>(v[k]));
+      if (PATH == ANY || g < groups)
+        store_group<WHOLE>(static_cast<T*>(p.y) + row * p.ldy, g * GROUP, cols, t, team, pack<T>(v[k]));
     } else {
       if (Q == 2) {
         // the 16 groups of 128 columns sit on 16 neighbouring lanes
@@ -488,26 +620,19 @@ __global__ void __launch_bounds__(MOST) add_rms_norm_kernel(const __grid_constan
         if ((t & 15) == 0 && g < groups)
           p.scales[row * ((cols + QUANT_GROUP - 1) / QUANT_GROUP) + g / 16] = scale;
       }
-      if (g < groups) {
-        const float inv = 1.0f / scale;
-        uint32_t out[2];
+      const float inv = 1.0f / scale;
+      uint32_t out[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-              make_float2(v[k][4 * i] * inv, v[k][4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-          const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-              make_float2(v[k][4 * i + 2] * inv, v[k][4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
-          out[i] = lo | (hi << 16);
-        }
-        uint8_t* y = static_cast<uint8_t*>(p.y) + row * p.ldy + g * GROUP;
-        if (PATH != ANY || (wide && (g + 1) * GROUP <= cols)) {
-          *reinterpret_cast<uint2*>(y) = make_uint2(out[0], out[1]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < GROUP; ++i)
-            if (g * GROUP + i < cols) y[i] = static_cast<uint8_t>(out[i / 4] >> (8 * (i % 4)));
-        }
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(
+            make_float2(v[k][4 * i] * inv, v[k][4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+            make_float2(v[k][4 * i + 2] * inv, v[k][4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+        out[i] = lo | (hi << 16);
       }
+      if (PATH == ANY || g < groups)
+        store_bytes<WHOLE>(static_cast<uint8_t*>(p.y) + row * p.ldy, g * GROUP, cols, t, team,
+                           make_uint2(out[0], out[1]));
     }
   }
 }
@@ -641,7 +766,6 @@ struct NormGradParams {
   int64_t rows;
   int cols;
   int team;
-  int wide;                            // as above
   Dropout drop;
 };
 
@@ -650,15 +774,18 @@ struct NormGradParams {
 // one partial row, and dweight_kernel adds those in block order. So dweight
 // has the same bits on every run, whatever the timing.
 template <typename T, Path PATH, int VPT, int MOST>
-__global__ void __launch_bounds__(MOST, 1024 / MOST) add_rms_norm_grad_kernel(const __grid_constant__ NormGradParams p) {
+__global__ void __launch_bounds__(MOST, PATH == ANY ? 1 : 1024 / MOST)
+    add_rms_norm_grad_kernel(const __grid_constant__ NormGradParams p) {
   __shared__ SumMax box[2][32];
   extern __shared__ float share[];   // where a team is a warp: the block's sum of dweight
   grid_dependency_wait();
   grid_launch_dependents();
   const int team = p.team, t = threadIdx.x % team, teams = blockDim.x / team;
   const int cols = p.cols, groups = (cols + GROUP - 1) / GROUP;
-  const bool wide = p.wide;
+  constexpr bool WHOLE = PATH != ANY;
   const T* weight = static_cast<const T*>(p.weight);
+  const Span sy = span_of<T>(p.dy, p.rows, p.lddy, cols), sh = span_of<T>(p.h, p.rows, p.ldh, cols),
+             sd = span_of<T>(p.dh, p.rows, p.lddh, cols), sw = span_of<T>(weight, 1, cols, cols);
   const uint64_t seed = p.drop.rng[0], first = p.drop.rng[1];
   float acc[VPT][GROUP];
 #pragma unroll
@@ -677,9 +804,9 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) add_rms_norm_grad_kernel(co
     for (int k = 0; k < VPT; ++k) {
       const int g = k * team + t;
       if (g < groups) {
-        yr[k] = load_group<PATH != ANY>(dy, g * GROUP, cols, wide);
-        hr[k] = load_group<PATH != ANY>(h, g * GROUP, cols, wide);
-        if (dh) dr[k] = load_group<PATH != ANY>(dh, g * GROUP, cols, wide);
+        yr[k] = load_group<WHOLE>(dy, g * GROUP, cols, sy);
+        hr[k] = load_group<WHOLE>(h, g * GROUP, cols, sh);
+        if (dh) dr[k] = load_group<WHOLE>(dh, g * GROUP, cols, sd);
       }
     }
     const float r = p.rstd[row];
@@ -691,7 +818,7 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) add_rms_norm_grad_kernel(co
         float a[GROUP], n[GROUP], w[GROUP];
         unpack(yr[k], a);
         unpack(hr[k], n);
-        unpack(load_group<PATH != ANY>(weight, g * GROUP, cols, wide), w);
+        unpack(load_group<WHOLE>(weight, g * GROUP, cols, sw), w);
 #pragma unroll
         for (int i = 0; i < GROUP; ++i) {
           const float ni = n[i] * r;
@@ -710,13 +837,14 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) add_rms_norm_grad_kernel(co
         float a[GROUP], n[GROUP], w[GROUP];
         unpack(yr[k], a);
         unpack(hr[k], n);
-        unpack(load_group<PATH != ANY>(weight, g * GROUP, cols, wide), w);
+        unpack(load_group<WHOLE>(weight, g * GROUP, cols, sw), w);
         unpack(dr[k], d[k]);
 #pragma unroll
         for (int i = 0; i < GROUP; ++i) d[k][i] = fmaf(r, a[i] * w[i] - n[i] * rc, d[k][i]);
-        if (p.dres)
-          store_group<PATH != ANY>(static_cast<T*>(p.dres) + row * p.lddres, g * GROUP, cols, wide, pack<T>(d[k]));
       }
+      if (p.dres && (PATH == ANY || g < groups))
+        store_group<WHOLE>(static_cast<T*>(p.dres) + row * p.lddres, g * GROUP, cols, t, team,
+                           pack<T>(d[k]));
     }
     if (PATH == DROP || (PATH == ANY && p.drop.on)) {
       uint64_t counter[VPT];
@@ -728,8 +856,8 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST) add_rms_norm_grad_kernel(co
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int g = k * team + t;
-      if (g < groups)
-        store_group<PATH != ANY>(static_cast<T*>(p.dx) + row * p.lddx, g * GROUP, cols, wide, pack<T>(d[k]));
+      if (PATH == ANY || g < groups)
+        store_group<WHOLE>(static_cast<T*>(p.dx) + row * p.lddx, g * GROUP, cols, t, team, pack<T>(d[k]));
     }
   }
   if (!p.partial) return;
@@ -981,7 +1109,6 @@ struct DropoutParams {
   int cols;
   int64_t groups;      // FLAT: of the whole matrix; else of a row
   int row_threads;     // not FLAT: threads of a row, a power of two
-  int wide;            // not FLAT: rows start on 16-byte boundaries
   Dropout drop;
 };
 
@@ -1020,18 +1147,23 @@ __global__ void __launch_bounds__(DROP_THREADS) dropout_rows_kernel(const __grid
   grid_dependency_wait();
   grid_launch_dependents();
   const uint64_t seed = p.drop.rng[0], first = p.drop.rng[1];
-  const int per_block = DROP_THREADS / p.row_threads;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / p.row_threads;
-  if (row >= p.rows) return;
-  const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-  T* y = static_cast<T*>(p.y) + row * p.ldy;
+  const int team = p.row_threads, t = threadIdx.x % team;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (DROP_THREADS / team) + threadIdx.x / team;
+  const bool there = row < p.rows;
+  const T* x = static_cast<const T*>(p.x) + (there ? row : 0) * p.ldx;
+  T* y = static_cast<T*>(p.y) + (there ? row : 0) * p.ldy;
+  const Span sx = span_of<T>(p.x, p.rows, p.ldx, p.cols);
   const int groups = static_cast<int>(p.groups);
-  for (int g = threadIdx.x % p.row_threads; g < groups; g += p.row_threads) {
+  for (int g0 = 0; g0 < groups; g0 += team) {   // whole warps stay together for the stores
+    const int g = g0 + t;
+    const bool mine = there && g < groups;
+    Raw<T> raw = {};
+    if (mine) raw = load_group<false>(x, g * GROUP, p.cols, sx);
     float v[1][GROUP];
-    unpack(load_group<false>(x, g * GROUP, p.cols, p.wide), v[0]);
+    unpack(raw, v[0]);
     const uint64_t counter[1] = {first + static_cast<uint64_t>(row) * groups + g};
     if (p.drop.on) drop_groups(p.drop, seed, counter, v);
-    store_group<false>(y, g * GROUP, p.cols, p.wide, pack<T>(v[0]));
+    store_group<false>(y, (mine ? g : groups + t) * GROUP, p.cols, t, team, pack<T>(v[0]));
   }
 }
 

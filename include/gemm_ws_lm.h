@@ -19,7 +19,9 @@
  * nothing. Results have the same bits on every run.
  *
  * A matrix is `rows` rows of `cols` contiguous elements, `ld` elements from
- * one row to the next (ld >= cols). An output may be exactly one of the call's
+ * one row to the next (ld >= cols). What lies between two rows of an input may be
+ * read, and plays no part; between two rows of an output nothing is written. An
+ * output may be exactly one of the call's
  * inputs where that is said; any other overlap of an output with another
  * argument is refused.
  */

@@ -343,6 +343,66 @@ def test_norm_of_infinities_and_nan(g):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,H", [(1, 9), (5, 33), (3, 257), (40, 1001), (2, 8195), (1300, 77)])
+@pytest.mark.parametrize("pad,shift", [(1, 1), (6, 3), (0, 7), (13, 5)])
+def test_rows_off_any_boundary_leave_the_rest_alone(g, dtype, T, H, pad, shift):
+    """Unaligned inputs and outputs: right values, in place too, and no element between rows written."""
+    gen = torch.Generator().manual_seed(T + H + pad)
+
+    def room(kind=dtype):
+        """An output of canaries: (buffer, its T x H window, the mask of what lies outside)."""
+        buf = torch.full((T * (H + pad) + shift + 16,), 5.0, device="cuda").to(kind)
+        outside = torch.ones(buf.numel(), dtype=torch.bool, device="cuda")
+        outside[shift:shift + T * (H + pad)].view(T, H + pad)[:, :H] = False
+        return buf, buf[shift:shift + T * (H + pad)].view(T, H + pad)[:, :H], outside
+
+    def untouched(*rooms):
+        for buf, _, outside in rooms:
+            assert torch.all(buf.float()[outside] == 5.0)
+
+    x, res, dy = (rows(T, H, dtype, gen, pad, 8 - shift) for _ in range(3))
+    w = rows(1, H, dtype, gen, 0, 1)[0]
+    ry, rh, rx, rd = (room() for _ in range(4))
+    rstd = torch.empty(T, device="cuda")
+    g.add_rms_norm(x, w, ry[1], residual=res, h=rh[1], rstd=rstd, eps=EPS)
+    want_h, want_r, want_y = ref.add_rms_norm(x.cpu(), res.cpu(), w.cpu(), EPS)
+    sizes = x.cpu().double().abs() + res.cpu().double().abs()
+    close(rh[1], want_h, dtype, sizes, 2.0 ** -22, "h")
+    close(ry[1], want_y, dtype, sizes * want_r[:, None] * w.cpu().double().abs(), what="y")
+    dw = torch.empty(H + 1, dtype=dtype, device="cuda")[1:]
+    g.add_rms_norm_backward(dy, rh[1], w, rstd, rx[1], dw, dresidual=rd[1])
+    want = ref.add_rms_norm_backward(dy.cpu(), rh[1].cpu(), w.cpu(), rstd.cpu())
+    close(rx[1], want[0], dtype, want[3], what="dx")
+    close(dw, want[2], dtype, want[4], what="dw")
+    assert torch.equal(rx[1], rd[1])
+    untouched(ry, rh, rx, rd)
+
+    r8 = room(torch.float8_e4m3fn)
+    scales = torch.empty(T, -(-H // 128), device="cuda")
+    g.add_rms_norm(x, w, r8[1], residual=res, scales=scales)
+    v = want_y / scales.cpu().double().repeat_interleave(128, 1)[:, :H]
+    off = (r8[1].float().cpu().double() - v).abs()
+    assert torch.all(off <= (ref.E4M3_UNIT + 8 * F32) * v.abs() + ref.E4M3_TINY + 8 * F32)
+    untouched(r8)
+
+    y, h = ry[1].clone(), rh[1].clone()
+    rx[1].copy_(x)
+    rd[1].copy_(res)
+    g.add_rms_norm(rx[1], w, rx[1], residual=rd[1], h=rd[1], eps=EPS)     # in place
+    assert torch.equal(rx[1], y) and torch.equal(rd[1], h)
+    words = rng_words(9, 2)
+    g.dropout(x, ry[1], 0.4, words)
+    rx[1].copy_(x)
+    g.dropout(rx[1], rx[1], 0.4, words)
+    keep = ref.keep_factor(T, H, 0.4, (9, 2)) if T * H < 50000 else None
+    assert torch.equal(rx[1], ry[1])
+    if keep is not None:
+        close(ry[1], ref.apply_keep(x.cpu().double(), keep), dtype, slack=2.0 ** -22, what="dropout")
+    untouched(rx, rd, ry)
+
+
+@gpu
 def test_empty_and_no_rows(g):
     w = torch.randn(64, device="cuda", dtype=torch.bfloat16)
     none = torch.empty(0, 64, device="cuda", dtype=torch.bfloat16)
