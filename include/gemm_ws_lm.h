@@ -21,9 +21,9 @@
  * A matrix is `rows` rows of `cols` contiguous elements, `ld` elements from
  * one row to the next (ld >= cols). What lies between two rows of an input may be
  * read, and plays no part; between two rows of an output nothing is written. An
- * output may be exactly one of the call's
- * inputs where that is said; any other overlap of an output with another
- * argument is refused.
+ * output may be exactly one of the call's inputs where that is said; any other
+ * overlap of an output with another argument (first to last element, what lies
+ * between the rows included) is refused.
  */
 #ifndef GEMM_WS_LM_H_
 #define GEMM_WS_LM_H_
