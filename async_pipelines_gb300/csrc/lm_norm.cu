@@ -137,19 +137,22 @@ bool plan_ring(int64_t cols, int64_t size, int inputs, Q* q, int* vpt) {
 }
 
 // The kernel instance for a team and a path. Fewer threads a block leave each
-// more registers: 64 with 1024, 128 with 512.
-#define LM_NORM_INSTANCE(KERNEL, T, PATH, ...)                                     \
-  (t.vpt == 1                      ? gws::KERNEL<T, PATH, 1, 1024, ##__VA_ARGS__>  \
-   : t.vpt == 2                    ? gws::KERNEL<T, PATH, 2, 512, ##__VA_ARGS__>   \
-   : t.threads * t.rows <= 512     ? gws::KERNEL<T, PATH, 4, 512, ##__VA_ARGS__>   \
-                                   : gws::KERNEL<T, PATH, 4, 1024, ##__VA_ARGS__>)
+// more registers: 64 with 1024, 128 with 512. NARROW: four groups a thread and at
+// most 256 threads, in 16 bits kept to 80 registers, so that an SM holds three rows of
+// 8192 columns (78 us; 84 with two).
+#define LM_NORM_INSTANCE(KERNEL, NARROW, T, PATH, ...)                              \
+  (t.vpt == 1                  ? gws::KERNEL<T, PATH, 1, 1024, ##__VA_ARGS__>       \
+   : t.vpt == 2                ? gws::KERNEL<T, PATH, 2, 512, ##__VA_ARGS__>        \
+   : t.threads * t.rows <= 256 ? gws::KERNEL<T, PATH, 4, NARROW, ##__VA_ARGS__>     \
+   : t.threads * t.rows <= 512 ? gws::KERNEL<T, PATH, 4, 512, ##__VA_ARGS__>        \
+                               : gws::KERNEL<T, PATH, 4, 1024, ##__VA_ARGS__>)
 
 template <typename T, int Q>
 int launch_norm(gemm_ws* h, const Team& t, gws::Path path, const gws::NormParams& p, cudaStream_t s) {
-  auto kernel = LM_NORM_INSTANCE(add_rms_norm_kernel, T, gws::ANY, Q);
-  if (path == gws::FAST) kernel = LM_NORM_INSTANCE(add_rms_norm_kernel, T, gws::FAST, Q);
+  auto kernel = LM_NORM_INSTANCE(add_rms_norm_kernel, 512, T, gws::ANY, Q);
+  if (path == gws::FAST) kernel = LM_NORM_INSTANCE(add_rms_norm_kernel, 256, T, gws::FAST, Q);
   if constexpr (Q == 0)   // 8 bits are for serving: with dropout they take the general path
-    if (path == gws::DROP) kernel = LM_NORM_INSTANCE(add_rms_norm_kernel, T, gws::DROP, Q);
+    if (path == gws::DROP) kernel = LM_NORM_INSTANCE(add_rms_norm_kernel, 512, T, gws::DROP, Q);
   return launch(h, kernel, ceil_div(p.rows, t.rows), t.threads * t.rows, 0, s, p);
 }
 
@@ -199,9 +202,9 @@ int launch_grad_ring(gemm_ws* h, int vpt, const gws::NormGradRing& q, void* dwei
 template <typename T>
 int launch_grad(gemm_ws* h, const Team& t, gws::Path path, const gws::NormGradParams& p, void* dweight,
                 cudaStream_t s) {
-  const auto kernel = path == gws::ANY    ? LM_NORM_INSTANCE(add_rms_norm_grad_kernel, T, gws::ANY)
-                      : path == gws::FAST ? LM_NORM_INSTANCE(add_rms_norm_grad_kernel, T, gws::FAST)
-                                          : LM_NORM_INSTANCE(add_rms_norm_grad_kernel, T, gws::DROP);
+  const auto kernel = path == gws::ANY    ? LM_NORM_INSTANCE(add_rms_norm_grad_kernel, 512, T, gws::ANY)
+                      : path == gws::FAST ? LM_NORM_INSTANCE(add_rms_norm_grad_kernel, 512, T, gws::FAST)
+                                          : LM_NORM_INSTANCE(add_rms_norm_grad_kernel, 512, T, gws::DROP);
   const int threads = t.threads * t.rows;
   const size_t smem = t.rows > 1 ? static_cast<size_t>(p.cols) * sizeof(float) : 0;
   // As many blocks as run at once (1024 threads of an SM hold their rows in

@@ -186,6 +186,11 @@ __device__ __forceinline__ Raw<T> from_bits(const uint32_t (&e)[GROUP]) {
   return raw;
 }
 
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+
 template <int SIZE>
 struct Bits;
 template <>
@@ -233,29 +238,23 @@ __device__ __forceinline__ void unpack(const Raw<T>& raw, Pair (&v)[GROUP / 2]) 
 // dropout behind a branch.
 enum Path { ANY = 0, FAST = 1, DROP = 2 };
 
-// Where a matrix lies: what may be read of it.
-struct Span {
-  uintptr_t lo, hi;
-};
-template <typename T>
-__device__ __forceinline__ Span span_of(const void* first, int64_t rows, int64_t ld, int cols) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(first);
-  return {lo, lo + ((rows - 1) * ld + cols) * sizeof(T)};
-}
-
-// out = the bytes [by, by + 4 W) of `in`, by < 16.
+// out = the bytes [by, by + 4 W) of `in`, 0 < by < 16. A warp's groups are mostly
+// of one row, so that `by` is one and the branches are taken together.
 template <int W>
-__device__ __forceinline__ void shift_bytes(uint32_t (&in)[W + 4], int by, uint32_t (&out)[W]) {
-  if (by & 8) {
+__device__ __forceinline__ void shift_bytes(const uint32_t (&in)[W + 4], int by, uint32_t (&out)[W]) {
+  const int bits = (by & 3) * 8;
+  auto from = [&](auto first) {
+    constexpr int F = decltype(first)::value;
 #pragma unroll
-    for (int i = 0; i < W + 2; ++i) in[i] = in[i + 2];
+    for (int i = 0; i < W; ++i)
+      out[i] = __funnelshift_r(in[i + F], in[i + F + 1 < W + 4 ? i + F + 1 : W + 3], bits);
+  };
+  switch (by >> 2) {
+    case 0: from(Int<0>()); break;
+    case 1: from(Int<1>()); break;
+    case 2: from(Int<2>()); break;
+    default: from(Int<3>()); break;
   }
-  if (by & 4) {
-#pragma unroll
-    for (int i = 0; i < W + 1; ++i) in[i] = in[i + 1];
-  }
-#pragma unroll
-  for (int i = 0; i < W; ++i) out[i] = __funnelshift_r(in[i], in[i + 1], (by & 3) * 8);
 }
 
 template <typename T>
@@ -272,14 +271,27 @@ __device__ __forceinline__ void words_of(const Raw<T>& raw, uint32_t (&w)[WORDS<
   }
 }
 
+// A row of a matrix, and whether the matrix has at least 16 bytes before and
+// after it (which may then be read along with it).
+template <typename T>
+struct Row {
+  const T* at;
+  bool before, after;
+};
+template <typename T>
+__device__ __forceinline__ Row<T> row_of(const void* first, int64_t row, int64_t rows, int64_t ld) {
+  const bool far = ld * sizeof(T) >= 16;
+  return {static_cast<const T*>(first) + row * ld, far && row > 0, far && row + 1 < rows};
+}
+
 // Columns [c, c + 8) of a row whose end is `cols`; past it zeros. WHOLE (not
 // ANY): a group moves in 16-byte pieces and nothing is tested. Else a group that
 // does not start on a 16-byte boundary is cut out of the 16-byte pieces around it,
 // where those lie within the matrix; at its two ends and the row's, single
-// elements. (8192 x 8191 bf16, forward: 398 us with single elements, 186 so.)
+// elements (which took twice the time for all of 8192 x 8191 bf16).
 template <bool WHOLE, typename T>
-__device__ __forceinline__ Raw<T> load_group(const T* row, int c, int cols, const Span& span) {
-  const auto* src = reinterpret_cast<const typename Bits<sizeof(T)>::type*>(row) + c;
+__device__ __forceinline__ Raw<T> load_group(const Row<T>& row, int c, int cols) {
+  const auto* src = reinterpret_cast<const typename Bits<sizeof(T)>::type*>(row.at) + c;
   constexpr int PIECES = WORDS<T> / 4;
   const uintptr_t at = reinterpret_cast<uintptr_t>(src);
   const int off = static_cast<int>(at & 15);
@@ -288,7 +300,7 @@ __device__ __forceinline__ Raw<T> load_group(const T* row, int c, int cols, cons
   if (WHOLE || (whole && off == 0)) {
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) raw.w[i] = reinterpret_cast<const uint4*>(src)[i];
-  } else if (whole && at - off >= span.lo && at - off + 16 * (PIECES + 1) <= span.hi) {
+  } else if (whole && (c > 0 || row.before) && (c + 2 * GROUP <= cols || row.after)) {
     uint32_t in[WORDS<T> + 4], out[WORDS<T>];
 #pragma unroll
     for (int i = 0; i <= PIECES; ++i) {
@@ -311,13 +323,63 @@ __device__ __forceinline__ Raw<T> load_group(const T* row, int c, int cols, cons
   return raw;
 }
 
+// Fetches the group into the cache, without waiting: the general path's loads
+// take their data apart one after the other, so what they find there counts.
+template <typename T>
+__device__ __forceinline__ void prefetch_group(const Row<T>& row, int c) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(row.at + c));
+}
+
+// The bytes [from, 4 W) of w, to an address `to` that they bring to a 16-byte
+// boundary: in pieces that grow with its alignment.
+template <int W>
+__device__ __forceinline__ void store_lead(uintptr_t to, const uint32_t (&w)[W]) {
+  auto word = [&](int byte) { return __funnelshift_r(w[byte >> 2 & 3], w[((byte >> 2) + 1) & 3], (byte & 3) * 8); };
+  int at = 0;
+  if (to & 1) {
+    *reinterpret_cast<uint8_t*>(to) = static_cast<uint8_t>(w[0]);
+    at = 1;
+  }
+  if ((to + at) & 2) {
+    *reinterpret_cast<uint16_t*>(to + at) = static_cast<uint16_t>(word(at));
+    at += 2;
+  }
+  if ((to + at) & 4) {
+    *reinterpret_cast<uint32_t*>(to + at) = word(at);
+    at += 4;
+  }
+  if constexpr (W > 2)
+    if ((to + at) & 8) *reinterpret_cast<uint2*>(to + at) = make_uint2(word(at), word(at + 4));
+}
+
+// The first `n` bytes of w to a 16-byte (W == 2: 8-byte) boundary.
+template <int W>
+__device__ __forceinline__ void store_tail(uintptr_t to, const uint32_t (&w)[W], int n) {
+  int at = 0;
+  if constexpr (W > 2)
+    if (n & 8) {
+      *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+      at = 8;
+    }
+  if (n & 4) {
+    *reinterpret_cast<uint32_t*>(to + at) = w[(at >> 2) & (W - 1)];
+    at += 4;
+  }
+  const uint32_t last = w[(at >> 2) & (W - 1)];
+  if (n & 2) {
+    *reinterpret_cast<uint16_t*>(to + at) = static_cast<uint16_t>(last);
+    at += 2;
+  }
+  if (n & 1) *reinterpret_cast<uint8_t*>(to + at) = static_cast<uint8_t>(last >> (n & 2 ? 16 : 0));
+}
+
 // Stores columns [c, c + 8) (as many as there are) of thread t's group of a row of
 // `team` threads; WHOLE needs no other thread. Else the whole warp has to call it,
 // threads without a group with c >= cols: neighbouring threads hold neighbouring
 // groups, and where these do not start on a 16-byte boundary each thread stores the
 // 16-byte pieces that end in its group, with the rest of its left neighbour's; the
-// pieces at a warp's and the row's ends go as single elements. (Two bytes a store,
-// 8192 x 8191 bf16 took five times as long as 8192 x 8192.)
+// bytes at a warp's two ends go in smaller pieces, and a row's last group element by
+// element.
 template <bool WHOLE, typename T>
 __device__ __forceinline__ void store_group(T* row, int c, int cols, int t, int team,
                                             const Raw<T>& raw) {
@@ -333,73 +395,107 @@ __device__ __forceinline__ void store_group(T* row, int c, int cols, int t, int 
     words_of(raw, own);
 #pragma unroll
     for (int i = 0; i < 4; ++i) in[i] = __shfl_up_sync(0xffffffffu, own[WORDS<T> - 4 + i], 1);
-    if (off == 0 && c + GROUP <= cols) {
+    const bool whole = c + GROUP <= cols;
+    if (off == 0 && whole) {
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) reinterpret_cast<uint4*>(dst)[i] = raw.w[i];
       return;
     }
-    unsigned stored = 0;   // bit k: the k-th piece that touches the group is stored
-    if (off != 0) {
+    const int lane = threadIdx.x & 31;
+    const bool left = lane > 0 && t > 0, right = lane < 31 && t + 1 < team;
+    const int lead = (16 - off) / static_cast<int>(sizeof(T));   // elements up to the boundary
+    if (off != 0 && whole) {
 #pragma unroll
       for (int i = 0; i < WORDS<T>; ++i) in[4 + i] = own[i];
       shift_bytes<WORDS<T>>(in, 16 - off, out);
-      // elements of the group in the piece that its left neighbour begins
-      const int lead = (16 - off) / static_cast<int>(sizeof(T));
-      const int lane = threadIdx.x & 31;
 #pragma unroll
-      for (int k = 0; k < PIECES; ++k) {
-        const int end = lead + k * 16 / static_cast<int>(sizeof(T));
-        if ((k > 0 || (lane > 0 && t > 0)) && c + end <= cols) {
+      for (int k = 0; k < PIECES; ++k)
+        if (k > 0 || left)
           reinterpret_cast<uint4*>(at - off)[k] =
               make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]);
-          stored |= 1u << k;
-        }
+      if (!left) {
+        const uint32_t first[4] = {own[0], own[1], own[2], own[3]};
+        store_lead<4>(at, first);
       }
-      // the right neighbour stores the piece that it ends
-      if (lane < 31 && t + 1 < team && c + GROUP + lead <= cols) stored |= 1u << PIECES;
-    }
-    if (stored != (2u << PIECES) - 1) {
+      // The right neighbour stores the piece that begins here, if all of it is there.
+      if (!(right && c + GROUP + lead <= cols)) {
+        uint32_t end[8], rest[4];
 #pragma unroll
-      for (int i = 0; i < GROUP; ++i) {
-        const int piece = (off + i * static_cast<int>(sizeof(T))) / 16;
-        if (c + i < cols && !(off != 0 && (stored >> piece & 1)))
-          dst[i] = static_cast<typename Bits<sizeof(T)>::type>(bits_of(raw, i));
+        for (int i = 0; i < 4; ++i) {
+          end[i] = own[WORDS<T> - 4 + i];
+          end[4 + i] = 0;
+        }
+        shift_bytes<4>(end, 16 - off, rest);
+        store_tail<4>(at - off + 16 * PIECES, rest, off);
       }
+      return;
     }
+    if (c >= cols) return;
+    // The row's last group, not whole: what the left neighbour begins, if all of
+    // that piece is there, and the rest by elements.
+    int from = 0;
+    if (off != 0 && left && c + lead <= cols) {
+#pragma unroll
+      for (int i = 0; i < WORDS<T>; ++i) in[4 + i] = own[i];
+      shift_bytes<WORDS<T>>(in, 16 - off, out);
+      *reinterpret_cast<uint4*>(at - off) = make_uint4(out[0], out[1], out[2], out[3]);
+      from = lead;
+    }
+#pragma unroll
+    for (int i = 0; i < GROUP; ++i)
+      if (i >= from && c + i < cols)
+        dst[i] = static_cast<typename Bits<sizeof(T)>::type>(bits_of(raw, i));
   }
 }
 
-// The same for the 8 bytes of an e4m3 group.
+// The same for the 8 bytes of an e4m3 group and pieces of 8 bytes.
 template <bool WHOLE>
 __device__ __forceinline__ void store_bytes(uint8_t* row, int c, int cols, int t, int team,
                                             uint2 raw) {
   uint8_t* dst = row + c;
   const uintptr_t at = reinterpret_cast<uintptr_t>(dst);
-  const int off = static_cast<int>(at & 7);
+  const int off = static_cast<int>(at & 7), lead = 8 - off;
   if constexpr (WHOLE) {
     *reinterpret_cast<uint2*>(dst) = raw;
   } else {
-    const unsigned long long own = raw.x | static_cast<unsigned long long>(raw.y) << 32;
-    const unsigned long long left = __shfl_up_sync(0xffffffffu, own, 1);
-    if (off == 0 && c + GROUP <= cols) {
+    using Word = unsigned long long;
+    const Word own = raw.x | static_cast<Word>(raw.y) << 32;
+    const Word other = __shfl_up_sync(0xffffffffu, own, 1);
+    const bool whole = c + GROUP <= cols;
+    if (off == 0 && whole) {
       *reinterpret_cast<uint2*>(dst) = raw;
       return;
     }
-    unsigned stored = 0;
-    if (off != 0) {
-      const int lane = threadIdx.x & 31, lead = 8 - off;
-      if (lane > 0 && t > 0 && c + lead <= cols) {
-        *reinterpret_cast<unsigned long long*>(at - off) = own << (8 * off) | left >> (8 * lead);
-        stored |= 1;
+    if (c >= cols) return;
+    const int lane = threadIdx.x & 31;
+    const bool left = off != 0 && lane > 0 && t > 0 && c + lead <= cols;
+    if (left) *reinterpret_cast<Word*>(at - off) = own << (8 * off) | other >> (8 * lead);
+    if (off != 0 && whole) {
+      if (!left) {
+        const uint32_t first[4] = {raw.x, raw.y, 0, 0};
+        int n = 0;   // up to the 8-byte boundary
+        if (at & 1) {
+          dst[0] = static_cast<uint8_t>(raw.x);
+          n = 1;
+        }
+        if ((at + n) & 2) {
+          *reinterpret_cast<uint16_t*>(dst + n) = static_cast<uint16_t>(raw.x >> (8 * n));
+          n += 2;
+        }
+        if ((at + n) & 4)
+          *reinterpret_cast<uint32_t*>(dst + n) = __funnelshift_r(first[0], first[1], 8 * n);
       }
-      if (lane < 31 && t + 1 < team && c + GROUP + lead <= cols) stored |= 2;
+      if (!(lane < 31 && t + 1 < team && c + GROUP + lead <= cols)) {
+        const Word end = own >> (8 * lead);
+        const uint32_t rest[2] = {static_cast<uint32_t>(end), static_cast<uint32_t>(end >> 32)};
+        store_tail<2>(at + lead, rest, off);
+      }
+      return;
     }
-    if (stored != 3) {
 #pragma unroll
-      for (int i = 0; i < GROUP; ++i)
-        if (c + i < cols && !(off != 0 && (stored >> ((off + i) / 8) & 1)))
-          dst[i] = static_cast<uint8_t>((i < 4 ? raw.x : raw.y) >> (8 * (i % 4)));
-    }
+    for (int i = 0; i < GROUP; ++i)
+      if (i >= (left ? lead : 0) && c + i < cols)
+        dst[i] = static_cast<uint8_t>((i < 4 ? raw.x : raw.y) >> (8 * (i % 4)));
   }
 }
 
@@ -522,29 +618,37 @@ struct NormParams {
 // One row a team. Q: 0 y has the type of x; 1 e4m3 with one scale a row; 2
 // e4m3 with a scale for each 128 columns.
 template <typename T, Path PATH, int VPT, int MOST, int Q>
-__global__ void __launch_bounds__(MOST) add_rms_norm_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(MOST, MOST == 256 ? (sizeof(T) == 2 ? 3 : 2) : 1)
+    add_rms_norm_kernel(const __grid_constant__ NormParams p) {
   __shared__ SumMax box[32];
   grid_dependency_wait();
   grid_launch_dependents();
   const int team = p.team, t = threadIdx.x % team;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / team) + threadIdx.x / team;
   if (row >= p.rows) return;   // only whole warps, and only where a team is a warp
-  const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-  const T* res = p.residual ? static_cast<const T*>(p.residual) + row * p.ldr : nullptr;
-  const T* weight = static_cast<const T*>(p.weight);
+  const Row<T> x = row_of<T>(p.x, row, p.rows, p.ldx), res = row_of<T>(p.residual, row, p.rows, p.ldr),
+               weight = row_of<T>(p.weight, 0, 1, 0);
   const int cols = p.cols, groups = (cols + GROUP - 1) / GROUP;
   constexpr bool WHOLE = PATH != ANY;
-  const Span sx = span_of<T>(p.x, p.rows, p.ldx, cols), sr = span_of<T>(p.residual, p.rows, p.ldr, cols),
-             sw = span_of<T>(weight, 1, cols, cols);
 
+  if constexpr (!WHOLE) {
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int c = (k * team + t) * GROUP;
+      if (c < cols) {
+        prefetch_group(x, c);
+        if (p.residual) prefetch_group(res, c);
+      }
+    }
+  }
   Raw<T> xr[VPT] = {}, rr[VPT], wr[VPT];
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
     const int g = k * team + t;
     if (g < groups) {
-      xr[k] = load_group<WHOLE>(x, g * GROUP, cols, sx);
-      if (res) rr[k] = load_group<WHOLE>(res, g * GROUP, cols, sr);
-      wr[k] = load_group<WHOLE>(weight, g * GROUP, cols, sw);
+      xr[k] = load_group<WHOLE>(x, g * GROUP, cols);
+      if (p.residual) rr[k] = load_group<WHOLE>(res, g * GROUP, cols);
+      wr[k] = load_group<WHOLE>(weight, g * GROUP, cols);
     }
   }
   const uint64_t seed = p.drop.rng[0];
@@ -569,7 +673,7 @@ __global__ void __launch_bounds__(MOST) add_rms_norm_kernel(const __grid_constan
     if (g < groups) {
       float w[GROUP];
       if (Q == 1) unpack(wr[k], w);
-      if (res) {
+      if (p.residual) {
         float r[GROUP];
         unpack(rr[k], r);
 #pragma unroll
@@ -783,9 +887,7 @@ __global__ void __launch_bounds__(MOST, PATH == ANY ? 1 : 1024 / MOST)
   const int team = p.team, t = threadIdx.x % team, teams = blockDim.x / team;
   const int cols = p.cols, groups = (cols + GROUP - 1) / GROUP;
   constexpr bool WHOLE = PATH != ANY;
-  const T* weight = static_cast<const T*>(p.weight);
-  const Span sy = span_of<T>(p.dy, p.rows, p.lddy, cols), sh = span_of<T>(p.h, p.rows, p.ldh, cols),
-             sd = span_of<T>(p.dh, p.rows, p.lddh, cols), sw = span_of<T>(weight, 1, cols, cols);
+  const Row<T> weight = row_of<T>(p.weight, 0, 1, 0);
   const uint64_t seed = p.drop.rng[0], first = p.drop.rng[1];
   float acc[VPT][GROUP];
 #pragma unroll
@@ -796,17 +898,27 @@ __global__ void __launch_bounds__(MOST, PATH == ANY ? 1 : 1024 / MOST)
   int turn = 0;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * teams + threadIdx.x / team; row < p.rows;
        row += static_cast<int64_t>(gridDim.x) * teams, turn ^= 1) {
-    const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
-    const T* h = static_cast<const T*>(p.h) + row * p.ldh;
-    const T* dh = p.dh ? static_cast<const T*>(p.dh) + row * p.lddh : nullptr;
+    const Row<T> dy = row_of<T>(p.dy, row, p.rows, p.lddy), h = row_of<T>(p.h, row, p.rows, p.ldh),
+                 dh = row_of<T>(p.dh, row, p.rows, p.lddh);
+    if constexpr (!WHOLE) {
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        const int c = (k * team + t) * GROUP;
+        if (c < cols) {
+          prefetch_group(dy, c);
+          prefetch_group(h, c);
+          if (p.dh) prefetch_group(dh, c);
+        }
+      }
+    }
     Raw<T> yr[VPT], hr[VPT], dr[VPT] = {};
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int g = k * team + t;
       if (g < groups) {
-        yr[k] = load_group<WHOLE>(dy, g * GROUP, cols, sy);
-        hr[k] = load_group<WHOLE>(h, g * GROUP, cols, sh);
-        if (dh) dr[k] = load_group<WHOLE>(dh, g * GROUP, cols, sd);
+        yr[k] = load_group<WHOLE>(dy, g * GROUP, cols);
+        hr[k] = load_group<WHOLE>(h, g * GROUP, cols);
+        if (p.dh) dr[k] = load_group<WHOLE>(dh, g * GROUP, cols);
       }
     }
     const float r = p.rstd[row];
@@ -818,7 +930,7 @@ __global__ void __launch_bounds__(MOST, PATH == ANY ? 1 : 1024 / MOST)
         float a[GROUP], n[GROUP], w[GROUP];
         unpack(yr[k], a);
         unpack(hr[k], n);
-        unpack(load_group<WHOLE>(weight, g * GROUP, cols, sw), w);
+        unpack(load_group<WHOLE>(weight, g * GROUP, cols), w);
 #pragma unroll
         for (int i = 0; i < GROUP; ++i) {
           const float ni = n[i] * r;
@@ -837,7 +949,7 @@ __global__ void __launch_bounds__(MOST, PATH == ANY ? 1 : 1024 / MOST)
         float a[GROUP], n[GROUP], w[GROUP];
         unpack(yr[k], a);
         unpack(hr[k], n);
-        unpack(load_group<WHOLE>(weight, g * GROUP, cols, sw), w);
+        unpack(load_group<WHOLE>(weight, g * GROUP, cols), w);
         unpack(dr[k], d[k]);
 #pragma unroll
         for (int i = 0; i < GROUP; ++i) d[k][i] = fmaf(r, a[i] * w[i] - n[i] * rc, d[k][i]);
@@ -1150,15 +1262,14 @@ __global__ void __launch_bounds__(DROP_THREADS) dropout_rows_kernel(const __grid
   const int team = p.row_threads, t = threadIdx.x % team;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (DROP_THREADS / team) + threadIdx.x / team;
   const bool there = row < p.rows;
-  const T* x = static_cast<const T*>(p.x) + (there ? row : 0) * p.ldx;
+  const Row<T> x = row_of<T>(p.x, there ? row : 0, p.rows, p.ldx);
   T* y = static_cast<T*>(p.y) + (there ? row : 0) * p.ldy;
-  const Span sx = span_of<T>(p.x, p.rows, p.ldx, p.cols);
   const int groups = static_cast<int>(p.groups);
   for (int g0 = 0; g0 < groups; g0 += team) {   // whole warps stay together for the stores
     const int g = g0 + t;
     const bool mine = there && g < groups;
     Raw<T> raw = {};
-    if (mine) raw = load_group<false>(x, g * GROUP, p.cols, sx);
+    if (mine) raw = load_group<false>(x, g * GROUP, p.cols);
     float v[1][GROUP];
     unpack(raw, v[0]);
     const uint64_t counter[1] = {first + static_cast<uint64_t>(row) * groups + g};
