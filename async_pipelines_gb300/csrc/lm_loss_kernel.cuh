@@ -159,18 +159,20 @@ struct Unit {
 
 constexpr int GROUP_M = 8;   // tiles walk 8 rows of tiles down, then step a column (L2 reuse)
 
-// Tiles, and ring stages of K, of a job.
+// The tiles of a job, and the ring stages of its K.
+struct Grid {
+  int tm, tn, tiles, units, stages;
+};
 template <int CG>
-__device__ __forceinline__ int job_tiles(const Params& p, const Job& job, int count, int* tm, int* tn) {
-  const int m = job.m < 0 ? count : job.m;
-  *tm = (m + BM * CG - 1) / (BM * CG);
-  *tn = (job.n + p.bn - 1) / p.bn;
-  return *tm * *tn;
-}
-template <int CG>
-__device__ __forceinline__ int job_stages(const Job& job, int count) {
-  const int k = job.k < 0 ? count : job.k;
-  return (k + BK * ksub<CG>() - 1) / (BK * ksub<CG>());
+__device__ __forceinline__ Grid grid_of(const Params& p, const Job& job, int count) {
+  Grid g;
+  const int m = job.m < 0 ? count : job.m, k = job.k < 0 ? count : job.k;
+  g.tm = (m + BM * CG - 1) / (BM * CG);
+  g.tn = (job.n + p.bn - 1) / p.bn;
+  g.tiles = g.tm * g.tn;
+  g.units = g.tiles * job.splits;
+  g.stages = (k + BK * ksub<CG>() - 1) / (BK * ksub<CG>());
+  return g;
 }
 
 // What every role of a cluster walks: units first, first + clusters, ... of
@@ -180,11 +182,14 @@ __device__ __forceinline__ int job_stages(const Job& job, int count) {
 // turn, so that no cluster ends more than about one of the shorter units
 // after the others. (Without it dx's quarter-full last wave of long units
 // held the launch up: 4096 x 4096 over 131072, both gradients of a piece,
-// 1378 us.)
+// 1378 us instead of 1290.) All that does not change from unit to unit is kept
+// here: a division costs a role that walks short units more than its unit.
 struct Walk {
   int cluster, clusters;
-  int units0;   // of the first job
+  Grid a, b;        // of the two jobs
   int heavy, extra;
+  int turns, rank;  // units of the first job that this cluster has; its place after them
+  bool light;
 };
 
 template <int CG>
@@ -192,55 +197,65 @@ __device__ __forceinline__ Walk make_walk(const Params& p, int count) {
   Walk k;
   k.cluster = blockIdx.x / CG;
   k.clusters = gridDim.x / CG;
-  k.units0 = k.heavy = k.extra = 0;
+  k.a = grid_of<CG>(p, p.job[0], count);
+  k.b = k.a;
+  k.heavy = k.extra = k.turns = k.rank = 0;
+  k.light = true;
   if (p.jobs == 2) {
-    int tm, tn;
-    k.units0 = job_tiles<CG>(p, p.job[0], count, &tm, &tn) * p.job[0].splits;
-    k.heavy = k.units0 % k.clusters;
-    const int s0 = job_stages<CG>(p.job[0], count) / p.job[0].splits;
-    const int s1 = job_stages<CG>(p.job[1], count);
-    if (k.heavy && s1 > 0) k.extra = s0 / s1;
+    k.b = grid_of<CG>(p, p.job[1], count);
+    k.heavy = k.a.units % k.clusters;
+    // Short units take about a stage's time on top, for their stores.
+    const int each = k.b.stages < 8 ? k.b.stages + 1 : k.b.stages;
+    if (k.heavy) k.extra = k.a.stages / p.job[0].splits / each;
+    k.light = k.cluster >= k.heavy;
+    k.turns = k.a.units / k.clusters + (k.light ? 0 : 1);
+    k.rank = k.light ? k.cluster - k.heavy : k.cluster + k.clusters - k.heavy;
   }
   return k;
 }
 
 // The i-th unit of the walk.
 template <int CG>
-__device__ __forceinline__ bool next_unit(const Params& p, int count, const Walk& k, int i, Unit& w) {
+__device__ __forceinline__ bool next_unit(const Params& p, const Walk& k, int i, Unit& w) {
   int u = k.cluster + i * k.clusters;
-  int j = 0;
-  if (p.jobs == 2 && u >= k.units0) {
-    j = 1;
+  const bool second = p.jobs == 2 && u >= k.a.units;
+  if (second) {
     if (k.extra == 0) {
-      u -= k.units0;
+      u -= k.a.units;
     } else {
-      // i counts on from this cluster's units of the first job
-      const bool light = k.cluster >= k.heavy;
-      const int lights = k.clusters - k.heavy;
-      const int t = i - k.units0 / k.clusters - (light ? 0 : 1);
-      const int rank = light ? k.cluster - k.heavy : k.cluster + lights;
-      if (light && t < k.extra)
-        u = t * lights + rank;
+      const int t = i - k.turns, lights = k.clusters - k.heavy;
+      if (k.light && t < k.extra)
+        u = t * lights + k.rank;
       else
-        u = k.extra * lights + (light ? t - k.extra : t) * k.clusters + rank;
+        u = k.extra * lights + (k.light ? t - k.extra : t) * k.clusters + k.rank;
     }
   }
-  const Job& job = p.job[j];
-  int tm, tn;
-  const int tiles = job_tiles<CG>(p, job, count, &tm, &tn);
-  if (u >= tiles * job.splits) return false;
+  const Grid& g = second ? k.b : k.a;
+  if (u >= g.units) return false;
+  const Job& job = p.job[second];
   w.job = &job;
-  w.cut = u / tiles;
-  const int t = u - w.cut * tiles;
-  const int g = t / (GROUP_M * tn), first = g * GROUP_M;
-  const int gm = tm - first < GROUP_M ? tm - first : GROUP_M;
-  const int r = t - g * GROUP_M * tn;
-  w.m0 = (first + r % gm) * BM * CG;
-  w.nb = r / gm;
+  int t = u;
+  w.cut = 0;
+  w.s0 = 0;
+  w.s1 = g.stages;
+  if (job.splits > 1) {
+    w.cut = u / g.tiles;
+    t = u - w.cut * g.tiles;
+    w.s0 = static_cast<int>(static_cast<int64_t>(w.cut) * g.stages / job.splits);
+    w.s1 = static_cast<int>(static_cast<int64_t>(w.cut + 1) * g.stages / job.splits);
+  }
+  const int group = t / (GROUP_M * g.tn), first = group * GROUP_M;
+  const int r = t - group * GROUP_M * g.tn;
+  int dm;
+  if (g.tm - first >= GROUP_M) {
+    dm = r % GROUP_M;
+    w.nb = r / GROUP_M;
+  } else {
+    w.nb = r / (g.tm - first);
+    dm = r - w.nb * (g.tm - first);
+  }
+  w.m0 = (first + dm) * BM * CG;
   w.n0 = w.nb * p.bn;
-  const int ns = job_stages<CG>(job, count);
-  w.s0 = static_cast<int>(static_cast<int64_t>(w.cut) * ns / job.splits);
-  w.s1 = static_cast<int>(static_cast<int64_t>(w.cut + 1) * ns / job.splits);
   return true;
 }
 
@@ -272,7 +287,7 @@ __device__ __forceinline__ void producer(const Params& p, uint32_t sbase, uint32
   uint32_t s = 0, ph = 0, g = 0;
   bool ok = true;
   Unit w;
-  for (int i = 0; ok && next_unit<CG>(p, count, walk, i, w); ++i) {
+  for (int i = 0; ok && next_unit<CG>(p, walk, i, w); ++i) {
     const Job& job = *w.job;
     const CUtensorMap* map = a_part ? &job.tmA : &job.tmB;
     const bool mn = a_part ? job.a_mn : job.b_mn;
@@ -343,7 +358,7 @@ __device__ __forceinline__ void mma_issuer(const Params& p, uint32_t sbase, uint
   uint32_t handed = 0;   // accumulators handed over so far
   bool issued = false;
   Unit w;
-  for (int i = 0; next_unit<CG>(p, count, walk, i, w); ++i) {
+  for (int i = 0; next_unit<CG>(p, walk, i, w); ++i) {
     const Job& job = *w.job;
     const bool a_mn = job.a_mn, b_mn = job.b_mn;
     const uint32_t idesc = idesc_bf16_f32(BM * CG, p.bn, a_mn, b_mn);
@@ -511,7 +526,7 @@ __device__ __forceinline__ void epilogue_logits(const Params& p, uint32_t sbase,
     sum = 0.0f;
   };
   Unit w;
-  for (int i = 0; next_unit<CG>(p, count, walk, i, w); ++i) {
+  for (int i = 0; next_unit<CG>(p, walk, i, w); ++i) {
     any = true;
     const int part0 = w.m0 + static_cast<int>(rank) * BM;   // this CTA's first row
     row = part0 + 32 * me.q + me.lane;
@@ -628,7 +643,7 @@ __device__ __forceinline__ void epilogue_sums(const Params& p, uint32_t sbase, u
   Epilogue<CG> me(sbase, smem, tmem, rank, warp);
   const Walk walk = make_walk<CG>(p, count);
   Unit w;
-  for (int i = 0; next_unit<CG>(p, count, walk, i, w); ++i) {
+  for (int i = 0; next_unit<CG>(p, walk, i, w); ++i) {
     const Job& job = *w.job;
     const int part0 = w.m0 + static_cast<int>(rank) * BM;   // this CTA's first row
     const bool f32 = job.out == OUT_ADD;
