@@ -4,6 +4,9 @@
 #include <cstring>
 
 #include "gemm_ws_lm.h"
+#ifdef GEMM_WS_DEBUG
+#include "gemm_ws_debug.h"
+#endif
 #include "handle.cuh"
 #include "lm_loss_kernel.cuh"
 
@@ -519,5 +522,57 @@ int gemm_ws_linear_ce_backward(gemm_ws_t* h, const uint16_t* x, int64_t ldx,
   }
   return rc;
 }
+
+#ifdef GEMM_WS_DEBUG
+}  // extern "C"
+
+namespace {
+
+template <int CG>
+int64_t list_units(const ce::Params& p, int count, int clusters, int* rows, int64_t max_rows) {
+  int64_t n = 0;
+  for (int c = 0; c < clusters; ++c) {
+    const ce::Walk walk = ce::make_walk<CG>(p, count, c, clusters);
+    ce::Unit w;
+    for (int i = 0; ce::next_unit<CG>(p, walk, i, w); ++i, ++n) {
+      if (n >= max_rows) continue;
+      int* r = rows + n * 8;
+      r[0] = c;
+      r[1] = i;
+      r[2] = static_cast<int>(w.job - p.job);
+      r[3] = w.m0;
+      r[4] = w.n0;
+      r[5] = w.cut;
+      r[6] = w.s0;
+      r[7] = w.s1;
+    }
+  }
+  return n;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gemm_ws_debug_ce_units(int cta_group, int clusters, int bn, int count, const int* jobs,
+                           int num_jobs, int* rows, int64_t max_rows, int64_t* num_rows) {
+  if (cta_group < 1 || cta_group > 2 || clusters < 1 || bn < 16 || count < 0 || !jobs ||
+      num_jobs < 1 || num_jobs > 2 || !num_rows)
+    return GEMM_WS_ERR_INVALID_ARG;
+  ce::Params p;
+  std::memset(&p, 0, sizeof p);
+  p.jobs = num_jobs;
+  p.bn = bn;
+  for (int j = 0; j < num_jobs; ++j) {
+    p.job[j].m = jobs[4 * j];
+    p.job[j].n = jobs[4 * j + 1];
+    p.job[j].k = jobs[4 * j + 2];
+    p.job[j].splits = jobs[4 * j + 3];
+  }
+  *num_rows = cta_group == 2 ? list_units<2>(p, count, clusters, rows, rows ? max_rows : 0)
+                             : list_units<1>(p, count, clusters, rows, rows ? max_rows : 0);
+  return GEMM_WS_OK;
+}
+#endif
 
 }  // extern "C"

@@ -164,7 +164,7 @@ struct Grid {
   int tm, tn, tiles, units, stages;
 };
 template <int CG>
-__device__ __forceinline__ Grid grid_of(const Params& p, const Job& job, int count) {
+__host__ __device__ __forceinline__ Grid grid_of(const Params& p, const Job& job, int count) {
   Grid g;
   const int m = job.m < 0 ? count : job.m, k = job.k < 0 ? count : job.k;
   g.tm = (m + BM * CG - 1) / (BM * CG);
@@ -193,10 +193,11 @@ struct Walk {
 };
 
 template <int CG>
-__device__ __forceinline__ Walk make_walk(const Params& p, int count) {
+__host__ __device__ __forceinline__ Walk make_walk(const Params& p, int count, int cluster,
+                                                   int clusters) {
   Walk k;
-  k.cluster = blockIdx.x / CG;
-  k.clusters = gridDim.x / CG;
+  k.cluster = cluster;
+  k.clusters = clusters;
   k.a = grid_of<CG>(p, p.job[0], count);
   k.b = k.a;
   k.heavy = k.extra = k.turns = k.rank = 0;
@@ -216,7 +217,7 @@ __device__ __forceinline__ Walk make_walk(const Params& p, int count) {
 
 // The i-th unit of the walk.
 template <int CG>
-__device__ __forceinline__ bool next_unit(const Params& p, const Walk& k, int i, Unit& w) {
+__host__ __device__ __forceinline__ bool next_unit(const Params& p, const Walk& k, int i, Unit& w) {
   int u = k.cluster + i * k.clusters;
   const bool second = p.jobs == 2 && u >= k.a.units;
   if (second) {
@@ -230,7 +231,12 @@ __device__ __forceinline__ bool next_unit(const Params& p, const Walk& k, int i,
         u = k.extra * lights + (k.light ? t - k.extra : t) * k.clusters + k.rank;
     }
   }
-  const Grid& g = second ? k.b : k.a;
+  Grid g;   // chosen value by value, so that the walk stays in registers
+  g.tm = second ? k.b.tm : k.a.tm;
+  g.tn = second ? k.b.tn : k.a.tn;
+  g.tiles = second ? k.b.tiles : k.a.tiles;
+  g.units = second ? k.b.units : k.a.units;
+  g.stages = second ? k.b.stages : k.a.stages;
   if (u >= g.units) return false;
   const Job& job = p.job[second];
   w.job = &job;
@@ -279,7 +285,7 @@ __device__ __forceinline__ void producer(const Params& p, uint32_t sbase, uint32
                                          int count, const Watchdog& wd) {
   auto full = [&](uint32_t s) { return sbase + OFF_BAR + 8 * (BAR_FULL + s); };
   auto empty = [&](uint32_t s) { return sbase + OFF_BAR + 8 * (BAR_EMPTY + s); };
-  const Walk walk = make_walk<CG>(p, count);
+  const Walk walk = make_walk<CG>(p, count, blockIdx.x / CG, gridDim.x / CG);
   const bool leader = a_part && rank == 0;   // arms full[s] for the pair
   const uint32_t stages = p.stages, sbytes = stage_bytes<CG>(p.bn);
   const uint32_t b_block = static_cast<uint32_t>(p.bn / CG) * BK * 2;
@@ -351,7 +357,7 @@ __device__ __forceinline__ void mma_issuer(const Params& p, uint32_t sbase, uint
     else
       umma_commit_pair(b, static_cast<uint16_t>(0x3u));
   };
-  const Walk walk = make_walk<CG>(p, count);
+  const Walk walk = make_walk<CG>(p, count, blockIdx.x / CG, gridDim.x / CG);
   const uint32_t stages = p.stages, sbytes = stage_bytes<CG>(p.bn);
   const uint32_t b_block = static_cast<uint32_t>(p.bn / CG) * BK * 2;
   uint32_t s = 0, ph = 0;
@@ -516,7 +522,7 @@ __device__ __forceinline__ void epilogue_logits(const Params& p, uint32_t sbase,
                                                 uint32_t tmem, uint32_t rank, int warp, int count,
                                                 const Watchdog& wd) {
   Epilogue<CG> me(sbase, smem, tmem, rank, warp);
-  const Walk walk = make_walk<CG>(p, count);
+  const Walk walk = make_walk<CG>(p, count, blockIdx.x / CG, gridDim.x / CG);
   float top = -INFINITY, sum = 0.0f;
   int row = 0;
   bool any = false;
@@ -641,7 +647,7 @@ __device__ __forceinline__ void epilogue_sums(const Params& p, uint32_t sbase, u
                                               uint32_t tmem, uint32_t rank, int warp, int count,
                                               const Watchdog& wd) {
   Epilogue<CG> me(sbase, smem, tmem, rank, warp);
-  const Walk walk = make_walk<CG>(p, count);
+  const Walk walk = make_walk<CG>(p, count, blockIdx.x / CG, gridDim.x / CG);
   Unit w;
   for (int i = 0; next_unit<CG>(p, walk, i, w); ++i) {
     const Job& job = *w.job;

@@ -87,7 +87,7 @@ def load_library(path: Optional[str] = None):
 
 DEBUG_EXPORTS = ("gemm_ws_debug_configure", "gemm_ws_debug_launch_shape",
                  "gemm_ws_debug_schedule", "gemm_ws_debug_phases",
-                 "gemm_ws_debug_noalloc_configure")
+                 "gemm_ws_debug_noalloc_configure", "gemm_ws_debug_ce_units")
 
 _debug_lib = None
 
@@ -115,6 +115,10 @@ def load_debug_library():
         lib.gemm_ws_debug_noalloc_configure.argtypes = [ctypes.c_int, ctypes.c_int,
                                                         ctypes.c_longlong]
         lib.gemm_ws_debug_noalloc_configure.restype = ctypes.c_int
+        lib.gemm_ws_debug_ce_units.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                               ctypes.c_int, ip, ctypes.c_int, ctypes.c_void_p,
+                                               i64, ctypes.POINTER(i64)]
+        lib.gemm_ws_debug_ce_units.restype = ctypes.c_int
         _debug_lib = lib
     return _debug_lib
 

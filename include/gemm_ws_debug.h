@@ -93,6 +93,15 @@ int gemm_ws_debug_schedule(int cta_group, int num_sms, int max_clusters, int str
  * 0 restores the default. Returns GEMM_WS_OK or GEMM_WS_ERR_INVALID_ARG. */
 int gemm_ws_debug_noalloc_configure(int device, int fault, long long timeout_ms);
 
+/* The units of the cross entropy's product kernel, in the order its clusters walk
+ * them; host arithmetic only, the same functions the kernel runs. jobs: for each
+ * of num_jobs (1 or 2) its M, N and K (-1: `count`, the counted rows) and the cuts
+ * of K. rows: for each unit 8 ints: cluster, position in its walk, job, first row,
+ * first column, cut, first and last + 1 ring stage of K; at most max_rows are
+ * written, *num_rows is how many there are. */
+int gemm_ws_debug_ce_units(int cta_group, int clusters, int bn, int count, const int* jobs,
+                           int num_jobs, int* rows, int64_t max_rows, int64_t* num_rows);
+
 #ifdef __cplusplus
 }
 #endif
