@@ -106,6 +106,9 @@ int gemm_ws_add_rms_norm_backward(gemm_ws_t* h, int dtype, const void* dy, int64
  *  - A token whose target is `ignore` is not counted: its loss and lse are 0
  *    and its row of x plays no part (it may hold anything). A counted token
  *    whose target is outside [0, vocab) has loss NaN, and no gradient.
+ *  - A logit of -inf is a word of no probability: nothing to lse, loss +inf
+ *    where it is the target. A logit of +inf or NaN makes the token's lse and
+ *    loss NaN.
  *  - loss, lse: tokens fp32; mean: two fp32, the mean loss over the counted
  *    tokens and 1 / their number (both 0 with none), or NULL.
  *  - workspace: gemm_ws_linear_ce_workspace bytes on the device, 256-byte

@@ -201,6 +201,35 @@ def test_uncounted_rows_are_not_read(g, T):
 
 
 @gpu
+@pytest.mark.parametrize("T", [1, 8, 100, 300])
+def test_infinite_logits(g, T):
+    """Words of logit -inf, more than a tile of them, count as nothing; +inf and NaN make NaN."""
+    H, V, shut, inf = 256, 5000, 1000, float("inf")
+    gen = torch.Generator().manual_seed(T)
+    x = (torch.rand(T, H, generator=gen) + 0.1).bfloat16()
+    w = (torch.randn(V, H, generator=gen) / 16).bfloat16()
+    t = torch.randint(shut, V, (T,), generator=gen)
+    w[:shut] = -inf
+    got = forward(g, x.cuda(), w.cuda(), t.cuda())
+    check_forward(got, x, w[shut:], t - shut)
+    dw = torch.full_like(w, 3.0, device="cuda")
+    g.linear_cross_entropy_backward(x.cuda(), w.cuda(), t.cuda(), got[1], got[2][1:], dweight=dw)
+    dx = torch.empty_like(x, device="cuda")
+    open_ = w[shut:].cuda()
+    g.linear_cross_entropy_backward(x.cuda(), open_, (t - shut).cuda(), got[1], got[2][1:], dx=dx)
+    assert not dw[:shut].any()
+    check_backward(dx, dw[shut:], x, w[shut:], t - shut, torch.full((T,), float(got[2][1])))
+
+    t[0] = 3
+    loss, lse, mean = forward(g, x.cuda(), w.cuda(), t.cuda())
+    assert loss[0] == inf and mean[0] == inf and torch.equal(lse, got[1]) and torch.equal(loss[1:], got[0][1:])
+    for value in (inf, float("nan")):
+        w[shut + 7] = value
+        loss, lse, _ = forward(g, x.cuda(), w.cuda(), t.cuda())
+        assert lse.isnan().all() and loss.isnan().all()
+
+
+@gpu
 def test_no_counted_token_and_no_token(g):
     x, w, t = make(130, 64, 500, 2)
     t[:] = IGNORE
