@@ -364,9 +364,11 @@ int gemm_ws_linear_ce(gemm_ws_t* h, const uint16_t* x, int64_t ldx, const uint16
     return GEMM_WS_ERR_CUDA;
   DeviceGuard guard(h->device);
 
-  // Up to 128 rows that the TMA can read where they lie are not packed: each row
-  // has its own sums, so an uncounted one touches nothing.
-  p.direct = T <= ce::BM && pack.wide;
+  // Rows that the TMA can read where they lie are not packed if there are up to 128 of
+  // them, or if all tiles run at once, so that packing could save none of their time:
+  // each row has its own sums, so an uncounted one touches nothing. (256 x 256 over 1000
+  // words 10.3 us, packed 12.3; 2100 x 1024 over 1000 15.5 and 19.7.)
+  p.direct = pack.wide && (T <= ce::BM || units <= q.logits.clusters);
   p.join = p.direct && T <= ce::JOIN_FEW;
   p.rows = static_cast<int>(T);
   p.given = pack.given;

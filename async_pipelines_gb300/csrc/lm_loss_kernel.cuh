@@ -136,7 +136,7 @@ struct Params {
   int cut_k;                 // K of one accumulator, a multiple of 128 (the same in both)
   int carry;                 // one row of tiles: a CTA keeps its sums over its tiles
   const float *lse, *grad;   // [row]: lse, and g
-  // LSE of at most 128 rows: x itself is A, so nothing is packed; and with at most
+  // LSE of few rows or tiles: x itself is A, so nothing is packed; and with at most
   // JOIN_FEW rows the CTA that ends last joins the sums, so that the pass is one
   // launch. (It is one SM's work: 61 rows so take 10 us longer than with a launch.)
   int direct;
@@ -1055,8 +1055,13 @@ __global__ void __launch_bounds__(JOIN_ROWS* JOIN_LANES)
     loss = 0.0f;
     for (int l = 0; l < JOIN_LANES; ++l) loss += sums[l];
   }
-  const int t = threadIdx.x;   // direct: at most 128 rows
-  const int n = p.direct ? __syncthreads_count(t < p.rows && p.given.raw(t) != p.given.ignore) : *p.count;
+  int n = 0;
+  if (!p.direct) n = *p.count;
+  else
+    for (int t0 = 0; t0 < p.rows; t0 += JOIN_ROWS * JOIN_LANES) {
+      const int t = t0 + threadIdx.x;
+      n += __syncthreads_count(t < p.rows && p.given.raw(t) != p.given.ignore);
+    }
   if (threadIdx.x == 0) {
     write_mean(p.result, loss, n);
     *p.done = 0u;

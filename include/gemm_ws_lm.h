@@ -117,8 +117,9 @@ int gemm_ws_add_rms_norm_backward(gemm_ws_t* h, int dtype, const void* dy, int64
  *    may lie anywhere). 0 <= tokens, 1 <= vocab, 8 <= hidden, each < 2^31,
  *    tokens * hidden, vocab * hidden and tokens * vocab < 2^40.
  * Products in bf16 with fp32 sums in tensor memory; everything after them in
- * fp32. Launches three kernels; two for up to 128 tokens whose rows lie on
- * 16-byte boundaries, one for up to 8 of them. */
+ * fp32. Launches three kernels; two where x's rows lie on 16-byte boundaries and
+ * there are up to 128 of them or no more tiles than run at once, one for up to
+ * 8 of them. */
 int gemm_ws_linear_ce(gemm_ws_t* h, const uint16_t* x, int64_t ldx, const uint16_t* weight,
                       int64_t ldw, const void* target, int target_bytes, int64_t ignore,
                       float* loss, float* lse, float* mean, int64_t tokens, int64_t hidden,
