@@ -171,6 +171,9 @@ int launch_norm(gemm_ws* h, int output, const Team& t, gws::Path path, const gws
   }
 }
 
+// Elements between the blocks' rows of dweight partials: whole groups.
+int64_t partial_pitch(int64_t cols) { return ceil_div(cols, gws::GROUP) * gws::GROUP; }
+
 template <typename T>
 int launch_dweight(gemm_ws* h, const float* partial, int64_t blocks, int cols, void* dweight,
                    cudaStream_t s) {
@@ -178,9 +181,10 @@ int launch_dweight(gemm_ws* h, const float* partial, int64_t blocks, int cols, v
   q.partial = partial;
   q.blocks = static_cast<int>(blocks);
   q.cols = cols;
+  q.pitch = static_cast<int>(partial_pitch(cols));
   q.dweight = dweight;
   return launch(h, gws::dweight_kernel<T>, ceil_div(cols, gws::DW_COLS),
-                gws::DW_COLS * gws::DW_LANES, 0, s, q);
+                gws::DW_THREADS, 0, s, q);
 }
 
 template <typename T, bool ON>
@@ -206,13 +210,13 @@ int launch_grad(gemm_ws* h, const Team& t, gws::Path path, const gws::NormGradPa
                       : path == gws::FAST ? LM_NORM_INSTANCE(add_rms_norm_grad_kernel, 512, T, gws::FAST)
                                           : LM_NORM_INSTANCE(add_rms_norm_grad_kernel, 512, T, gws::DROP);
   const int threads = t.threads * t.rows;
-  const size_t smem = t.rows > 1 ? static_cast<size_t>(p.cols) * sizeof(float) : 0;
+  const size_t smem = t.rows > 1 ? t.rows * partial_pitch(p.cols) * sizeof(float) : 0;   // at most 32 KB
   // As many blocks as run at once (1024 threads of an SM hold their rows in
   // registers), no more than the partials have room for.
   int64_t blocks = ceil_div(p.rows, t.rows);
   const int64_t resident = static_cast<int64_t>(h->num_sms) * (threads >= 1024 ? 1 : 1024 / threads);
   if (blocks > resident) blocks = resident;
-  const int64_t room = h->num_sms * kPartialPerSm / p.cols;
+  const int64_t room = h->num_sms * kPartialPerSm / partial_pitch(p.cols);
   if (p.partial && blocks > room) blocks = room;
   const int rc = launch(h, kernel, blocks, threads, smem, s, p);
   if (rc != GEMM_WS_OK || !dweight) return rc;
