@@ -87,8 +87,8 @@ struct Team {
   int threads, vpt, rows;   // rows: of a block
 };
 
-// Up to 1024 columns a warp holds a row and a block has several (no barrier).
-// Longer rows take a block. With few rows (less than two for each SM) every
+// Up to 256 columns, or 1024 of many rows, a warp holds a row and a block has
+// several (no barrier). Longer rows take a block. With few rows (less than two for each SM) every
 // thread takes one group, for the shortest row; with many, two, and from 2048
 // columns four, so that an SM has more bytes in flight for the threads that it
 // can hold (8192 x 8192 bf16: 78 us with four, 86 with two); beyond 8192 columns
@@ -99,7 +99,7 @@ Team pick_team(const gemm_ws* h, int64_t rows, int64_t cols, gws::Path path, int
   const int64_t groups = ceil_div(cols, gws::GROUP);
   const bool any = path == gws::ANY;
   Team t;
-  if (groups <= (any ? 32 : 128)) {
+  if (groups <= 32 || (!any && groups <= 128 && rows >= 2 * h->num_sms)) {
     t.vpt = groups <= 32 ? 1 : groups <= 64 ? 2 : 4;
     t.threads = 32;
     t.rows = rows >= 8 * h->num_sms ? 8 : rows >= 2 * h->num_sms ? 4 : 1;
@@ -211,10 +211,11 @@ int launch_grad(gemm_ws* h, const Team& t, gws::Path path, const gws::NormGradPa
                                           : LM_NORM_INSTANCE(add_rms_norm_grad_kernel, 512, T, gws::DROP);
   const int threads = t.threads * t.rows;
   const size_t smem = t.rows > 1 ? t.rows * partial_pitch(p.cols) * sizeof(float) : 0;   // at most 32 KB
-  // As many blocks as run at once (1024 threads of an SM hold their rows in
-  // registers), no more than the partials have room for.
+  // As many blocks as run at once (1024 threads of an SM, 512 with more than one group
+  // each), no more than the partials have room for.
   int64_t blocks = ceil_div(p.rows, t.rows);
-  const int64_t resident = static_cast<int64_t>(h->num_sms) * (threads >= 1024 ? 1 : 1024 / threads);
+  const int held = t.vpt == 1 ? 1024 : 512;
+  const int64_t resident = static_cast<int64_t>(h->num_sms) * (threads >= held ? 1 : held / threads);
   if (blocks > resident) blocks = resident;
   const int64_t room = h->num_sms * kPartialPerSm / partial_pitch(p.cols);
   if (p.partial && blocks > room) blocks = room;
@@ -455,7 +456,11 @@ int gemm_ws_add_rms_norm_backward(gemm_ws_t* h, int dtype, const void* dy, int64
   DeviceGuard guard(h->device);
   gws::NormGradRing ring;
   int vpt = 0;
-  if (path != gws::ANY && rows >= kRingRows * h->num_sms) {
+  const Team t = pick_team(h, rows, cols, path, 1);
+  // The ring from one row of each SM on, but four where the other kernel's threads hold
+  // one or two groups: that starts sooner. (With dweight, bf16: 600 x 4096 8.1 us, 16.7
+  // without the ring; 600 x 512 5.1 and 4.4, 200 x 4096 with one group a thread 7.2 and 5.9.)
+  if (path != gws::ANY && rows >= (t.vpt == 4 ? 1 : kRingRows) * h->num_sms) {
     ring.p = q;
     ring.status = h->work + 1;
     ring.timeout_ns = h->timeout_ns;
@@ -467,7 +472,6 @@ int gemm_ws_add_rms_norm_backward(gemm_ws_t* h, int dtype, const void* dy, int64
       }
     }
   }
-  const Team t = pick_team(h, rows, cols, path, 1);
   q.team = t.threads;
   switch (dtype) {
     case GEMM_WS_BF16: return launch_grad<__nv_bfloat16>(h, t, path, q, dweight, s);

@@ -913,7 +913,7 @@ __device__ __forceinline__ void leave_partial(const float (&acc)[VPT][GROUP], fl
 // one partial row, and dweight_kernel adds those in block order. So dweight
 // has the same bits on every run, whatever the timing.
 template <typename T, Path PATH, int VPT, int MOST>
-__global__ void __launch_bounds__(MOST, PATH == ANY ? 1 : 1024 / MOST)
+__global__ void __launch_bounds__(MOST, 1)
     add_rms_norm_grad_kernel(const __grid_constant__ NormGradParams p) {
   __shared__ SumMax box[2][32];
   extern __shared__ __align__(16) float share[];   // where a team is a warp: their shares of dweight
