@@ -211,6 +211,25 @@ def test_gradients_of_many_rows(g, T, H, dtype, dropout):
 
 
 @gpu
+@pytest.mark.parametrize("T", [1, 40, 151, 153, 303, 305, 607])
+@pytest.mark.parametrize("H,dtype", [
+    (256, torch.bfloat16), (264, torch.float16), (512, torch.float32), (776, torch.bfloat16),
+    (1024, torch.float32), (1032, torch.bfloat16), (2048, torch.float16), (4104, torch.bfloat16)])
+@pytest.mark.parametrize("dropout", [False, True])
+def test_gradients_from_one_row_to_some_of_each_sm(g, T, H, dtype, dropout):
+    """Where a warp, a block and the rows in shared memory take over from each other."""
+    test_gradients_of_many_rows(g, T, H, dtype, dropout)
+
+
+@gpu
+@pytest.mark.parametrize("T,H,dtype", [(3, 12288, torch.bfloat16), (153, 12288, torch.float32),
+                                       (160, 16392, torch.float16), (170, 32768, torch.bfloat16)])
+@pytest.mark.parametrize("dropout", [False, True])
+def test_gradients_of_long_rows(g, T, H, dtype, dropout):
+    test_gradients_of_many_rows(g, T, H, dtype, dropout)
+
+
+@gpu
 @pytest.mark.parametrize("T,H,dtype", [
     (608, 8, torch.bfloat16), (650, 8192, torch.bfloat16), (700, 4104, torch.float16),
     (1400, 2048, torch.float32), (615, 16384, torch.bfloat16), (640, 8192, torch.float32),
