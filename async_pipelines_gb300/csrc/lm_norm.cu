@@ -4,6 +4,9 @@
 #include <cstring>
 
 #include "gemm_ws_lm.h"
+#ifdef GEMM_WS_DEBUG
+#include "gemm_ws_debug.h"
+#endif
 #include "handle.cuh"
 #include "lm_norm_kernel.cuh"
 
@@ -479,5 +482,21 @@ int gemm_ws_add_rms_norm_backward(gemm_ws_t* h, int dtype, const void* dy, int64
     default: return launch_grad<float>(h, t, path, q, dweight, s);
   }
 }
+
+#ifdef GEMM_WS_DEBUG
+int gemm_ws_debug_row_columns(int64_t cols, int64_t first, int count, int* rows) {
+  if (cols < 1 || cols > kMaxDim || first < 0 || first > kMaxDim / gws::GROUP + 1 || count < 0 || !rows)
+    return GEMM_WS_ERR_INVALID_ARG;
+  const int end = static_cast<int>(cols), groups = static_cast<int>(ceil_div(cols, gws::GROUP));
+  for (int i = 0; i < count; ++i) {
+    const int c = gws::column_of(static_cast<int>(first) + i, groups, end);
+    int* r = rows + 3 * i;
+    r[0] = c;
+    r[1] = gws::has_columns(c, gws::GROUP, end);
+    r[2] = gws::has_columns(c, 2 * gws::GROUP, end);
+  }
+  return GEMM_WS_OK;
+}
+#endif
 
 }  // extern "C"

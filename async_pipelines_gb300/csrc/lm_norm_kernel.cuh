@@ -284,6 +284,15 @@ __device__ __forceinline__ Row<T> row_of(const void* first, int64_t row, int64_t
   return {static_cast<const T*>(first) + row * ld, far && row > 0, far && row + 1 < rows};
 }
 
+// The column at which group `g` of a row begins (the row's end for a thread without a
+// group), and whether `n` columns from c on are all in the row. Rows have up to 2^31 - 1
+// columns, so neither a group past the last nor c + n may be formed in 32 bits: they wrap,
+// and a thread without a group would store below the row.
+__host__ __device__ constexpr int column_of(int g, int groups, int cols) {
+  return g < groups ? g * GROUP : cols;
+}
+__host__ __device__ constexpr bool has_columns(int c, int n, int cols) { return cols - c >= n; }
+
 // Columns [c, c + 8) of a row whose end is `cols`; past it zeros. WHOLE (not
 // ANY): a group moves in 16-byte pieces and nothing is tested. Else a group that
 // does not start on a 16-byte boundary is cut out of the 16-byte pieces around it,
@@ -295,12 +304,13 @@ __device__ __forceinline__ Raw<T> load_group(const Row<T>& row, int c, int cols)
   constexpr int PIECES = WORDS<T> / 4;
   const uintptr_t at = reinterpret_cast<uintptr_t>(src);
   const int off = static_cast<int>(at & 15);
-  const bool whole = c + GROUP <= cols;
+  const bool whole = has_columns(c, GROUP, cols);
   Raw<T> raw;
   if (WHOLE || (whole && off == 0)) {
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) raw.w[i] = reinterpret_cast<const uint4*>(src)[i];
-  } else if (whole && (c > 0 || row.before) && (c + 2 * GROUP <= cols || row.after)) {
+  } else if (whole && (c > 0 || row.before) &&
+             (has_columns(c, 2 * GROUP, cols) || row.after)) {
     uint32_t in[WORDS<T> + 4], out[WORDS<T>];
 #pragma unroll
     for (int i = 0; i <= PIECES; ++i) {
@@ -395,7 +405,7 @@ __device__ __forceinline__ void store_group(T* row, int c, int cols, int t, int 
     words_of(raw, own);
 #pragma unroll
     for (int i = 0; i < 4; ++i) in[i] = __shfl_up_sync(0xffffffffu, own[WORDS<T> - 4 + i], 1);
-    const bool whole = c + GROUP <= cols;
+    const bool whole = has_columns(c, GROUP, cols);
     if (off == 0 && whole) {
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) reinterpret_cast<uint4*>(dst)[i] = raw.w[i];
@@ -418,7 +428,7 @@ __device__ __forceinline__ void store_group(T* row, int c, int cols, int t, int 
         store_lead<4>(at, first);
       }
       // The right neighbour stores the piece that begins here, if all of it is there.
-      if (!(right && c + GROUP + lead <= cols)) {
+      if (!(right && has_columns(c, GROUP + lead, cols))) {
         uint32_t end[8], rest[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -434,7 +444,7 @@ __device__ __forceinline__ void store_group(T* row, int c, int cols, int t, int 
     // The row's last group, not whole: what the left neighbour begins, if all of
     // that piece is there, and the rest by elements.
     int from = 0;
-    if (off != 0 && left && c + lead <= cols) {
+    if (off != 0 && left && has_columns(c, lead, cols)) {
 #pragma unroll
       for (int i = 0; i < WORDS<T>; ++i) in[4 + i] = own[i];
       shift_bytes<WORDS<T>>(in, 16 - off, out);
@@ -461,14 +471,14 @@ __device__ __forceinline__ void store_bytes(uint8_t* row, int c, int cols, int t
     using Word = unsigned long long;
     const Word own = raw.x | static_cast<Word>(raw.y) << 32;
     const Word other = __shfl_up_sync(0xffffffffu, own, 1);
-    const bool whole = c + GROUP <= cols;
+    const bool whole = has_columns(c, GROUP, cols);
     if (off == 0 && whole) {
       *reinterpret_cast<uint2*>(dst) = raw;
       return;
     }
     if (c >= cols) return;
     const int lane = threadIdx.x & 31;
-    const bool left = off != 0 && lane > 0 && t > 0 && c + lead <= cols;
+    const bool left = off != 0 && lane > 0 && t > 0 && has_columns(c, lead, cols);
     if (left) *reinterpret_cast<Word*>(at - off) = own << (8 * off) | other >> (8 * lead);
     if (off != 0 && whole) {
       if (!left) {
@@ -485,7 +495,7 @@ __device__ __forceinline__ void store_bytes(uint8_t* row, int c, int cols, int t
         if ((at + n) & 4)
           *reinterpret_cast<uint32_t*>(dst + n) = __funnelshift_r(first[0], first[1], 8 * n);
       }
-      if (!(lane < 31 && t + 1 < team && c + GROUP + lead <= cols)) {
+      if (!(lane < 31 && t + 1 < team && has_columns(c, GROUP + lead, cols))) {
         const Word end = own >> (8 * lead);
         const uint32_t rest[2] = {static_cast<uint32_t>(end), static_cast<uint32_t>(end >> 32)};
         store_tail<2>(at + lead, rest, off);
@@ -1291,12 +1301,12 @@ __global__ void __launch_bounds__(DROP_THREADS) dropout_rows_kernel(const __grid
     const int g = g0 + t;
     const bool mine = there && g < groups;
     Raw<T> raw = {};
-    if (mine) raw = load_group<false>(x, g * GROUP, p.cols);
+    if (mine) raw = load_group<false>(x, column_of(g, groups, p.cols), p.cols);
     float v[1][GROUP];
     unpack(raw, v[0]);
     const uint64_t counter[1] = {first + static_cast<uint64_t>(row) * groups + g};
     if (p.drop.on) drop_groups(p.drop, seed, counter, v);
-    store_group<false>(y, (mine ? g : groups + t) * GROUP, p.cols, t, team, pack<T>(v[0]));
+    store_group<false>(y, column_of(mine ? g : groups, groups, p.cols), p.cols, t, team, pack<T>(v[0]));
   }
 }
 

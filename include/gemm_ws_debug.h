@@ -102,6 +102,13 @@ int gemm_ws_debug_noalloc_configure(int device, int fault, long long timeout_ms)
 int gemm_ws_debug_ce_units(int cta_group, int clusters, int bn, int count, const int* jobs,
                            int num_jobs, int* rows, int64_t max_rows, int64_t* num_rows);
 
+/* Where the threads of a row of `cols` columns stand that have the groups of eight
+ * columns `first`, first + 1, ..., of which those past the row's end are nobody's;
+ * host arithmetic only, the same functions the dropout kernel for any rows runs. rows:
+ * for each of `count` threads 3 ints: its first column, whether all eight columns from
+ * there are in the row, and whether sixteen are. */
+int gemm_ws_debug_row_columns(int64_t cols, int64_t first, int count, int* rows);
+
 #ifdef __cplusplus
 }
 #endif
