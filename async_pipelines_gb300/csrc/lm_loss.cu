@@ -194,8 +194,12 @@ int ring_stages(const Tiling& t) {
   return n < ce::MAX_STAGES ? n : ce::MAX_STAGES;
 }
 
+// Rows, columns and the copies' coordinates are 32-bit numbers in the kernels, up to
+// the end of an extent's last tile, stage or piece, which lies less than this far behind it.
+constexpr int64_t kMaxExtent = (int64_t{1} << 31) - 4096;
+
 int check_sizes(const gemm_ws* h, int64_t T, int64_t H, int64_t V) {
-  if (!h || T < 0 || H < 1 || V < 1 || T > kMaxDim || H > kMaxDim || V > kMaxDim)
+  if (!h || T < 0 || H < 1 || V < 1 || T > kMaxExtent || H > kMaxExtent || V > kMaxExtent)
     return GEMM_WS_ERR_INVALID_ARG;
   if (T * H > kMaxElems || V * H > kMaxElems || T * V > kMaxElems) return GEMM_WS_ERR_INVALID_ARG;
   if (H % 8 != 0) return GEMM_WS_ERR_ALIGNMENT;

@@ -161,6 +161,9 @@ struct Unit {
 
 constexpr int GROUP_M = 8;   // tiles walk 8 rows of tiles down, then step a column (L2 reuse)
 
+// ceil(a / b); a may be any int (a + b - 1 may not be one).
+__host__ __device__ constexpr int parts_of(int a, int b) { return a / b + (a % b != 0); }
+
 // The tiles of a job, and the ring stages of its K.
 struct Grid {
   int tm, tn, tiles, units, stages;
@@ -169,11 +172,11 @@ template <int CG>
 __host__ __device__ __forceinline__ Grid grid_of(const Params& p, const Job& job, int count) {
   Grid g;
   const int m = job.m < 0 ? count : job.m, k = job.k < 0 ? count : job.k;
-  g.tm = (m + BM * CG - 1) / (BM * CG);
-  g.tn = (job.n + p.bn - 1) / p.bn;
+  g.tm = parts_of(m, BM * CG);
+  g.tn = parts_of(job.n, p.bn);
   g.tiles = g.tm * g.tn;
   g.units = g.tiles * job.splits;
-  g.stages = (k + BK * ksub<CG>() - 1) / (BK * ksub<CG>());
+  g.stages = parts_of(k, BK * ksub<CG>());
   return g;
 }
 

@@ -114,8 +114,8 @@ int gemm_ws_add_rms_norm_backward(gemm_ws_t* h, int dtype, const void* dy, int64
  *  - workspace: gemm_ws_linear_ce_workspace bytes on the device, 256-byte
  *    aligned, for this call alone (its contents mean nothing before or after).
  *  - hidden: a multiple of 8; weight 16-byte aligned, ldw a multiple of 8 (x
- *    may lie anywhere). 0 <= tokens, 1 <= vocab, 8 <= hidden, each < 2^31,
- *    tokens * hidden, vocab * hidden and tokens * vocab < 2^40.
+ *    may lie anywhere). 0 <= tokens, 1 <= vocab, 8 <= hidden, each at most
+ *    2^31 - 4096; tokens * hidden, vocab * hidden and tokens * vocab at most 2^40.
  * Products in bf16 with fp32 sums in tensor memory; everything after them in
  * fp32. Launches three kernels; two where x's rows lie on 16-byte boundaries and
  * there are up to 128 of them or no more tiles than run at once, one for up to

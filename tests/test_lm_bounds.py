@@ -6,6 +6,8 @@ outputs watched.
 """
 from __future__ import annotations
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -39,6 +41,23 @@ def test_columns_of_a_row(dbg, cols):
         assert next_whole == (c + 16 <= cols)
 
 
+LARGEST = 2 ** 31 - 4096      # of an extent of the cross entropy
+
+
+@pytest.mark.parametrize("cg,bn", [(1, 256), (1, 96), (2, 256)])
+@pytest.mark.parametrize("extent", [LARGEST - 1, LARGEST, 2 ** 31 - 256, 2 ** 31 - 255, 2 ** 31 - 1])
+def test_units_of_the_largest_extents(dbg, cg, bn, extent):
+    """A vocabulary, a hidden size or a count of tokens of almost 2^31: all of its tiles are walked."""
+    for count, n, k, tiles in ((1, extent, 8, -(-extent // bn)), (1, 8, extent, 1),
+                               (extent, 8, 8, -(-extent // (128 * cg)))):
+        jobs = (ctypes.c_int * 4)(-1, n, k, 1)
+        rows, total = np.zeros((1, 8), dtype=np.int32), ctypes.c_int64()
+        assert dbg.gemm_ws_debug_ce_units(cg, 7, bn, count, jobs, 1, rows.ctypes.data, 1,
+                                          ctypes.byref(total)) == gemm_ws.OK
+        assert total.value == tiles
+        assert tuple(rows[0, 6:]) == (0, -(-k // (64 * cg)))
+
+
 # ------------------------------------------------------------------ on the GPU
 
 gpu = pytest.mark.gpu
@@ -70,4 +89,39 @@ def test_dropout_of_the_longest_rows(g, cols):
     share = float((row[0, ::1024] == 0).float().mean())
     assert abs(share - 0.5) < 2e-3      # two million samples: a deviation of 3.5e-4
     del buf, row
+    torch.cuda.empty_cache()
+
+
+@gpu
+def test_extents_past_the_largest_are_refused(g):
+    for sizes in ((LARGEST + 1, 8, 8), (1, LARGEST + 8, 8), (1, 8, LARGEST + 1), (2 ** 31 - 1, 8, 1),
+                  (1, 8, 2 ** 31 - 255), (2 ** 31, 8, 1)):
+        for backward in (False, True):
+            with pytest.raises(gemm_ws.GemmWSError) as e:
+                g.linear_cross_entropy_workspace(*sizes, backward)
+            assert e.value.status == gemm_ws.ERR_INVALID_ARG
+    assert g.linear_cross_entropy_workspace(1, 8, LARGEST) > 0
+    assert g.linear_cross_entropy_workspace(1, LARGEST, 8) > 0
+
+
+@gpu
+def test_the_largest_vocabulary(g):
+    """2^31 - 4096 words. A part of a row's sum is added to 2e5 times, each time off by up to 2^-24 of
+    it: by about sqrt(2e5) of that, 3e-5, at the most."""
+    T, H, V, step = 3, 8, LARGEST, 2 ** 24
+    gen = torch.Generator("cuda").manual_seed(5)
+    w = torch.empty(V, H, device="cuda", dtype=torch.bfloat16)
+    for a in range(0, V, step):
+        w[a:a + step] = torch.randn(min(step, V - a), H, device="cuda", generator=gen) / 2
+    x = torch.randn(T, H, device="cuda", generator=gen).bfloat16()
+    t = torch.tensor([V - 1, 0, V // 2], device="cuda")
+    loss, lse, mean = (torch.empty(n, device="cuda") for n in (T, T, 2))
+    g.linear_cross_entropy(x, w, t, loss, lse, mean=mean)
+    parts = [torch.logsumexp(x.double() @ w[a:a + step].double().T, 1) for a in range(0, V, step)]
+    want = torch.logsumexp(torch.stack(parts), 0)
+    assert torch.all((lse - want).abs() <= 1e-4)
+    at = (x.double() * w[t].double()).sum(1)
+    assert torch.all((loss - (want - at)).abs() <= 1e-4)
+    assert abs(float(mean[0]) - float((want - at).mean())) <= 1e-4
+    del w
     torch.cuda.empty_cache()
