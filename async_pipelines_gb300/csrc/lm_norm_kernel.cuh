@@ -596,13 +596,17 @@ __device__ __forceinline__ bool team_sync(int id, int threads, bool ok) {
 
 // The sum over a team of a value a thread, in every thread, in a fixed order.
 // `ok` is false after it unless it was true in all of them: the team's warps give
-// up together. `box`: a slot for each warp of the CTA, not used again before the
-// next sum but one.
+// up together. What the team's threads read before it, they have read: one of them may
+// then fill that memory anew. `box`: a slot for each warp of the CTA, not used again before
+// the next sum but one.
 __device__ __forceinline__ float ring_sum(float sum, int which, int team, float* box, bool* ok) {
   const int warps = team / 32, lane = threadIdx.x % 32;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (warps == 1) return sum;
+  if (warps == 1) {
+    __syncwarp();   // the shuffles alone order no memory
+    return sum;
+  }
   if (lane == 0) box[threadIdx.x / 32] = sum;
   *ok = team_sync(1 + which, team, *ok);
   sum = (lane & 15) < warps ? box[which * warps + (lane & 15)] : 0.0f;
@@ -841,7 +845,6 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
         if (p.h) h[j * team] = pack<T>(v[j]);
       }
     }
-    __syncwarp();
     sum = ring_sum(sum, which, team, box[turn], &ok);
     if (!ok) break;
     if (t == 0 && k + q.stages < rows.count) fetch(k + q.stages, s);   // the row is in registers
@@ -1133,7 +1136,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
       const float sum =
           ring_sum(values_of(sums).x + values_of(sums).y, which, team, box[turn], &ok);
       if (!ok) break;
-      // The whole team is here, so it has done with the row before.
+      // The whole team has been in the sum, so it has done with the row before.
       if (t == 0 && k > 0 && k - 1 + q.stages < rows.count) fetch(k - 1 + q.stages, before);
       // dres = dh + r dy weight - h r^2 mean(dy weight h r)
       const float m = -r * r * (r * sum / static_cast<float>(cols));
