@@ -563,8 +563,6 @@ int gemm_ws_create(gemm_ws_t** out, int device) {
   h->k_snake = k_snake_from_env();
   e = configure_kernels(h->num_sms, &h->max_pair_clusters);
   if (e == cudaSuccess && h->max_pair_clusters < 1) h->cta_group = 1;
-  if (e == cudaSuccess) e = ce_configure(h->num_sms, &h->ce_pair_clusters);
-  if (e == cudaSuccess) e = norm_configure();
   const size_t wbytes = work_words(h->num_sms) * sizeof(uint32_t);
   if (e == cudaSuccess) e = cudaMalloc(&h->work, wbytes);
   if (e == cudaSuccess) e = cudaMemset(h->work, 0, wbytes);

@@ -20,6 +20,8 @@ struct MapCacheEntry {
   CUtensorMap map;
 };
 constexpr int kMapCache = 16;
+// The operators' kernels that take more shared memory than a kernel has by default.
+constexpr int kLargeKernels = 24;
 
 struct gemm_ws {
   int device;
@@ -31,7 +33,6 @@ struct gemm_ws {
   int stream_k;                   // 0 off, 1 where the cost model gains (default), 2 always
   int sk_inline;                  // two-piece tiles: fix-up inside the GEMM (default 1)
   int k_snake;                    // every other unit of a cluster walks K backwards
-  int ce_pair_clusters;           // co-resident 2-CTA clusters of the cross entropy's product
   uint32_t* work;                 // [0] stream-out counter, [1] status, [2] done count, [3] the
                                   // cross entropy's done count, then the in-kernel fix-up words
                                   // (work_words)
@@ -41,6 +42,8 @@ struct gemm_ws {
   PFN_cuTensorMapEncodeTiled_v12000 encode;
   MapCacheEntry map_cache[kMapCache];   // recently encoded tensor maps (host memory)
   int map_cache_next;
+  const void* large[kLargeKernels];     // kernels allowed the shared memory they ask for, in
+                                        // the order of their first use (see allow_smem)
 #ifdef GEMM_WS_DEBUG
   int debug_fault;
   unsigned long long* trace;
@@ -48,20 +51,30 @@ struct gemm_ws {
 #endif
 };
 
-// Sets the shared-memory attributes of the cross entropy's product kernels on
-// the current device; *pair_clusters: how many of its 2-CTA clusters fit at once.
-cudaError_t ce_configure(int num_sms, int* pair_clusters);
-// The same of the norm's gradient.
-cudaError_t norm_configure();
-
 namespace {
 
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxElems = int64_t{1} << 40;
+[[maybe_unused]] constexpr size_t kDefaultSmem = 48 * 1024;   // dynamic shared memory a kernel has unasked
 
 int cuda_fail(gemm_ws* h, cudaError_t e) {
   if (h) h->last_cuda_error = static_cast<int>(e);
   return GEMM_WS_ERR_CUDA;
+}
+
+// Allows `kernel` `bytes` of dynamic shared memory before its first launch by the handle
+// (whose device is current). Not at the handle's creation: that would load every such
+// kernel, 22 of them, for callers that use none (21 ms instead of 0.6).
+[[maybe_unused]] cudaError_t allow_smem(gemm_ws* h, const void* kernel, size_t bytes) {
+  for (const void*& k : h->large) {
+    if (k == kernel) return cudaSuccess;
+    if (k) continue;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(bytes));
+    if (e == cudaSuccess) k = kernel;
+    return e;
+  }
+  return cudaErrorInvalidValue;   // more such kernels than kLargeKernels
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -29,7 +29,8 @@ struct Tiling {
 // rows and hand-over). Up to 128 rows a pair's second CTA would idle.
 // `step`: what the width must be a multiple of.
 Tiling pick_tiling(const gemm_ws* h, int64_t m, int64_t n, int step) {
-  const int64_t pairs = h->ce_pair_clusters;
+  // as many as of the GEMM's: both have one CTA on an SM
+  const int64_t pairs = h->max_pair_clusters;
   if (pairs > 0 && m > ce::BM && ceil_div(m, 2 * ce::BM) * ceil_div(n, ce::BN_MAX) >= pairs)
     return {2, ce::BN_MAX, pairs};
   Tiling best = {1, ce::BN_MAX, h->num_sms};
@@ -175,7 +176,9 @@ int launch(gemm_ws* h, void (*kernel)(P), int64_t blocks, int threads, size_t sm
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, params);
+  cudaError_t e = cudaSuccess;
+  if (smem > kDefaultSmem) e = allow_smem(h, reinterpret_cast<const void*>(kernel), smem);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, params);
   return e == cudaSuccess ? GEMM_WS_OK : cuda_fail(h, e);
 }
 
@@ -283,33 +286,6 @@ ce::Params product_params(const gemm_ws* h, const Plan& q, uint8_t* ws, const Ti
 }
 
 }  // namespace
-
-cudaError_t ce_configure(int num_sms, int* pair_clusters) {
-  const void* kernels[6] = {
-      reinterpret_cast<const void*>(ce::product_kernel<1, ce::LSE>),
-      reinterpret_cast<const void*>(ce::product_kernel<2, ce::LSE>),
-      reinterpret_cast<const void*>(ce::product_kernel<1, ce::GRAD>),
-      reinterpret_cast<const void*>(ce::product_kernel<2, ce::GRAD>),
-      reinterpret_cast<const void*>(ce::product_kernel<1, ce::SUMS>),
-      reinterpret_cast<const void*>(ce::product_kernel<2, ce::SUMS>)};
-  for (const void* k : kernels) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(ce::SMEM_BYTES));
-    if (e != cudaSuccess) return e;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(2 * (num_sms / 2), 1, 1);
-  cfg.blockDim = dim3(ce::THREADS, 1, 1);
-  cfg.dynamicSmemBytes = ce::SMEM_BYTES;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaOccupancyMaxActiveClusters(pair_clusters, ce::product_kernel<2, ce::SUMS>, &cfg);
-}
 
 extern "C" {
 

@@ -76,7 +76,9 @@ int launch(gemm_ws* h, void (*kernel)(P), int64_t blocks, int threads, size_t sm
     cfg.attrs = attr;
     cfg.numAttrs = 1;
   }
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, params);
+  cudaError_t e = cudaSuccess;
+  if (smem > kDefaultSmem) e = allow_smem(h, reinterpret_cast<const void*>(kernel), smem);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, params);
   return e == cudaSuccess ? GEMM_WS_OK : cuda_fail(h, e);
 }
 
@@ -237,31 +239,7 @@ int launch_dropout(gemm_ws* h, bool flat, int64_t blocks, const gws::DropoutPara
                 blocks, gws::DROP_THREADS, 0, s, p);
 }
 
-// Sets the shared-memory attribute of the ring kernels on the current device.
-template <typename T>
-cudaError_t configure_ring() {
-  const int bytes = static_cast<int>(gws::RING_BYTES);
-  for (int vpt : {2, 4})
-    for (int k = 0; k < 3; ++k) {
-      const void* kernel = reinterpret_cast<const void*>(ring_kernel<T, false>(vpt));
-      if (k == 1) kernel = reinterpret_cast<const void*>(ring_kernel<T, true>(vpt));
-      if constexpr (sizeof(T) == 2)
-        if (k == 2) kernel = reinterpret_cast<const void*>(forward_ring_kernel<T>(vpt));
-      const cudaError_t e =
-          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-      if (e != cudaSuccess) return e;
-    }
-  return cudaSuccess;
-}
-
 }  // namespace
-
-cudaError_t norm_configure() {
-  cudaError_t e = configure_ring<__nv_bfloat16>();
-  if (e == cudaSuccess) e = configure_ring<__half>();
-  if (e == cudaSuccess) e = configure_ring<float>();
-  return e;
-}
 
 extern "C" {
 
