@@ -509,6 +509,46 @@ __device__ __forceinline__ void store_bytes(uint8_t* row, int c, int cols, int t
   }
 }
 
+// The e4m3 roundings of v / scale, lowest column first. A product with 1 / scale is off by
+// a unit of the last place or two, which moves a quotient that lies between two e4m3 values
+// (25 of scale 7 to 26, not 24). So the quotients are put between products with a smaller and
+// a larger factor than 1 / scale: where the two round alike, so does what lies between
+// them, and only else (one group in 10^5) are there divisions. (8192 x 8192 bf16, a scale a
+// row: 75 us, 90 with divisions throughout, 70 with the product that rounds some wrongly.)
+__device__ __forceinline__ uint2 quotients(const float (&v)[GROUP], float scale) {
+  auto e4m3 = [](const float (&q)[GROUP]) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[4 * i], q[4 * i + 1]),
+                                                   __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q[4 * i + 2], q[4 * i + 3]),
+                                                   __NV_SATFINITE, __NV_E4M3);
+      w[i] = lo | (hi << 16);
+    }
+    return make_uint2(w[0], w[1]);
+  };
+  // 1 / scale and each factor are off by at most 2^-24 of themselves
+  const float inv = 1.0f / scale;
+  auto times = [&](float factor) {
+    const Pair f = pair_of(factor, factor);
+    float q[GROUP];
+#pragma unroll
+    for (int i = 0; i < GROUP; i += 2) {
+      const float2 two = values_of(mul2(pair_of(v[i], v[i + 1]), f));
+      q[i] = two.x;
+      q[i + 1] = two.y;
+    }
+    return e4m3(q);
+  };
+  const uint2 least = times(inv * (1.0f - 0x1p-22f)), most = times(inv * (1.0f + 0x1p-22f));
+  if (least.x == most.x && least.y == most.y) return least;
+  float q[GROUP];
+#pragma unroll
+  for (int i = 0; i < GROUP; ++i) q[i] = v[i] / scale;
+  return e4m3(q);
+}
+
 // ------------------------------------------------------------ reductions
 
 // The larger, or NaN where either is NaN.
@@ -738,19 +778,10 @@ __global__ void __launch_bounds__(MOST, MOST == 256 ? (sizeof(T) == 2 ? 3 : 2) :
         if ((t & 15) == 0 && g < groups)
           p.scales[row * ((cols + QUANT_GROUP - 1) / QUANT_GROUP) + g / 16] = scale;
       }
-      const float inv = 1.0f / scale;
-      uint32_t out[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-            make_float2(v[k][4 * i] * inv, v[k][4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-            make_float2(v[k][4 * i + 2] * inv, v[k][4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
-        out[i] = lo | (hi << 16);
-      }
+      const uint2 out = quotients(v[k], scale);
       if (PATH == ANY || g < groups)
         store_bytes<WHOLE>(static_cast<uint8_t*>(p.y) + row * p.ldy, g * GROUP, cols, t, team,
-                           make_uint2(out[0], out[1]));
+                           out);
     }
   }
 }
