@@ -46,7 +46,7 @@ Tiling pick_tiling(const gemm_ws* h, int64_t m, int64_t n, int step) {
   return best;
 }
 
-// G of one piece takes at most this many bytes, or 4096 columns.
+// G of one piece, in whole tiles of rows, takes at most this many bytes, or 4096 columns.
 constexpr int64_t kPieceBytes = int64_t{256} << 20;
 constexpr int64_t kMinPiece = 4096;
 constexpr int64_t kShortK = 128;
@@ -93,7 +93,7 @@ Plan make_plan(const gemm_ws* h, int64_t T, int64_t H, int64_t V, bool backward)
     q.part = take(q.slots * T * 8);
     q.block_sum = take(q.blocks * 4);
   } else {
-    q.piece = kPieceBytes / (2 * T) / ce::BN_MAX * ce::BN_MAX;
+    q.piece = kPieceBytes / (2 * q.rows) / ce::BN_MAX * ce::BN_MAX;
     if (q.piece < kMinPiece) q.piece = kMinPiece;
     if (q.piece > round_up(V, ce::BN_MAX)) q.piece = round_up(V, ce::BN_MAX);
     q.pieces = ceil_div(V, q.piece);
