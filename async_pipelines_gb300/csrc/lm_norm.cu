@@ -117,19 +117,24 @@ Team pick_team(const gemm_ws* h, int64_t rows, int64_t cols, gws::Path path, int
   return t;
 }
 
+// The forward pass's `any_vpt`.
+template <typename T>
+constexpr int kAnyVpt = sizeof(T) == 2 ? 2 : 1;
+
 // The ring needs some rows of each SM to be worth its set-up.
 constexpr int64_t kRingRows = 4;
 
 // How the rows pass through the ring: four groups a thread, the smallest teams
-// that hold a row, and two rows at least for each team; two groups and larger teams
-// where the ring has not that many rows (8192 fp32 columns). *vpt: which. False
+// that hold a row, and two rows at least for each team; of fp32 (8192 columns, say) two
+// groups and larger teams where the ring has not that many rows (of 16-bit types it always
+// has: teams * 2 rows of 3 matrices are at most 16384 * 2 * 3 * 2 bytes). *vpt: which. False
 // where two rows do not fit, or a row is more than a CTA's warps hold.
 template <typename Q>
 bool plan_ring(int64_t cols, int64_t size, int inputs, Q* q, int* vpt) {
   const int64_t row = cols * size, groups = cols / gws::GROUP;
   int64_t room = gws::RING_BYTES / (inputs * row);
   if (room > gws::RING_MAX_STAGES) room = gws::RING_MAX_STAGES;
-  for (*vpt = 4; *vpt >= 2; *vpt /= 2) {
+  for (*vpt = 4; *vpt >= (size == 2 ? 4 : 2); *vpt /= 2) {
     const int64_t warps = ceil_div(groups, 32 * *vpt);
     if (warps > gws::RING_WARPS) return false;
     q->row_bytes = static_cast<uint32_t>(row);
@@ -144,26 +149,24 @@ bool plan_ring(int64_t cols, int64_t size, int inputs, Q* q, int* vpt) {
 // The kernel instance for a team and a path. Fewer threads a block leave each
 // more registers: 64 with 1024, 128 with 512. NARROW: four groups a thread and at
 // most 256 threads, in 16 bits kept to 80 registers, so that an SM holds three rows of
-// 8192 columns (78 us; 84 with two).
-#define LM_NORM_INSTANCE(KERNEL, NARROW, T, PATH, ...)                              \
+// 8192 columns (78 us; 84 with two). TWO: 2, or 1 where no team of the path has two groups
+// a thread.
+#define LM_NORM_INSTANCE(KERNEL, NARROW, TWO, T, PATH, ...)                         \
   (t.vpt == 1                  ? gws::KERNEL<T, PATH, 1, 1024, ##__VA_ARGS__>       \
-   : t.vpt == 2                ? gws::KERNEL<T, PATH, 2, 512, ##__VA_ARGS__>        \
+   : t.vpt == 2                ? gws::KERNEL<T, PATH, TWO, 1024 / TWO, ##__VA_ARGS__> \
    : t.threads * t.rows <= 256 ? gws::KERNEL<T, PATH, 4, NARROW, ##__VA_ARGS__>     \
    : t.threads * t.rows <= 512 ? gws::KERNEL<T, PATH, 4, 512, ##__VA_ARGS__>        \
                                : gws::KERNEL<T, PATH, 4, 1024, ##__VA_ARGS__>)
 
 template <typename T, int Q>
 int launch_norm(gemm_ws* h, const Team& t, gws::Path path, const gws::NormParams& p, cudaStream_t s) {
-  auto kernel = LM_NORM_INSTANCE(add_rms_norm_kernel, 512, T, gws::ANY, Q);
-  if (path == gws::FAST) kernel = LM_NORM_INSTANCE(add_rms_norm_kernel, 256, T, gws::FAST, Q);
-  if constexpr (Q == 0)   // 8 bits are for serving: with dropout they take the general path
-    if (path == gws::DROP) kernel = LM_NORM_INSTANCE(add_rms_norm_kernel, 512, T, gws::DROP, Q);
+  // 8 bits are for serving: with dropout they take the general path, with the aligned one's teams
+  auto kernel =
+      LM_NORM_INSTANCE(add_rms_norm_kernel, 512, (Q > 0 ? 2 : kAnyVpt<T>), T, gws::ANY, Q);
+  if (path == gws::FAST) kernel = LM_NORM_INSTANCE(add_rms_norm_kernel, 256, 2, T, gws::FAST, Q);
+  if constexpr (Q == 0)
+    if (path == gws::DROP) kernel = LM_NORM_INSTANCE(add_rms_norm_kernel, 512, 2, T, gws::DROP, Q);
   return launch(h, kernel, ceil_div(p.rows, t.rows), t.threads * t.rows, 0, s, p);
-}
-
-template <typename T>
-auto forward_ring_kernel(int vpt) {
-  return vpt == 4 ? gws::add_rms_norm_ring_kernel<T, 4> : gws::add_rms_norm_ring_kernel<T, 2>;
 }
 
 template <typename T>
@@ -194,8 +197,10 @@ int launch_dweight(gemm_ws* h, const float* partial, int64_t blocks, int cols, v
 
 template <typename T, bool ON>
 auto ring_kernel(int vpt) {
-  return vpt == 4 ? gws::add_rms_norm_grad_ring_kernel<T, ON, 4>
-                  : gws::add_rms_norm_grad_ring_kernel<T, ON, 2>;
+  auto kernel = gws::add_rms_norm_grad_ring_kernel<T, ON, 4>;
+  if constexpr (sizeof(T) == 4)
+    if (vpt == 2) kernel = gws::add_rms_norm_grad_ring_kernel<T, ON, 2>;
+  return kernel;
 }
 
 template <typename T>
@@ -211,9 +216,9 @@ int launch_grad_ring(gemm_ws* h, int vpt, const gws::NormGradRing& q, void* dwei
 template <typename T>
 int launch_grad(gemm_ws* h, const Team& t, gws::Path path, const gws::NormGradParams& p, void* dweight,
                 cudaStream_t s) {
-  const auto kernel = path == gws::ANY    ? LM_NORM_INSTANCE(add_rms_norm_grad_kernel, 512, T, gws::ANY)
-                      : path == gws::FAST ? LM_NORM_INSTANCE(add_rms_norm_grad_kernel, 512, T, gws::FAST)
-                                          : LM_NORM_INSTANCE(add_rms_norm_grad_kernel, 512, T, gws::DROP);
+  const auto kernel = path == gws::ANY    ? LM_NORM_INSTANCE(add_rms_norm_grad_kernel, 512, 1, T, gws::ANY)
+                      : path == gws::FAST ? LM_NORM_INSTANCE(add_rms_norm_grad_kernel, 512, 2, T, gws::FAST)
+                                          : LM_NORM_INSTANCE(add_rms_norm_grad_kernel, 512, 2, T, gws::DROP);
   const int threads = t.threads * t.rows;
   const size_t smem = t.rows > 1 ? t.rows * partial_pitch(p.cols) * sizeof(float) : 0;   // at most 32 KB
   // As many blocks as run at once (1024 threads of an SM, 512 with more than one group
@@ -354,12 +359,12 @@ int gemm_ws_add_rms_norm(gemm_ws_t* h, int dtype, const void* x, int64_t ldx,
     ring.timeout_ns = h->timeout_ns;
     if (plan_ring(cols, size, residual ? 2 : 1, &ring, &vpt)) {
       return launch(h,
-                    dtype == GEMM_WS_BF16 ? forward_ring_kernel<__nv_bfloat16>(vpt)
-                                          : forward_ring_kernel<__half>(vpt),
+                    dtype == GEMM_WS_BF16 ? gws::add_rms_norm_ring_kernel<__nv_bfloat16, 4>
+                                          : gws::add_rms_norm_ring_kernel<__half, 4>,
                     h->num_sms, gws::RING_THREADS, gws::RING_BYTES, s, ring);
     }
   }
-  const Team t = pick_team(h, rows, cols, path, size == 2 ? 2 : 1);
+  const Team t = pick_team(h, rows, cols, path, size == 2 ? kAnyVpt<__half> : kAnyVpt<float>);
   q.team = t.threads;
   switch (dtype) {
     case GEMM_WS_BF16: return launch_norm<__nv_bfloat16>(h, output, t, path, q, s);
