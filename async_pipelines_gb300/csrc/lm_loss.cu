@@ -282,6 +282,9 @@ ce::Params product_params(const gemm_ws* h, const Plan& q, uint8_t* ws, const Ti
   p.part_stride = T;
   p.status = h->work + 1;
   p.timeout_ns = h->timeout_ns;
+#ifdef GEMM_WS_DEBUG
+  p.debug_fault = h->debug_fault;
+#endif
   return p;
 }
 

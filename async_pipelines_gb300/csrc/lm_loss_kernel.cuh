@@ -148,6 +148,9 @@ struct Params {
   uint32_t* done;            // CTAs that ended; zero at launch, left zero
   uint32_t* status;
   unsigned long long timeout_ns;
+#ifdef GEMM_WS_DEBUG
+  int debug_fault;           // 3: A's producer brings nothing
+#endif
 };
 
 // A unit of work: a tile of a job, or of one cut of its K.
@@ -298,6 +301,9 @@ __device__ __forceinline__ void producer(const Params& p, uint32_t sbase, uint32
   uint32_t s = 0, ph = 0, g = 0;
   bool ok = true;
   Unit w;
+#ifdef GEMM_WS_DEBUG
+  if (p.debug_fault == 3 && a_part) return;   // injected fault: no stage ever fills
+#endif
   for (int i = 0; ok && next_unit<CG>(p, walk, i, w); ++i) {
     const Job& job = *w.job;
     const CUtensorMap* map = a_part ? &job.tmA : &job.tmB;

@@ -357,6 +357,9 @@ int gemm_ws_add_rms_norm(gemm_ws_t* h, int dtype, const void* x, int64_t ldx,
     ring.p = q;
     ring.status = h->work + 1;
     ring.timeout_ns = h->timeout_ns;
+#ifdef GEMM_WS_DEBUG
+    ring.debug_fault = h->debug_fault;
+#endif
     if (plan_ring(cols, size, residual ? 2 : 1, &ring, &vpt)) {
       return launch(h,
                     dtype == GEMM_WS_BF16 ? gws::add_rms_norm_ring_kernel<__nv_bfloat16, 4>
@@ -450,6 +453,9 @@ int gemm_ws_add_rms_norm_backward(gemm_ws_t* h, int dtype, const void* dy, int64
     ring.p = q;
     ring.status = h->work + 1;
     ring.timeout_ns = h->timeout_ns;
+#ifdef GEMM_WS_DEBUG
+    ring.debug_fault = h->debug_fault;
+#endif
     if (plan_ring(cols, size, dhidden ? 3 : 2, &ring, &vpt)) {
       switch (dtype) {
         case GEMM_WS_BF16: return launch_grad_ring<__nv_bfloat16>(h, vpt, ring, dweight, s);

@@ -792,6 +792,9 @@ struct NormRing {
   uint32_t row_bytes;   // of one matrix
   uint32_t* status;
   unsigned long long timeout_ns;
+#ifdef GEMM_WS_DEBUG
+  int debug_fault;      // 3: only the first stages are ever filled
+#endif
 };
 
 // The forward pass with dropout for many rows of a 16-bit type that lie FAST: as
@@ -826,6 +829,9 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
   const uint32_t stage0 = smem_addr(ring) + which * q.stages * stage_bytes;
   auto full = [&](int s) { return smem_addr(&bars[which * q.stages + s]); };
   auto fetch = [&](int64_t k, int s) {
+#ifdef GEMM_WS_DEBUG
+    if (q.debug_fault == 3 && k >= q.stages) return;   // injected fault: the row never comes
+#endif
     const int64_t row = rows.first + k * rows.step;
     const uint32_t dst = stage0 + s * stage_bytes;
     mbar_arrive_expect_tx(full(s), stage_bytes);
@@ -1072,6 +1078,9 @@ struct NormGradRing {
   uint32_t row_bytes;   // of one matrix
   uint32_t* status;
   unsigned long long timeout_ns;
+#ifdef GEMM_WS_DEBUG
+  int debug_fault;      // 3: only the first stages are ever filled
+#endif
 };
 
 template <typename T, bool ON, int VPT>
@@ -1108,6 +1117,9 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
     auto full = [&](int s) { return smem_addr(&bars[which * q.stages + s]); };
     // One thread of the team fetches row k into stage s.
     auto fetch = [&](int64_t k, int s) {
+#ifdef GEMM_WS_DEBUG
+      if (q.debug_fault == 3 && k >= q.stages) return;   // injected fault: the row never comes
+#endif
       const int64_t row = rows.first + k * rows.step;
       const uint32_t dst = stage0 + s * stage_bytes;
       mbar_arrive_expect_tx(full(s), stage_bytes);

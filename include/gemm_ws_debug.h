@@ -30,7 +30,10 @@ extern "C" {
  *    pieces that write their partial for the in-kernel fix-up never set
  *    their written flag, so the piece that adds it can only stop waiting by
  *    the watchdog (its fix-up words are then left part-way, for
- *    gemm_ws_query_status to clear).
+ *    gemm_ws_query_status to clear); 3 the cross entropy's product kernel never
+ *    loads its first operand, and the norm's kernels that bring rows
+ *    through shared memory load none after the first stages, so each wait for
+ *    them can only end by the watchdog.
  *  - trace: device buffer of num_units * ctas_per_cluster * 2 uint64 (see
  *    gemm_ws_debug_launch_shape) or NULL. For work unit u and CTA rank r
  *    in its cluster, trace[(u*ctas_per_cluster + r)*2] = global time (ns) at which
