@@ -8,8 +8,10 @@
 //
 // Tokens that are not counted (target == ignore) are left out before the
 // first product: a gather packs the counted rows of x, so such a row costs
-// nothing, is never read, and cannot put a NaN into dweight. How many rows
-// are counted is known on the device only; every kernel reads it there.
+// no product, and cannot put a NaN into dweight. How many rows are counted is
+// known on the device only; every kernel reads it there. (A loss of few rows or
+// of few tiles takes x as it lies: there an uncounted row is multiplied like any
+// other, and its sums, which are its own, are left out at the end.)
 //
 // One persistent warp-specialised product kernel serves all of it, with the
 // roles of the GEMM (two TMA producer warps, one MMA thread, eight epilogue
@@ -17,9 +19,13 @@
 //   LSE    the logits' tile stays in TMEM; each row's running maximum and sum
 //          of exponentials leave, and the target's logit.
 //   GRAD   the tile is computed again for a piece of the vocabulary and G
-//          leaves in bf16. That is the one rounding of G (2^-9 of each
-//          value, independent from element to element, so the sums that dx and
-//          dweight are lose no more than by their own rounding).
+//          leaves in bf16, since the tensor cores multiply 16-bit operands. That
+//          rounds G once, by up to 2^-9 of each value, independently from element
+//          to element. In the norm dx and dweight are then off by 1.9e-3 (4096
+//          tokens x 4096 over 131072), 2.3e-3 (256 x 256 over 1000), 2.6e-3 (few
+//          tokens; 5e-3 in the worst of 8000 random small cases), where their own
+//          rounding to bf16 alone makes 1.7e-3. A second product with what the
+//          rounding leaves would take them to that, for twice the operations.
 //   SUMS   the two products of that piece in one launch, dx's units (fp32,
 //          added to by later pieces) before dweight's (bf16, final). G^T, x
 //          and weight are read as they lie, as MN-major operands, so nothing

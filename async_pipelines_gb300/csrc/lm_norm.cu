@@ -98,8 +98,9 @@ struct Team {
 // columns four, so that an SM has more bytes in flight for the threads that it
 // can hold (8192 x 8192 bf16: 78 us with four, 86 with two); beyond 8192 columns
 // always four. On the general path, whose loads take many registers, a row longer
-// than a warp's 32 groups takes a block with `any_vpt` groups a thread (8192 x 8191
-// bf16, forward: 188 us with two, 264 with one; fp32 169 and 152; backward 376 and 286).
+// than a warp's 32 groups takes a block with `any_vpt` groups a thread (8192 x 8191 bf16,
+// forward: 163 us with two, 232 with one; 5000 x 4095 fp32 82 and 78; backward 8192 x 8191 bf16 314
+// and 249).
 Team pick_team(const gemm_ws* h, int64_t rows, int64_t cols, gws::Path path, int any_vpt) {
   const int64_t groups = ceil_div(cols, gws::GROUP);
   const bool any = path == gws::ANY;

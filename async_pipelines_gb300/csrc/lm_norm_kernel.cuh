@@ -1249,9 +1249,10 @@ struct DweightParams {
   void* dweight;
 };
 
-// dweight[c] = the sum of the blocks' partial rows, in a fixed order. All of a
-// thread's rows are in flight at once: a thread has a few of them (1000 at most in
-// eight turns), four columns of each.
+// dweight[c] = the sum of the blocks' partial rows, in a fixed order. A thread has four
+// columns of every 128th row, eight of them in flight at once. There are 152 rows from a ring
+// (two a thread), and up to 2432 (19 a thread) where the blocks are smallest: of 64 threads,
+// of unaligned rows of 257 to 512 columns.
 template <typename T>
 __global__ void __launch_bounds__(DW_THREADS)
     dweight_kernel(const __grid_constant__ DweightParams p) {
