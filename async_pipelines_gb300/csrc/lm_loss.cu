@@ -63,7 +63,8 @@ struct Plan {
   int64_t pitch, rows;   // of the packed rows of x; rows of G, too
   int64_t blocks;     // of the joining kernel
   // byte offsets in the workspace
-  int64_t packed, place, target, count, logit, part, block_sum, lse, grad, g, sums_at, bytes;
+  int64_t packed, place, target, count, logit, part, block_sum, lse, grad, scale, g, sums_at,
+      bytes;
 };
 
 Plan make_plan(const gemm_ws* h, int64_t T, int64_t H, int64_t V, bool backward) {
@@ -115,6 +116,7 @@ Plan make_plan(const gemm_ws* h, int64_t T, int64_t H, int64_t V, bool backward)
     if (q.cuts > kMaxCuts) q.cuts = kMaxCuts;
     q.lse = take(T * 4);
     q.grad = take(T * 4);
+    q.scale = take(4);
     q.g = take(q.rows * q.piece * 2);
     q.sums_at = take(q.cuts * T * H * 4);
   }
@@ -422,6 +424,7 @@ int gemm_ws_linear_ce_backward(gemm_ws_t* h, const uint16_t* x, int64_t ldx,
   pack.grad_step = grad_step;
   pack.lse_out = reinterpret_cast<float*>(ws + q.lse);
   pack.grad_out = reinterpret_cast<float*>(ws + q.grad);
+  pack.scale = reinterpret_cast<float*>(ws + q.scale);
   uint16_t* g = reinterpret_cast<uint16_t*>(ws + q.g);
   float* sums = reinterpret_cast<float*>(ws + q.sums_at);
 
@@ -437,6 +440,7 @@ int gemm_ws_linear_ce_backward(gemm_ws_t* h, const uint16_t* x, int64_t ldx,
   jg.out = ce::OUT_GRAD;
   ce::Params ps = product_params(h, q, ws, q.sums, T);
   ps.jobs = 0;
+  ps.scale = pack.scale;
   const int b_rows = q.sums.bn / q.sums.cg;
   ce::Job* jx = dx ? &ps.job[ps.jobs++] : nullptr;
   ce::Job* jw = dweight ? &ps.job[ps.jobs++] : nullptr;
@@ -498,6 +502,8 @@ int gemm_ws_linear_ce_backward(gemm_ws_t* h, const uint16_t* x, int64_t ldx,
     sp.cuts = static_cast<int>(q.cuts);
     sp.cut_stride = T * H;
     sp.place = pack.place;
+    sp.grad = pack.grad_out;
+    sp.scale = pack.scale;
     sp.rows = static_cast<int>(T);
     sp.cols = static_cast<int>(H);
     sp.dx = dx;

@@ -3,8 +3,9 @@
 //
 //   z = x * weight^T (T x V);  lse_i = log sum_j exp(z_ij);
 //   loss_i = lse_i - z_i,target(i)
-//   G_ij = g_i * (exp(z_ij - lse_i) - [j == target(i)])
-//   dx = G * weight;  dweight = G^T * x
+//   G_ij = g_i / s * (exp(z_ij - lse_i) - [j == target(i)])
+//   dx = s * G * weight;  dweight = s * G^T * x
+// where s is the largest |g|, or g itself if all tokens have one.
 //
 // Tokens that are not counted (target == ignore) are left out before the
 // first product: a gather packs the counted rows of x, so such a row costs
@@ -20,12 +21,13 @@
 //          of exponentials leave, and the target's logit.
 //   GRAD   the tile is computed again for a piece of the vocabulary and G
 //          leaves in bf16, since the tensor cores multiply 16-bit operands. That
-//          rounds G once, by up to 2^-9 of each value, independently from element
-//          to element. In the norm dx and dweight are then off by 1.9e-3 (4096
-//          tokens x 4096 over 131072), 2.3e-3 (256 x 256 over 1000), 2.6e-3 (few
-//          tokens; 5e-3 in the worst of 8000 random small cases), where their own
-//          rounding to bf16 alone makes 1.7e-3. A second product with what the
-//          rounding leaves would take them to that, for twice the operations.
+//          rounds G once, by up to 2^-8 of each value. It is rounded without s: the
+//          targets' -1 of tokens that the model does not expect, which are most
+//          of dx and dweight, are then exact, where -g, the same for all of them,
+//          would be off by one and the same share (3.9e-3 for the mean of 255
+//          tokens). In the norm dx and dweight are off by 1.6e-3 to 2.1e-3 (1 to 8192
+//          tokens), where their own rounding to bf16 alone makes 1.7e-3. A second product
+//          with what G's rounding leaves would take them to that, for twice the operations.
 //   SUMS   the two products of that piece in one launch, dx's units (fp32,
 //          added to by later pieces) before dweight's (bf16, final). G^T, x
 //          and weight are read as they lie, as MN-major operands, so nothing
@@ -141,7 +143,8 @@ struct Params {
   int64_t part_stride;
   int cut_k;                 // K of one accumulator, a multiple of 128 (the same in both)
   int carry;                 // one row of tiles: a CTA keeps its sums over its tiles
-  const float *lse, *grad;   // [row]: lse, and g
+  const float *lse, *grad;   // [row]: lse, and g / s (0: no gradient)
+  const float* scale;        // SUMS: s
   // LSE of few rows or tiles: x itself is A, so nothing is packed; and with at most
   // JOIN_FEW rows the CTA that ends last joins the sums, so that the pass is one
   // launch. (It is one SM's work: 61 rows so take 10 us longer than with a launch.)
@@ -519,6 +522,16 @@ struct Epilogue {
   }
 };
 
+// Two fp32 values times s, in bf16 (one instruction for both products).
+__device__ __forceinline__ uint32_t scaled_bf16x2(float lo, float hi, float s) {
+  unsigned long long v, f;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(f) : "f"(s));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(f));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+  return pack_bf16x2(lo, hi);
+}
+
 // 64 fp32 values of a row in bf16 to the warp's block.
 template <int CG>
 __device__ __forceinline__ void put_bf16(const Epilogue<CG>& w, const float (&lo)[32],
@@ -658,13 +671,15 @@ __device__ __forceinline__ void epilogue_logits(const Params& p, uint32_t sbase,
 }
 
 // SUMS: dx's tiles leave in fp32 (stored, or added to the pieces before), dweight's
-// in bf16.
+// times s in bf16. (The product with s costs 4 % where the tiles' stores bound the
+// launch, gradients of one token over 131072 x 4096 566 us, and below 1 % from 128 tokens on.)
 template <int CG>
 __device__ __forceinline__ void epilogue_sums(const Params& p, uint32_t sbase, uint8_t* smem,
                                               uint32_t tmem, uint32_t rank, int warp, int count,
                                               const Watchdog& wd) {
   Epilogue<CG> me(sbase, smem, tmem, rank, warp);
   const Walk walk = make_walk<CG>(p, count, blockIdx.x / CG, gridDim.x / CG);
+  const float scale = *p.scale;
   Unit w;
   for (int i = 0; next_unit<CG>(p, walk, i, w); ++i) {
     const Job& job = *w.job;
@@ -685,13 +700,23 @@ __device__ __forceinline__ void epilogue_sums(const Params& p, uint32_t sbase, u
         tmem_wait_ld();
       }
       if (j + 2 >= blocks) me.release();
-      me.reuse();
       if (f32) {
+        me.reuse();
 #pragma unroll
         for (int c = 0; c < 8; ++c)
           *me.piece(c) = make_uint4(a0[4 * c], a0[4 * c + 1], a0[4 * c + 2], a0[4 * c + 3]);
       } else {
-        put_bf16(me, reinterpret_cast<const float(&)[32]>(a0), reinterpret_cast<const float(&)[32]>(a1));
+        // scaled and rounded while the block's last store may still be read
+        uint32_t v[32];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          v[x] = scaled_bf16x2(__uint_as_float(a0[2 * x]), __uint_as_float(a0[2 * x + 1]), scale);
+          v[16 + x] = scaled_bf16x2(__uint_as_float(a1[2 * x]), __uint_as_float(a1[2 * x + 1]), scale);
+        }
+        me.reuse();
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *me.piece(c) = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
       }
       me.store(&job.tmD, w.n0 + j * step, job.d_row0 + part0 + 32 * me.q, w.cut, job.add);
     }
@@ -876,6 +901,7 @@ struct PackParams {
   const float *lse, *grad;    // GRAD: [row] (grad: grad_step 0 has one for all)
   int grad_step;
   float *lse_out, *grad_out;  // GRAD: [packed row]
+  float* scale;               // GRAD: s
 };
 
 constexpr int PACK_THREADS = 256;
@@ -892,9 +918,20 @@ __device__ __forceinline__ int block_sum(int v, int* box) {
   return s;
 }
 
+// The largest over the block, in every thread.
+__device__ __forceinline__ int block_max(int v, int* box) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  if ((threadIdx.x & 31) == 0) box[threadIdx.x >> 5] = v;
+  __syncthreads();
+  int m = box[0];
+  for (int w = 1; w < PACK_THREADS / 32; ++w) m = max(m, box[w]);
+  __syncthreads();
+  return m;
+}
+
 // Block b packs the counted rows of [b * chunk, (b + 1) * chunk). Each block
 // counts all targets itself (8 bytes a row, from L2 after the first block), which
-// saves a scan of its own before it. The rows that follow the last counted
+// saves a scan of its own before it, and all g for s. The rows that follow the last counted
 // one up to a multiple of 128 are zeroed, since dweight's product sums over
 // them; the uncounted rows' blocks do that, and rows that are there only to make up
 // the 128 count as uncounted.
@@ -905,14 +942,22 @@ __global__ void __launch_bounds__(PACK_THREADS) pack_kernel(const __grid_constan
   grid_launch_dependents();
   const int r0 = blockIdx.x * p.chunk, r1 = min(p.padded, r0 + p.chunk);
   int before = 0, all = 0;
+  float top = 0.0f;   // |g| of what has a gradient, at most
 #pragma unroll 4
   for (int r = threadIdx.x; r < p.rows; r += PACK_THREADS) {
-    const int c = p.given.raw(r) != p.given.ignore;
+    const int64_t t = p.given.raw(r);
+    const int c = t != p.given.ignore;
     all += c;
     before += r < r0 ? c : 0;
+    if (p.grad_step && c && p.given.inside(t)) top = fmaxf(top, fabsf(p.grad[r]));
   }
   before = block_sum(before, box);
   all = block_sum(all, box);
+  if (p.scale) {
+    // as integers, which order the same where nothing is negative
+    top = p.grad_step ? __int_as_float(block_max(__float_as_int(top), box)) : *p.grad;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.scale = top;
+  }
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.count = all;
   const int row = r0 + threadIdx.x;
   const bool mine = threadIdx.x < p.chunk && row < r1;
@@ -921,6 +966,7 @@ __global__ void __launch_bounds__(PACK_THREADS) pack_kernel(const __grid_constan
   const unsigned vote = __ballot_sync(0xffffffffu, counted);
   if ((threadIdx.x & 31) == 0) box[threadIdx.x >> 5] = __popc(vote);
   __syncthreads();
+  bool empty = false;   // counted, but without a gradient: its packed row is zeros
   int rank = before + __popc(vote & ((1u << (threadIdx.x & 31)) - 1u));
   for (int w = 0; w < static_cast<int>(threadIdx.x >> 5); ++w) rank += box[w];
   if (mine) {
@@ -930,13 +976,17 @@ __global__ void __launch_bounds__(PACK_THREADS) pack_kernel(const __grid_constan
       p.target_out[rank] = inside ? static_cast<int>(t) : -1;
       if (p.target_logit) p.target_logit[rank] = inside ? 0.0f : __int_as_float(0x7FC00000);
       if (p.lse_out) {
+        const float g = inside ? p.grad[static_cast<int64_t>(row) * p.grad_step] : 0.0f;
         p.lse_out[rank] = p.lse[row];
-        p.grad_out[rank] = inside ? p.grad[static_cast<int64_t>(row) * p.grad_step] : 0.0f;
+        p.grad_out[rank] = g == 0.0f ? 0.0f : g / top;
+        empty = g == 0.0f;
       }
     }
     // the k-th uncounted row zeroes the k-th packed row after the counted ones
     const int behind = all + (row - rank);
-    dst_row[threadIdx.x] = counted ? rank : behind < (all + 127) / 128 * 128 ? -1 - behind : NO_ROW;
+    dst_row[threadIdx.x] = empty     ? -1 - rank
+                           : counted ? rank
+                           : behind < (all + 127) / 128 * 128 ? -1 - behind : NO_ROW;
   }
   __syncthreads();
   const int groups = p.cols / 8;   // cols is a multiple of 8
@@ -1090,6 +1140,7 @@ struct SpreadParams {
   int cuts;
   int64_t cut_stride;
   const int* place;
+  const float *grad, *scale;   // [packed row]: g / s; s
   int rows, cols;
   uint16_t* dx;
   int64_t lddx;
@@ -1097,8 +1148,8 @@ struct SpreadParams {
 
 constexpr int SPREAD_THREADS = 256;
 
-// dx of every row: the cuts' sums of its packed row added in order and rounded
-// once, or zeros. Four columns a thread.
+// dx of every row: the cuts' sums of its packed row added in order, times s, and
+// rounded once, or zeros. Four columns a thread.
 __global__ void __launch_bounds__(SPREAD_THREADS) spread_kernel(const __grid_constant__ SpreadParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
@@ -1109,7 +1160,8 @@ __global__ void __launch_bounds__(SPREAD_THREADS) spread_kernel(const __grid_con
   const int c = static_cast<int>(v - row * quads) * 4;
   const int at = p.place[row];
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (at >= 0) {
+  if (at >= 0 && p.grad[at] != 0.0f) {
+    const float scale = *p.scale;
     const float* src = p.sums + static_cast<int64_t>(at) * p.cols + c;
 #pragma unroll 4
     for (int k = 0; k < p.cuts; ++k) {
@@ -1119,6 +1171,10 @@ __global__ void __launch_bounds__(SPREAD_THREADS) spread_kernel(const __grid_con
       s.z += f.z;
       s.w += f.w;
     }
+    s.x *= scale;
+    s.y *= scale;
+    s.z *= scale;
+    s.w *= scale;
   }
   uint2 out;
   out.x = pack_bf16x2(s.x, s.y);

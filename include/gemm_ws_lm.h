@@ -132,8 +132,9 @@ int gemm_ws_linear_ce(gemm_ws_t* h, const uint16_t* x, int64_t ldx, const uint16
  *  - dx: tokens x hidden bf16, zero for uncounted tokens; dweight: vocab x
  *    hidden bf16; either may be NULL. 16-byte aligned, lddx and lddw multiples
  *    of 8.
- * A piece's gradient of the logits is rounded to bf16; the sums over the
- * vocabulary (dx) and the tokens (dweight) are fp32 and rounded once. */
+ * (softmax - [target]) * grad / max |grad| is rounded to bf16; the sums over the
+ * vocabulary (dx) and the tokens (dweight) are fp32, multiplied by max |grad| and
+ * rounded once. */
 int gemm_ws_linear_ce_backward(gemm_ws_t* h, const uint16_t* x, int64_t ldx,
                                const uint16_t* weight, int64_t ldw, const void* target,
                                int target_bytes, int64_t ignore, const float* lse,
