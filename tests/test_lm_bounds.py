@@ -123,5 +123,22 @@ def test_the_largest_vocabulary(g):
     at = (x.double() * w[t].double()).sum(1)
     assert torch.all((loss - (want - at)).abs() <= 1e-4)
     assert abs(float(mean[0]) - float((want - at).mean())) <= 1e-4
-    del w
+    # the gradients, in 2048 pieces; the last rows of dweight
+    dx, dw = torch.full_like(x, 3.0), torch.full_like(w, 3.0)
+    g.linear_cross_entropy_backward(x, w, t, lse, mean[1:], dx=dx, dweight=dw)
+    want_dx = -w[t].double()
+    for a in range(0, V, step):
+        part = w[a:a + step].double()
+        want_dx += torch.exp(x.double() @ part.T - want[:, None]) @ part
+    want_dx /= T
+    assert float((dx.double() - want_dx).norm()) <= 4e-3 * float(want_dx.norm())
+    for a in (0, V // 2 - 500, V - 1000):
+        rows = torch.arange(a, a + 1000, device="cuda")
+        p = torch.exp(x.double() @ w[a:a + 1000].double().T - want[:, None])
+        p -= (t[:, None] == rows).double()
+        tail = p.T @ x.double() / T
+        assert float((dw[a:a + 1000].double() - tail).norm()) <= 4e-3 * float(tail.norm())
+        rest = ~torch.isin(rows, t)
+        assert float((dw[a:a + 1000][rest].double() - tail[rest]).norm()) <= 4e-3 * float(tail[rest].norm())
+    del w, dw
     torch.cuda.empty_cache()
