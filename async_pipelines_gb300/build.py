@@ -18,10 +18,12 @@ LIB = os.path.join(PKG, "libgemm_ws.so")
 # Debug build: the same sources with the test hooks of include/gemm_ws_debug.h
 # (fault injection for the watchdog, per-tile timestamps). Tests only.
 DEBUG_LIB = os.path.join(PKG, "libgemm_ws_debug.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("gemm_ws.cu", "lm_norm.cu", "lm_loss.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in (
+    "gemm_ws.cu", "lm_norm.cu", "lm_loss.cu", "lm_block.cu", "lm_int8.cu", "lm_logits.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in (
-    "ptx.cuh", "watchdog.cuh", "handle.cuh", "gemm_ws_kernel.cuh", "lm_norm_kernel.cuh",
-    "lm_loss_kernel.cuh")] + [
+    "ptx.cuh", "watchdog.cuh", "handle.cuh", "gemm_ws_kernel.cuh", "lm_host.cuh", "lm_rows.cuh",
+    "lm_norm_kernel.cuh", "lm_loss_kernel.cuh", "lm_block_kernel.cuh", "lm_int8_kernel.cuh",
+    "lm_logits_kernel.cuh")] + [
     os.path.join(INCLUDE, f) for f in ("gemm_ws.h", "gemm_ws_debug.h", "gemm_ws_lm.h")]
 
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"

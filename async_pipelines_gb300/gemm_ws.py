@@ -229,6 +229,7 @@ class GemmWS(_lm.LmOps):
     def __init__(self, device: int = 0, lib=None):
         self.device = int(device)
         self._ce_need = {}   # workspace bytes of the cross entropy, by sizes
+        self._int8_need = {}   # and of the 8-bit product
         self.lib = lib or load_library()
         h = ctypes.c_void_p()
         rc = self.lib.gemm_ws_create(ctypes.byref(h), self.device)

@@ -11,6 +11,13 @@
  *   gemm_ws_linear_ce               softmax cross entropy of x * weight^T over a
  *                                   vocabulary, the logits never held
  *   gemm_ws_linear_ce_backward      its gradients
+ *   gemm_ws_block_norm              the norms after and before a block, with its gate
+ *                                   and the scaled residual, also in 8 bits with scales
+ *   gemm_ws_block_norm_backward     its gradients
+ *   gemm_ws_quantize_rows           rows to 8-bit integers with a scale for each
+ *   gemm_ws_int8_matmul             the product of 8-bit integers with a scale for each
+ *                                   token and each channel
+ *   gemm_ws_adjust_logits           penalties for repeated tokens, biases, masks
  *
  * Everything that gemm_ws.h says of handles, threads, streams, ownership and
  * errors holds here: calls are asynchronous on `stream`, allocate nothing,
@@ -45,7 +52,8 @@ typedef enum gemm_ws_dtype {
 typedef enum gemm_ws_norm_output {
   GEMM_WS_NORM_SAME = 0,        /* y has the type of x */
   GEMM_WS_NORM_E4M3_ROW = 1,    /* y is e4m3, one fp32 scale a row */
-  GEMM_WS_NORM_E4M3_GROUP = 2   /* y is e4m3, one fp32 scale for each 128 columns */
+  GEMM_WS_NORM_E4M3_GROUP = 2,  /* y is e4m3, one fp32 scale for each 128 columns */
+  GEMM_WS_NORM_INT8_ROW = 3     /* gemm_ws_block_norm: y is 8-bit integers, one fp32 scale a row */
 } gemm_ws_norm_output;
 
 /* Dropout (here and in the norm). `rng` is a device pointer to two uint64:
@@ -148,6 +156,104 @@ int gemm_ws_linear_ce_backward(gemm_ws_t* h, const uint16_t* x, int64_t ldx,
  * sizes that they refuse. Host arithmetic only. */
 int64_t gemm_ws_linear_ce_workspace(gemm_ws_t* h, int64_t tokens, int64_t hidden, int64_t vocab,
                                     int backward);
+
+/* What lies between one block of a model and the next:
+ *   n = x / sqrt(mean(x^2) + eps);  b = post_weight * n
+ *   hidden = alpha * residual + gate * b
+ *   y = weight * hidden / sqrt(mean(hidden^2) + eps)
+ * In 32 bits from the inputs to each output's one rounding: y is computed from the
+ * unrounded hidden.
+ *  - x (the block's output), residual, hidden (NULL: not written), y: rows x cols;
+ *    post_weight (NULL: no norm after the block, b = x), weight: cols; all of
+ *    `dtype`, but y bytes where `output` says so. hidden may be x or
+ *    residual, and y may be x.
+ *  - gate: NULL (1), cols with ldg 0 (one for each channel), or rows x cols.
+ *  - output: a gemm_ws_norm_output, and scales, as in gemm_ws_add_rms_norm. With
+ *    GEMM_WS_NORM_INT8_ROW the scale of a row is max |y| / 127, at least 2^-126, and y
+ *    holds the integers nearest to the fp32 quotients y / scale (halves to even). A row of y with an
+ *    infinity or a NaN has scale NaN and zeros.
+ *  - post_rstd (only with post_weight), rstd: rows fp32, 1 / sqrt(mean + eps) of the
+ *    two norms, for the backward pass; or NULL.
+ *  - alpha: finite. 1 <= cols <= 16384; 0 <= rows < 2^31.
+ * Launches one kernel. */
+int gemm_ws_block_norm(gemm_ws_t* h, int dtype, const void* x, int64_t ldx, const void* residual,
+                       int64_t ldr, const void* gate, int64_t ldg, const void* post_weight,
+                       const void* weight, void* hidden, int64_t ldh, void* y, int64_t ldy,
+                       int output, float* scales, float* post_rstd, float* rstd, int64_t rows,
+                       int64_t cols, float alpha, float eps, void* stream);
+
+/* The gradients of gemm_ws_block_norm with output GEMM_WS_NORM_SAME.
+ *  - dy: of y; dhidden: what reaches hidden from its other uses (NULL: zero); x, gate,
+ *    post_weight, weight, alpha: as given to the forward call; hidden, post_rstd (with
+ *    post_weight) and rstd: what it wrote.
+ *  - dx: of x; dresidual: of residual (NULL: not written). Each may be dy or dhidden.
+ *  - dgate: of gate, laid out like it (lddg elements between rows; not read for a gate of
+ *    each channel); dpost_weight, dweight: cols. Sums over rows are in 32 bits and rounded once;
+ *    each may be NULL, and with rows == 0 they are zero.
+ * Launches one kernel, two with a sum over rows. */
+int gemm_ws_block_norm_backward(gemm_ws_t* h, int dtype, const void* dy, int64_t lddy,
+                                const void* dhidden, int64_t lddh, const void* x, int64_t ldx,
+                                const void* hidden, int64_t ldh, const void* gate, int64_t ldg,
+                                const void* post_weight, const void* weight,
+                                const float* post_rstd, const float* rstd, void* dx, int64_t lddx,
+                                void* dresidual, int64_t lddr, void* dgate, int64_t lddg,
+                                void* dpost_weight, void* dweight, int64_t rows, int64_t cols,
+                                float alpha, void* stream);
+
+/* Rows in 8-bit integers: scales[r] = max_c |x[r][c]| / 127, at least 2^-126, and y the
+ * integers nearest to the fp32 quotients x / scale (halves to even), -127 to 127. A row with an infinity or
+ * a NaN has scale NaN and zeros.
+ *  - x: rows x cols of `dtype`; y: rows x cols; scales: rows.
+ *  - 1 <= cols <= 32768; 0 <= rows < 2^31. */
+int gemm_ws_quantize_rows(gemm_ws_t* h, int dtype, const void* x, int64_t ldx, int8_t* y,
+                          int64_t ldy, float* scales, int64_t rows, int64_t cols, void* stream);
+
+/* d[m][n] = (sum_k a[m][k] * w[n][k]) * a_scales[m] * w_scales[n] + bias[n]. The sums are
+ * exact in 32-bit integers; what follows is fp32, rounded once to `dtype`.
+ *  - a: tokens x k, w: channels x k, 8-bit integers, -128 included; a_scales: tokens,
+ *    w_scales: channels, bias: channels (NULL: none), fp32; d: tokens x channels of `dtype`.
+ *  - w 16-byte aligned, ldw a multiple of 16 (a, d and k are free).
+ *  - workspace: gemm_ws_int8_matmul_workspace bytes on the device, 256-byte aligned,
+ *    for this call alone (its contents mean nothing before or after); NULL where it is 0.
+ *  - 0 <= tokens, 1 <= channels, each at most 2^31 - 4096; 1 <= k < 2^17;
+ *    tokens * k, channels * k and tokens * channels at most 2^40. */
+int gemm_ws_int8_matmul(gemm_ws_t* h, const int8_t* a, int64_t lda, const float* a_scales,
+                        const int8_t* w, int64_t ldw, const float* w_scales, const float* bias,
+                        void* d, int64_t ldd, int dtype, int64_t tokens, int64_t channels,
+                        int64_t k, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of gemm_ws_int8_matmul for these sizes on this handle; negative (a
+ * gemm_ws_status, negated) for sizes that it refuses. Host arithmetic only. */
+int64_t gemm_ws_int8_matmul_workspace(gemm_ws_t* h, int64_t tokens, int64_t channels, int64_t k);
+
+/* Logits as a sampler takes them. For token v of a row, with c = how often it stands in
+ * the generated part of the row's history:
+ *   z = logits[v]
+ *   z = z > 0 ? z / repetition : z * repetition     if v stands in the history at all
+ *   z = z - (frequency * c + presence)               if c > 0
+ *   z = z + the sum of v's biases
+ *   z = -inf                                         if v is not allowed
+ * In fp32, rounded once.
+ *  - logits: rows x vocab of `dtype`; out: rows x vocab of `dtype` or fp32
+ *    (out_dtype); out may be the logits.
+ *  - tokens: rows x history, int64 (token_bytes 8) or int32 (4), ldt elements between
+ *    rows; the first lengths[r] (NULL: history; taken as at least 0 and at most history) of
+ *    row r count, of which the first prompt_lengths[r] (NULL: 0) are the prompt and the rest
+ *    generated. A token outside [0, vocab) counts for nothing. history 0: no history.
+ *  - repetition (not 0), frequency, presence: rows fp32, or NULL: 1, 0, 0.
+ *  - bias_tokens (int64 or int32), bias_values (fp32): rows x biases, at most 1024; a
+ *    token outside [0, vocab) is left out, one given twice gets both, added in their order.
+ *  - allowed: rows x ceil(vocab / 32) words, lda words between rows; token v is allowed iff
+ *    bit v % 32 of word v / 32 is set. NULL: all are. A row may allow nothing.
+ *  - 0 <= rows; 1 <= vocab < 2^31 - 4096; 0 <= history < 2^31. */
+int gemm_ws_adjust_logits(gemm_ws_t* h, int dtype, const void* logits, int64_t ldl, int out_dtype,
+                          void* out, int64_t ldo, const void* tokens, int token_bytes, int64_t ldt,
+                          int64_t history, const int32_t* lengths, const int32_t* prompt_lengths,
+                          const float* repetition, const float* frequency, const float* presence,
+                          const void* bias_tokens, int bias_token_bytes, int64_t ldb,
+                          const float* bias_values, int64_t ldv, int64_t biases,
+                          const uint32_t* allowed, int64_t lda, int64_t rows, int64_t vocab,
+                          void* stream);
 
 #ifdef __cplusplus
 }
