@@ -24,8 +24,6 @@
 
 namespace {
 
-constexpr int kWorkWords = 4;   // counter [0], status [1], consumers done [2], blocks done [3]
-
 // Words of a handle's work area: kWorkWords, then the in-kernel fix-up's
 // arrival counts and written flags (one per epilogue warp of each CTA).
 size_t work_words(int num_sms) {

@@ -53,6 +53,9 @@ struct gemm_ws {
 
 namespace {
 
+// The work area's counter [0], status [1], consumers done [2], blocks done [3]; the words for
+// arrivals follow.
+[[maybe_unused]] constexpr int kWorkWords = 4;
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxElems = int64_t{1} << 40;
 [[maybe_unused]] constexpr size_t kDefaultSmem = 48 * 1024;   // dynamic shared memory a kernel has unasked

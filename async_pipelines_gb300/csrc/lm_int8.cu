@@ -37,6 +37,93 @@ int launch_dot(gemm_ws* h, i8::DotParams& q, cudaStream_t s) {
   return e == cudaSuccess ? GEMM_WS_OK : cuda_fail(h, e);
 }
 
+// Up to this many tokens the integer dot products of the CUDA cores keep up with w's bytes.
+constexpr int64_t kDotTokens = 8;
+
+struct Plan {
+  bool dot;
+  int bn, splits;
+  int64_t tiles_m, tiles_n, stages, clusters;
+  int64_t chunks;    // of 16 in a row of the tokens in fp16
+  int64_t bytes;     // of workspace
+};
+
+// Tiles as wide as leave the least work to the slowest pair: rounds times tokens, and 24 tokens' worth of
+// time a round for what does not grow with them. K is cut where the tiles do not reach all pairs.
+Plan make_plan(const gemm_ws* h, int64_t tokens, int64_t channels, int64_t k) {
+  Plan q;
+  std::memset(&q, 0, sizeof q);
+  q.dot = tokens <= kDotTokens || h->max_pair_clusters < 1;
+  if (q.dot) return q;
+  q.stages = ceil_div(k, i8::BK);
+  q.tiles_n = ceil_div(channels, 2 * i8::BM);
+  const int64_t pairs = h->max_pair_clusters;
+  int64_t least = 0;
+  for (int bn = i8::BN_MAX; bn >= 32; bn -= 32) {
+    const int64_t cost = ceil_div(ceil_div(tokens, bn) * q.tiles_n, pairs) * (bn + 24);
+    if (q.bn == 0 || cost < least) {
+      least = cost;
+      q.bn = bn;
+    }
+  }
+  q.tiles_m = ceil_div(tokens, q.bn);
+  const int64_t tiles = q.tiles_m * q.tiles_n;
+  int64_t splits = pairs / tiles;
+  if (splits > q.stages / 2) splits = q.stages / 2;   // at least 256 of K
+  q.splits = splits > 1 ? static_cast<int>(splits) : 1;
+  q.clusters = tiles * q.splits < pairs ? tiles * q.splits : pairs;
+  q.chunks = ceil_div(k, 16);
+  q.bytes = ceil_div(tokens * q.chunks * 32, 256) * 256;
+  return q;
+}
+
+bool encode(gemm_ws* h, CUtensorMap* m, const void* ptr, bool half, int64_t inner, int64_t rows, int64_t ld,
+            int x, int y) {
+  const int64_t size = half ? 2 : 1;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows), 1};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * size), static_cast<cuuint64_t>(ld * rows * size)};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(x), static_cast<cuuint32_t>(y), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = h->encode(
+      m, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr),
+      dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) h->last_cuda_error = static_cast<int>(r);
+  return r == CUDA_SUCCESS;
+}
+
+// Whether the product kernel has the registers at launch that its warpgroups share out: with fewer
+// they would wait for each other forever. (A property of the built kernel.)
+bool registers_as_planned() {
+  static bool seen = false;
+  if (seen) return true;
+  cudaFuncAttributes a;
+  if (cudaFuncGetAttributes(&a, i8::product_kernel) != cudaSuccess) return false;
+  seen = a.numRegs == i8::REGS_LAUNCH;
+  return seen;
+}
+
+int launch_product(gemm_ws* h, const Plan& q, const i8::Params& p, cudaStream_t s) {
+  if (!registers_as_planned()) return GEMM_WS_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * q.clusters), 1, 1);
+  cfg.blockDim = dim3(i8::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = i8::SMEM_BYTES;
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = h->pdl ? 2 : 1;
+  cudaError_t e = allow_smem(h, reinterpret_cast<const void*>(i8::product_kernel), i8::SMEM_BYTES);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, i8::product_kernel, p);
+  return e == cudaSuccess ? GEMM_WS_OK : cuda_fail(h, e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -45,7 +132,7 @@ int64_t gemm_ws_int8_matmul_workspace(gemm_ws_t* h, int64_t tokens, int64_t chan
   if (!h || tokens < 0 || channels < 1 || k < 1 || tokens > kMaxExtent || channels > kMaxExtent ||
       k > kMaxK || tokens * k > kMaxElems || channels * k > kMaxElems || tokens * channels > kMaxElems)
     return -GEMM_WS_ERR_INVALID_ARG;
-  return 0;
+  return tokens == 0 ? 0 : make_plan(h, tokens, channels, k).bytes;
 }
 
 int gemm_ws_int8_matmul(gemm_ws_t* h, const int8_t* a, int64_t lda, const float* a_scales,
@@ -57,7 +144,7 @@ int gemm_ws_int8_matmul(gemm_ws_t* h, const int8_t* a, int64_t lda, const float*
   if (tokens == 0) return GEMM_WS_OK;
   const Mat ma{a, lda, 1}, mw{w, ldw, 1}, md{d, ldd, element_size(dtype)};
   if (!a || !a_scales || !w || !w_scales || !d || bad_matrix(ma, k) || bad_matrix(mw, k) ||
-      bad_matrix(md, channels) || (need > 0 && (!workspace || workspace_bytes < need)))
+      bad_matrix(md, channels) || ldw > kMaxElems / channels || (need > 0 && (!workspace || workspace_bytes < need)))
     return GEMM_WS_ERR_INVALID_ARG;
   for (const float* f : {a_scales, w_scales, bias})
     if (reinterpret_cast<uintptr_t>(f) % 4 != 0) return GEMM_WS_ERR_INVALID_ARG;
@@ -76,21 +163,62 @@ int gemm_ws_int8_matmul(gemm_ws_t* h, const int8_t* a, int64_t lda, const float*
   out.a_scales = a_scales;
   out.w_scales = w_scales;
   out.bias = bias;
-  i8::DotParams q;
+  const bool wide = aligned16(a) && (tokens == 1 || lda % 16 == 0);
+  const Plan plan = make_plan(h, tokens, channels, k);
+  if (plan.dot) {
+    i8::DotParams q;
+    std::memset(&q, 0, sizeof q);
+    q.a = a;
+    q.w = w;
+    q.lda = lda;
+    q.ldw = ldw;
+    q.tokens = static_cast<int>(tokens);
+    q.channels = static_cast<int>(channels);
+    q.k = static_cast<int>(k);
+    q.wide = wide;
+    q.out = out;
+    if (tokens <= 1) return launch_dot<1>(h, q, s);
+    if (tokens <= 2) return launch_dot<2>(h, q, s);
+    if (tokens <= 4) return launch_dot<4>(h, q, s);
+    return launch_dot<8>(h, q, s);
+  }
+  i8::ExpandParams e;
+  std::memset(&e, 0, sizeof e);
+  e.a = a;
+  e.lda = lda;
+  e.tokens = static_cast<int>(tokens);
+  e.k = static_cast<int>(k);
+  e.wide = wide;
+  e.chunks = static_cast<int>(plan.chunks);
+  e.out = static_cast<uint16_t*>(workspace);
+  i8::Params q;
   std::memset(&q, 0, sizeof q);
-  q.a = a;
-  q.w = w;
-  q.lda = lda;
-  q.ldw = ldw;
+  const int64_t pitch = 16 * plan.chunks;
+  if (!encode(h, &q.tmW, w, false, k, channels, channels > 1 ? ldw : ceil_div(k, 16) * 16, i8::BK, i8::BM) ||
+      !encode(h, &q.tmA, workspace, true, pitch, tokens, pitch, i8::HALF_K, plan.bn / 2))
+    return GEMM_WS_ERR_CUDA;
+  const int rc = launch(h, i8::expand_kernel, ceil_div(tokens * plan.chunks, i8::EXPAND_THREADS),
+                        i8::EXPAND_THREADS, 0, s, e);
+  if (rc != GEMM_WS_OK) return rc;
   q.tokens = static_cast<int>(tokens);
   q.channels = static_cast<int>(channels);
-  q.k = static_cast<int>(k);
-  q.wide = aligned16(a) && (tokens == 1 || lda % 16 == 0);
+  q.stages = static_cast<int>(plan.stages);
+  q.bn = plan.bn;
+  q.a_stages = i8::W_BUFS + 3;   // w's ring takes what the tokens' leaves; theirs is freed later
+  q.w_stages = static_cast<int>((i8::RING_ROOM - q.a_stages * i8::a_stage(q.bn)) / i8::W_STAGE);
+  if (q.w_stages > i8::MAX_STAGES) q.w_stages = i8::MAX_STAGES;
+  q.tiles_m = static_cast<int>(plan.tiles_m);
+  q.tiles_n = static_cast<int>(plan.tiles_n);
+  q.splits = plan.splits;
+  q.partial = reinterpret_cast<int*>(h->partial);
+  q.arrived = h->work + kWorkWords;
   q.out = out;
-  if (tokens <= 1) return launch_dot<1>(h, q, s);
-  if (tokens <= 2) return launch_dot<2>(h, q, s);
-  if (tokens <= 4) return launch_dot<4>(h, q, s);
-  return launch_dot<8>(h, q, s);
+  q.status = h->work + 1;
+  q.timeout_ns = h->timeout_ns;
+#ifdef GEMM_WS_DEBUG
+  q.debug_fault = h->debug_fault;
+#endif
+  return launch_product(h, plan, q, s);
 }
 
 }  // extern "C"

@@ -108,5 +108,517 @@ __global__ void __launch_bounds__(DOT_THREADS) dot_kernel(const __grid_constant_
   put(p.out, m, n, sum, p.out.a_scales[m], p.out.w_scales[n], p.out.bias ? p.out.bias[n] : 0.0f);
 }
 
+// ------------------------------------------------------------ tensor cores
+
+// This chip's tensor cores multiply 16-bit floats several times as fast as 8-bit integers, and an
+// 8-bit integer is exact in fp16. So is a product of two in the fp32 accumulator, and the sum of 1024
+// of them (2^10 * 2^14 = 2^24): the accumulator is handed over every 1024 of K, and the epilogue
+// adds what it held in 32-bit integers.
+//
+// w's rows are A of the product, from tensor memory: converted on their way there from
+// shared memory by warps of their own, they cost the shared memory 2 bytes of traffic each (in and
+// out) instead of the 5 that a copy in fp16 there would (1 in, 1 out, 2 back and 2 out to the
+// tensor cores, for the half that a CTA of a pair holds). a's rows, the tokens, are B: a small kernel
+// writes them in fp16 first, once for all channels.
+//
+// A pair of CTAs has a tile of 256 channels x bn tokens, each its 128 channels as
+// TMEM lanes. Tensor memory: two accumulators of up to 160 columns, and three buffers of w, 128 x 128
+// each, in the 192 columns after them.
+//
+// One warp issues all MMAs, and what it does beside that has to fit into their time: for 128 of K it
+// polls both operands at once and commits once, to w's buffer. That the tokens' stage of the same step
+// is free again a warp of its own tells on, when it sees w's buffer free.
+
+constexpr int BM = 128;              // channels of a CTA's tile
+constexpr int BN_MAX = 160;          // tokens of a tile, at most
+constexpr int BK = 128;              // K of a stage: one 128-byte swizzle row of 8-bit integers
+constexpr int HALF_K = 64;           // of a stage: one 128-byte swizzle row of fp16
+constexpr int UMMA_K = 16;
+constexpr int ACC_BUFS = 2, W_BUFS = 3;
+constexpr int W_COLS = BK / 2;       // TMEM columns of a buffer of w
+constexpr int TMEM_W = ACC_BUFS * BN_MAX, TMEM_COLS = 512;
+static_assert(TMEM_W + W_BUFS * W_COLS <= TMEM_COLS, "tensor memory");
+constexpr int CUT_STAGES = 1024 / BK;   // stages of one accumulator
+// Warpgroups: producers, the MMA warp and the teller; two that convert; two of the epilogue.
+constexpr int WARP_W = 0, WARP_MMA = 1, WARP_A = 2, WARP_TELL = 3, WARP_CONV0 = 4, CONV_WARPS = 8, WARP_EPI0 = WARP_CONV0 + CONV_WARPS,
+              EPI_WARPS = 8;
+constexpr int THREADS = (WARP_EPI0 + EPI_WARPS) * 32;
+// Registers a thread at launch, and after the warpgroups have shared them out: the epilogue holds 80 sums.
+constexpr int REGS_LAUNCH = 96, REGS_FEW = 72, REGS_EPI = 128;
+static_assert(WARP_EPI0 * REGS_FEW + EPI_WARPS * REGS_EPI <= THREADS / 32 * REGS_LAUNCH, "registers of a block");
+constexpr int MAX_STAGES = 12;
+constexpr uint32_t W_STAGE = BM * BK;                  // 16 KB
+constexpr uint32_t RING_ROOM = 224 * 1024;
+constexpr int BAR_W_FULL = 0, BAR_W_EMPTY = BAR_W_FULL + MAX_STAGES, BAR_A_FULL = BAR_W_EMPTY + MAX_STAGES,
+              BAR_A_EMPTY = BAR_A_FULL + MAX_STAGES, BAR_T_FULL = BAR_A_EMPTY + MAX_STAGES,
+              BAR_T_EMPTY = BAR_T_FULL + W_BUFS, BAR_ACC_FULL = BAR_T_EMPTY + W_BUFS,
+              BAR_ACC_EMPTY = BAR_ACC_FULL + ACC_BUFS, BAR_DRAIN = BAR_ACC_EMPTY + ACC_BUFS,
+              NUM_BARS = BAR_DRAIN + 1;
+constexpr uint32_t OFF_BAR = RING_ROOM;
+constexpr uint32_t OFF_TMEM = OFF_BAR + NUM_BARS * 8;
+constexpr uint32_t OFF_ABORT = OFF_TMEM + 4;
+constexpr uint32_t SMEM_BYTES = OFF_ABORT + 4 + 1024;   // + slack to align the base
+static_assert(SMEM_BYTES <= 232448, "exceeds the 227 KiB per-CTA shared memory");
+
+__host__ __device__ constexpr uint32_t a_stage(int bn) { return static_cast<uint32_t>(bn / 2) * BK * 2; }
+
+struct Params {
+  CUtensorMap tmW, tmA;
+  int tokens, channels, stages;   // stages of K
+  int bn;                         // tokens of a tile, a multiple of 32
+  int w_stages, a_stages;         // of the two rings in shared memory
+  int tiles_m, tiles_n;           // tiles of tokens, of channels
+  int splits;                     // cuts of K; more than one only where all units run at once
+  int* partial;                   // a CTA's sums of its cut: [column][channel]
+  uint32_t* arrived;              // [tile][CTA of the pair][epilogue warp]: zero at launch, left zero
+  Output out;
+  uint32_t* status;
+  unsigned long long timeout_ns;
+#ifdef GEMM_WS_DEBUG
+  int debug_fault;                // 3: w's producer brings nothing
+#endif
+};
+
+// A unit of work: a tile, or a cut of its K.
+struct Unit {
+  int n0, m0;      // first channel of the pair, first token
+  int tile, cut;
+  int s0, s1;      // stages of K
+};
+
+constexpr int GROUP_N = 8;   // tiles walk 8 tiles of channels down, then step on in the tokens (L2 reuse)
+
+__device__ __forceinline__ bool unit_of(const Params& p, int u, Unit& w) {
+  const int tiles = p.tiles_m * p.tiles_n;
+  if (u >= tiles * p.splits) return false;
+  const int t = p.splits > 1 ? u / p.splits : u;
+  w.tile = t;
+  w.cut = u - t * p.splits;
+  w.s0 = static_cast<int>(static_cast<int64_t>(w.cut) * p.stages / p.splits);
+  w.s1 = static_cast<int>(static_cast<int64_t>(w.cut + 1) * p.stages / p.splits);
+  const int group = t / (GROUP_N * p.tiles_m), first = group * GROUP_N;
+  const int r = t - group * GROUP_N * p.tiles_m;
+  const int high = min(GROUP_N, p.tiles_n - first);
+  w.m0 = r / high * p.bn;
+  w.n0 = (first + r % high) * 2 * BM;
+  return true;
+}
+
+// Four 8-bit integers in fp16, in the order 0 2 1 3: a byte's offset value b + 128 under the
+// exponent of 1024 is 1152 + b, and subtracting 1152 is exact. Both operands are laid out in this
+// order of K, which a sum does not see.
+__device__ __forceinline__ uint2 to_fp16(uint32_t w) {
+  const uint32_t even = (w & 0x00FF00FFu) ^ 0x64806480u, odd = (w >> 8 & 0x00FF00FFu) ^ 0x64806480u;
+  const uint32_t shift = 0x64806480u;   // 1152, 1152
+  const __half2 s = *reinterpret_cast<const __half2*>(&shift);
+  const __half2 e = __hsub2(*reinterpret_cast<const __half2*>(&even), s);
+  const __half2 o = __hsub2(*reinterpret_cast<const __half2*>(&odd), s);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&e), *reinterpret_cast<const uint32_t*>(&o));
+}
+
+__device__ __forceinline__ void produce_w(const Params& p, uint32_t sbase, uint32_t rank, const Watchdog& wd) {
+  auto full = [&](uint32_t s) { return sbase + OFF_BAR + 8 * (BAR_W_FULL + s); };
+  auto empty = [&](uint32_t s) { return sbase + OFF_BAR + 8 * (BAR_W_EMPTY + s); };
+  const uint32_t stages = p.w_stages;
+  uint32_t s = 0, ph = 0, g = 0;
+  bool ok = true;
+  Unit w;
+#ifdef GEMM_WS_DEBUG
+  if (p.debug_fault == 3) return;   // injected fault: no stage ever fills
+#endif
+  for (int u = blockIdx.x / 2; ok && unit_of(p, u, w); u += gridDim.x / 2)
+    for (int st = w.s0; st < w.s1; ++st) {
+      if (!wait_spin<false>(empty(s), ph ^ 1, wd)) {
+        ok = false;
+        break;
+      }
+      mbar_arrive_expect_tx(full(s), W_STAGE);
+      tma_load_3d(sbase + s * W_STAGE, &p.tmW, full(s), st * BK, w.n0 + static_cast<int>(rank) * BM, 0);
+      ++g;
+      if (++s == stages) {
+        s = 0;
+        ph ^= 1;
+      }
+    }
+  // Abort: the copies of the stages armed last land before the CTA goes on.
+  if (!ok)
+    for (uint32_t j = g > stages ? g - stages : 0; j < g; ++j) wait_drain(full(j % stages), (j / stages) & 1);
+}
+
+__device__ __forceinline__ void produce_a(const Params& p, uint32_t sbase, uint32_t rank, const Watchdog& wd) {
+  auto full = [&](uint32_t s) { return sbase + OFF_BAR + 8 * (BAR_A_FULL + s); };
+  auto empty = [&](uint32_t s) { return sbase + OFF_BAR + 8 * (BAR_A_EMPTY + s); };
+  const uint32_t stages = p.a_stages, bytes = a_stage(p.bn), ring = sbase + p.w_stages * W_STAGE;
+  const bool leader = rank == 0;   // arms full[s] for the pair
+  uint32_t s = 0, ph = 0, g = 0;
+  bool ok = true;
+  Unit w;
+  for (int u = blockIdx.x / 2; ok && unit_of(p, u, w); u += gridDim.x / 2)
+    for (int st = w.s0; st < w.s1; ++st) {
+      if (!wait_spin<false>(empty(s), ph ^ 1, wd)) {
+        ok = false;
+        break;
+      }
+      if (leader) mbar_arrive_expect_tx(full(s), 2 * bytes);
+      const uint32_t bar = mapa_shared(full(s), 0u), dst = ring + s * bytes;
+      const int row = w.m0 + static_cast<int>(rank) * (p.bn / 2);
+      tma_load_3d_pair(dst, &p.tmA, bar, st * BK, row, 0);
+      tma_load_3d_pair(dst + bytes / 2, &p.tmA, bar, st * BK + HALF_K, row, 0);
+      ++g;
+      if (++s == stages) {
+        s = 0;
+        ph ^= 1;
+      }
+    }
+  if (!ok && leader) {
+    for (uint32_t j = g > stages ? g - stages : 0; j < g; ++j) wait_drain(full(j % stages), (j / stages) & 1);
+  } else if (!ok) {
+    // Copies into a stage that the leader never armed have no barrier: give
+    // them 100 us (they take a few).
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 100000ull) __nanosleep(1000);
+  }
+}
+
+// A warp's 32 channels of every other stage, from shared memory to tensor memory. The two
+// warpgroups take the stages in turn: what a stage costs a warp besides its conversions (the waits and
+// arrivals) so has the time of two.
+__device__ __forceinline__ void convert(const Params& p, uint32_t sbase, const uint8_t* smem, uint32_t tmem,
+                                        int warp, const Watchdog& wd) {
+  auto bar = [&](int i) { return sbase + OFF_BAR + 8 * i; };
+  const int lane = threadIdx.x & 31, row = 32 * (warp & 3) + lane;
+  const uint32_t group = (warp - WARP_CONV0) / 4;
+  const uint32_t mine = tmem + TMEM_W + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+  const uint32_t t_full = mapa_shared(bar(BAR_T_FULL), 0u);   // the leader's
+  const uint32_t w_stages = p.w_stages;
+  uint32_t s = 0, ph = 0, t = 0, tph = 0, turn = 0;
+  Unit w;
+  for (int u = blockIdx.x / 2; unit_of(p, u, w); u += gridDim.x / 2)
+    for (int st = w.s0; st < w.s1; ++st, turn ^= 1) {
+      if (turn == group) {
+        if (!warp_wait_cta(bar(BAR_W_FULL + s), ph, wd)) return;
+        const uint8_t* from = smem + s * W_STAGE + row * BK;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint4 raw[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)   // the TMA's 128-byte swizzle
+            raw[c] = *reinterpret_cast<const uint4*>(from + (((4 * half + c) ^ (row & 7)) << 4));
+          uint32_t v[32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t x[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint2 two = to_fp16(x[i]);
+              v[8 * c + 2 * i] = two.x;
+              v[8 * c + 2 * i + 1] = two.y;
+            }
+          }
+          if (half == 0) {
+            if (!warp_wait_cta(bar(BAR_T_EMPTY + t), tph ^ 1, wd)) return;
+            tc_fence_after_sync();
+          } else {
+            __syncwarp();   // the stage has been read
+            if (lane == 0) mbar_arrive(bar(BAR_W_EMPTY + s));
+          }
+          tmem_st_32x32b_x32(mine + t * W_COLS + half * (W_COLS / 2), v);
+        }
+        tmem_wait_st();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(t_full + 8 * t);
+      }
+      if (++t == W_BUFS) {
+        t = 0;
+        tph ^= 1;
+      }
+      if (++s == w_stages) {
+        s = 0;
+        ph ^= 1;
+      }
+    }
+}
+
+// Frees the tokens' stages: the MMAs that have read w's buffer of a step have read the step's tokens.
+__device__ __forceinline__ void tell(const Params& p, uint32_t sbase, const Watchdog& wd) {
+  uint32_t s = 0, t = 0, tph = 0;
+  Unit w;
+  for (int u = blockIdx.x / 2; unit_of(p, u, w); u += gridDim.x / 2)
+    for (int st = w.s0; st < w.s1; ++st) {
+      if (!warp_wait_cta(sbase + OFF_BAR + 8 * (BAR_T_EMPTY + t), tph, wd)) return;
+      if ((threadIdx.x & 31) == 0) mbar_arrive(sbase + OFF_BAR + 8 * (BAR_A_EMPTY + s));
+      if (++t == W_BUFS) {
+        t = 0;
+        tph ^= 1;
+      }
+      if (++s == static_cast<uint32_t>(p.a_stages)) s = 0;
+    }
+}
+
+// The whole warp walks, so that addresses and descriptors stay in uniform registers; one lane waits and
+// issues. Once a wait has given up, the rest of the walk does nothing.
+__device__ __forceinline__ void issue(const Params& p, uint32_t sbase, uint32_t tmem, const Watchdog& wd) {
+  auto bar = [&](int i) { return sbase + OFF_BAR + 8 * i; };
+  constexpr uint16_t BOTH = 0x3;
+  const uint32_t bytes = a_stage(p.bn), ring = sbase + p.w_stages * W_STAGE;
+  const uint32_t idesc = idesc_f16_f32(2 * BM, p.bn);
+  const bool mine = elect_one();
+  uint32_t s = 0, ph = 0, t = 0, tph = 0, handed = 0;
+  bool ok = true, issued = false;
+  Unit w;
+  for (int u = blockIdx.x / 2; unit_of(p, u, w); u += gridDim.x / 2)
+    for (int first = w.s0; first < w.s1; first += CUT_STAGES, ++handed) {
+      const uint32_t b = handed & 1;
+      if (mine && ok) ok = wait_inline<true>(bar(BAR_ACC_EMPTY + b), ((handed >> 1) & 1) ^ 1, wd);
+      const uint32_t d = tmem + b * BN_MAX;
+      const int end = min(first + CUT_STAGES, w.s1);
+      for (int st = first; st < end; ++st) {
+        const uint32_t b_addr = ring + s * bytes, from = tmem + TMEM_W + t * W_COLS;
+        if (mine && ok) {
+          ok = wait_inline<false>(bar(BAR_A_FULL + s), ph, wd) &&
+               wait_inline<false>(bar(BAR_T_FULL + t), tph, wd);
+          if (ok) {
+            tc_fence_after_sync();
+#pragma unroll
+            for (int k = 0; k < BK / UMMA_K; ++k)
+              umma_16bit_pair_ts(d, from + k * (UMMA_K / 2),
+                                 sdesc_kmajor_sw128(b_addr + (k >= 4 ? bytes / 2 : 0) + (k & 3) * UMMA_K * 2),
+                                 idesc, st != first || k != 0 ? 1u : 0u);
+            umma_commit_pair(bar(BAR_T_EMPTY + t), BOTH);
+            issued = true;
+          }
+        }
+        if (++t == W_BUFS) {
+          t = 0;
+          tph ^= 1;
+        }
+        if (++s == static_cast<uint32_t>(p.a_stages)) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+      if (mine && ok) umma_commit_pair(bar(BAR_ACC_FULL + b), BOTH);
+    }
+  if (issued) {
+    // Every MMA issued has finished once this arrives (also after an abort).
+    umma_commit_pair(bar(BAR_DRAIN), static_cast<uint16_t>(0x1));
+    wait_drain(bar(BAR_DRAIN), 0);
+  }
+  __syncwarp();
+}
+
+// 16 tokens of a thread's channel. The sums of all others stay in registers meanwhile, so that
+// what this needs must not be loaded ahead of it.
+__device__ __forceinline__ void store_tokens(const Output& o, int m, int tokens, int n, const int (&sum)[16],
+                                             float w_scale, float bias) {
+  asm volatile("" ::: "memory");
+  auto value = [&](int i) { return fmaf(static_cast<float>(sum[i]) * o.a_scales[m + i], w_scale, bias); };
+  const int64_t at = static_cast<int64_t>(m) * o.ldd + n;
+  if (o.type == OUT_F32) {
+    float* d = static_cast<float*>(o.d) + at;
+#pragma unroll
+    for (int i = 0; i < 16; ++i, d += o.ldd)
+      if (m + i < tokens) *d = value(i);
+  } else if (o.type == OUT_F16) {
+    __half* d = static_cast<__half*>(o.d) + at;
+#pragma unroll
+    for (int i = 0; i < 16; ++i, d += o.ldd)
+      if (m + i < tokens) *d = __float2half_rn(value(i));
+  } else {
+    __nv_bfloat16* d = static_cast<__nv_bfloat16*>(o.d) + at;
+#pragma unroll
+    for (int i = 0; i < 16; ++i, d += o.ldd)
+      if (m + i < tokens) *d = __float2bfloat16_rn(value(i));
+  }
+  asm volatile("" ::: "memory");
+}
+
+// A thread has one channel, and half of the tile's tokens in registers.
+__device__ __forceinline__ void epilogue(const Params& p, uint32_t sbase, uint32_t tmem, uint32_t rank,
+                                         int warp, const Watchdog& wd) {
+  auto bar = [&](int i) { return sbase + OFF_BAR + 8 * i; };
+  constexpr int BLOCKS = BN_MAX / 2 / 16;   // of 16 tokens
+  const int lane = threadIdx.x & 31, q = warp & 3, hf = (warp - WARP_EPI0) / 4;
+  const int col0 = hf * (p.bn / 2), blocks = p.bn / 32;
+  uint32_t handed = 0;
+  Unit w;
+  for (int u = blockIdx.x / 2; unit_of(p, u, w); u += gridDim.x / 2) {
+    int sum[BLOCKS][16];
+    for (int first = w.s0; first < w.s1; first += CUT_STAGES, ++handed) {
+      const uint32_t b = handed & 1;
+      if (!warp_wait_cta(bar(BAR_ACC_FULL + b), (handed >> 1) & 1, wd)) return;
+      tc_fence_after_sync();
+      const uint32_t from = tmem + (static_cast<uint32_t>(32 * q) << 16) + b * BN_MAX + col0;
+#pragma unroll
+      for (int k = 0; k < BLOCKS; ++k) {
+        if (k >= blocks) continue;
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(from + 16 * k, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int x = __float2int_rn(__uint_as_float(v[i]));
+          sum[k][i] = first == w.s0 ? x : sum[k][i] + x;
+        }
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        const uint32_t e = bar(BAR_ACC_EMPTY + b);
+        if (rank == 0)
+          mbar_arrive(e);
+        else
+          mbar_arrive_cluster(mapa_shared(e, 0));
+      }
+    }
+    const int in_cta = 32 * q + lane;
+    if (p.splits > 1) {
+      // The cuts' sums meet in the warp that arrives last; integers, so in any order.
+      auto slot = [&](int cut) {
+        return p.partial + (static_cast<int64_t>(w.tile * p.splits + cut) * 2 + rank) * (BM * 256) + in_cta;
+      };
+      int* own = slot(w.cut);
+#pragma unroll
+      for (int k = 0; k < BLOCKS; ++k) {
+        if (k >= blocks) continue;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) __stcg(own + (col0 + 16 * k + i) * BM, sum[k][i]);
+      }
+      __threadfence();
+      __syncwarp();
+      uint32_t before = 0;
+      uint32_t* arrived = p.arrived + (w.tile * 2 + rank) * EPI_WARPS + (warp - WARP_EPI0);
+      if (lane == 0) before = atomicAdd(arrived, 1u);
+      before = __shfl_sync(0xffffffffu, before, 0);
+      if (before + 1 != static_cast<uint32_t>(p.splits)) continue;
+      __threadfence();
+      if (lane == 0) *arrived = 0u;
+      for (int cut = 0; cut < p.splits; ++cut) {
+        if (cut == w.cut) continue;
+        const int* other = slot(cut);
+#pragma unroll
+        for (int k = 0; k < BLOCKS; ++k) {
+          if (k >= blocks) continue;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sum[k][i] += __ldcg(other + (col0 + 16 * k + i) * BM);
+          asm volatile("" ::: "memory");
+        }
+      }
+    }
+    const int n = w.n0 + static_cast<int>(rank) * BM + in_cta, m = w.m0 + col0;
+    if (n < p.channels) {
+      const float w_scale = p.out.w_scales[n], bias = p.out.bias ? p.out.bias[n] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < BLOCKS; ++k) {
+        if (k >= blocks) continue;
+        store_tokens(p.out, m + 16 * k, p.tokens, n, sum[k], w_scale, bias);
+      }
+    }
+    __syncwarp();
+  }
+}
+
+__global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
+  uint8_t* smem = smem_raw + pad;
+  const uint32_t sbase = raw + pad;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0);
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + OFF_ABORT);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
+  if (warp == WARP_W && lane == 0) {
+    auto bar = [&](int i) { return sbase + OFF_BAR + 8 * i; };
+    for (int s = 0; s < MAX_STAGES; ++s) {
+      mbar_init(bar(BAR_W_FULL + s), 1);
+      mbar_init(bar(BAR_W_EMPTY + s), CONV_WARPS / 2);
+      mbar_init(bar(BAR_A_FULL + s), 1);
+      mbar_init(bar(BAR_A_EMPTY + s), 1);
+    }
+    for (int t = 0; t < W_BUFS; ++t) {
+      mbar_init(bar(BAR_T_FULL + t), CONV_WARPS);   // 4 of each CTA
+      mbar_init(bar(BAR_T_EMPTY + t), 1);
+    }
+    for (int b = 0; b < ACC_BUFS; ++b) {
+      mbar_init(bar(BAR_ACC_FULL + b), 1);
+      mbar_init(bar(BAR_ACC_EMPTY + b), 2 * EPI_WARPS);
+    }
+    mbar_init(bar(BAR_DRAIN), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&p.tmW);
+    prefetch_tensormap(&p.tmA);
+  }
+  if (warp == WARP_MMA) {
+    tmem_alloc_pair(smem_addr(tmem_slot), TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  const Watchdog wd{abort_flag, p.status, p.timeout_ns};
+  // The set-up above overlaps the previous kernel's end; nothing below does.
+  grid_dependency_wait();
+  if (threadIdx.x == 0) grid_launch_dependents();
+
+  if (warp >= WARP_EPI0) {
+    more_registers<REGS_EPI>();
+    epilogue(p, sbase, tmem, rank, warp, wd);
+  } else {
+    fewer_registers<REGS_FEW>();
+    if (warp >= WARP_CONV0) {
+      convert(p, sbase, smem, tmem, warp, wd);
+    } else if (warp == WARP_W) {
+      if (lane == 0) produce_w(p, sbase, rank, wd);
+    } else if (warp == WARP_A) {
+      if (lane == 0) produce_a(p, sbase, rank, wd);
+    } else if (warp == WARP_TELL) {
+      tell(p, sbase, wd);
+    } else if (warp == WARP_MMA) {
+      if (rank == 0) issue(p, sbase, tmem, wd);
+    }
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync();
+  if (warp == WARP_MMA) {
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem, TMEM_COLS);
+  }
+}
+
+// ------------------------------------------------------------ the tokens in fp16
+
+struct ExpandParams {
+  const int8_t* a;
+  int64_t lda;
+  int tokens, k;
+  int wide;          // a's rows lie on 16-byte boundaries
+  int chunks;        // of 16 in a row
+  uint16_t* out;     // rows of 16 * chunks fp16, zeros after k, in the order of to_fp16
+};
+
+constexpr int EXPAND_THREADS = 256;
+
+__global__ void __launch_bounds__(EXPAND_THREADS) expand_kernel(const __grid_constant__ ExpandParams p) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t v = static_cast<int64_t>(blockIdx.x) * EXPAND_THREADS + threadIdx.x;
+  const int64_t row = v / p.chunks;
+  if (row >= p.tokens) return;
+  const int c = static_cast<int>(v - row * p.chunks) * 16;
+  const uint4 raw = load16(p.a + row * p.lda, c, p.k, p.wide);
+  const uint2 w[4] = {to_fp16(raw.x), to_fp16(raw.y), to_fp16(raw.z), to_fp16(raw.w)};
+  uint4* to = reinterpret_cast<uint4*>(p.out + (row * p.chunks) * 16 + c);
+  to[0] = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
+  to[1] = make_uint4(w[2].x, w[2].y, w[3].x, w[3].y);
+}
+
 }  // namespace i8
 }  // namespace gws

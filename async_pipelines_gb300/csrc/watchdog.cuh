@@ -130,6 +130,47 @@ __device__ __forceinline__ bool warp_wait_spin(uint32_t bar, uint32_t parity,
   return ok != 0;
 }
 
+// The same for a barrier that only this CTA, its copies and its tensor cores arrive on, where the
+// wait's own latency counts: every lane polls, and nothing is called (a call's conventions would
+// spill what lives across it).
+template <typename Ready>
+__device__ __forceinline__ bool warp_poll(Ready ready, const Watchdog& wd) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1; !__all_sync(0xffffffffu, ready()); ++it) {
+    if (it & 255) continue;
+    bool over = *wd.abort != 0;
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > wd.limit_ns) {
+      *wd.abort = 1;
+      atomicExch(wd.status, STATUS_TIMEOUT);
+      over = true;
+    }
+    if (__any_sync(0xffffffffu, over)) return false;
+  }
+  return true;
+}
+__device__ __forceinline__ bool warp_wait_cta(uint32_t bar, uint32_t parity, const Watchdog& wd) {
+  return warp_poll([&] { return mbar_test_wait(bar, parity); }, wd);
+}
+// The same by one thread.
+template <bool kCluster>
+__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, const Watchdog& wd) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1; !(kCluster ? mbar_test_wait_cluster(bar, parity) : mbar_test_wait(bar, parity)); ++it) {
+    if (it & 255) continue;
+    if (*wd.abort) return false;
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > wd.limit_ns) {
+      *wd.abort = 1;
+      atomicExch(wd.status, STATUS_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
 // Warp-uniform bounded wait for a flag in global memory that another CTA
 // sets with release semantics (the in-kernel fix-up's partial-written flag):
 // lane 0 polls with acquire loads; on success every lane loads the flag once
