@@ -204,7 +204,8 @@ int gemm_ws_int8_matmul(gemm_ws_t* h, const int8_t* a, int64_t lda, const float*
   q.channels = static_cast<int>(channels);
   q.stages = static_cast<int>(plan.stages);
   q.bn = plan.bn;
-  q.a_stages = i8::W_BUFS + 3;   // w's ring takes what the tokens' leaves; theirs is freed later
+  q.bufs = i8::w_bufs(q.bn);
+  q.a_stages = q.bufs + 2 < 6 ? 6 : q.bufs + 2;   // freed later than w's, which take what these leave
   q.w_stages = static_cast<int>((i8::RING_ROOM - q.a_stages * i8::a_stage(q.bn)) / i8::W_STAGE);
   if (q.w_stages > i8::MAX_STAGES) q.w_stages = i8::MAX_STAGES;
   q.tiles_m = static_cast<int>(plan.tiles_m);

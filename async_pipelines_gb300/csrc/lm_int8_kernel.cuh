@@ -122,8 +122,10 @@ __global__ void __launch_bounds__(DOT_THREADS) dot_kernel(const __grid_constant_
 // writes them in fp16 first, once for all channels.
 //
 // A pair of CTAs has a tile of 256 channels x bn tokens, each its 128 channels as
-// TMEM lanes. Tensor memory: two accumulators of up to 160 columns, and three buffers of w, 128 x 128
-// each, in the 192 columns after them.
+// TMEM lanes. Tensor memory: two accumulators of bn columns, up to 160, and in what is left of its 512
+// columns buffers of w, 128 x 128 in 64 columns each: three to seven. From a buffer's hand-over until it is
+// seen free again pass about 1500 cycles (both CTAs' warps, the MMAs, and the way between
+// the CTAs), which is why there have to be several.
 //
 // One warp issues all MMAs, and what it does beside that has to fit into their time: for 128 of K it
 // polls both operands at once and commits once, to w's buffer. That the tokens' stage of the same step
@@ -134,10 +136,11 @@ constexpr int BN_MAX = 160;          // tokens of a tile, at most
 constexpr int BK = 128;              // K of a stage: one 128-byte swizzle row of 8-bit integers
 constexpr int HALF_K = 64;           // of a stage: one 128-byte swizzle row of fp16
 constexpr int UMMA_K = 16;
-constexpr int ACC_BUFS = 2, W_BUFS = 3;
+constexpr int ACC_BUFS = 2, MAX_W_BUFS = 7;
 constexpr int W_COLS = BK / 2;       // TMEM columns of a buffer of w
-constexpr int TMEM_W = ACC_BUFS * BN_MAX, TMEM_COLS = 512;
-static_assert(TMEM_W + W_BUFS * W_COLS <= TMEM_COLS, "tensor memory");
+constexpr int TMEM_COLS = 512;
+__host__ __device__ constexpr int w_bufs(int bn) { return (TMEM_COLS - ACC_BUFS * bn) / W_COLS; }
+static_assert(w_bufs(BN_MAX) >= 3 && w_bufs(32) <= MAX_W_BUFS, "tensor memory");
 constexpr int CUT_STAGES = 1024 / BK;   // stages of one accumulator
 // Warpgroups: producers, the MMA warp and the teller; two that convert; two of the epilogue.
 constexpr int WARP_W = 0, WARP_MMA = 1, WARP_A = 2, WARP_TELL = 3, WARP_CONV0 = 4, CONV_WARPS = 8, WARP_EPI0 = WARP_CONV0 + CONV_WARPS,
@@ -151,7 +154,7 @@ constexpr uint32_t W_STAGE = BM * BK;                  // 16 KB
 constexpr uint32_t RING_ROOM = 224 * 1024;
 constexpr int BAR_W_FULL = 0, BAR_W_EMPTY = BAR_W_FULL + MAX_STAGES, BAR_A_FULL = BAR_W_EMPTY + MAX_STAGES,
               BAR_A_EMPTY = BAR_A_FULL + MAX_STAGES, BAR_T_FULL = BAR_A_EMPTY + MAX_STAGES,
-              BAR_T_EMPTY = BAR_T_FULL + W_BUFS, BAR_ACC_FULL = BAR_T_EMPTY + W_BUFS,
+              BAR_T_EMPTY = BAR_T_FULL + MAX_W_BUFS, BAR_ACC_FULL = BAR_T_EMPTY + MAX_W_BUFS,
               BAR_ACC_EMPTY = BAR_ACC_FULL + ACC_BUFS, BAR_DRAIN = BAR_ACC_EMPTY + ACC_BUFS,
               NUM_BARS = BAR_DRAIN + 1;
 constexpr uint32_t OFF_BAR = RING_ROOM;
@@ -167,6 +170,7 @@ struct Params {
   int tokens, channels, stages;   // stages of K
   int bn;                         // tokens of a tile, a multiple of 32
   int w_stages, a_stages;         // of the two rings in shared memory
+  int bufs;                       // w_bufs(bn)
   int tiles_m, tiles_n;           // tiles of tokens, of channels
   int splits;                     // cuts of K; more than one only where all units run at once
   int* partial;                   // a CTA's sums of its cut: [column][channel]
@@ -228,7 +232,7 @@ __device__ __forceinline__ void produce_w(const Params& p, uint32_t sbase, uint3
 #endif
   for (int u = blockIdx.x / 2; ok && unit_of(p, u, w); u += gridDim.x / 2)
     for (int st = w.s0; st < w.s1; ++st) {
-      if (!wait_spin<false>(empty(s), ph ^ 1, wd)) {
+      if (!wait_suspended(empty(s), ph ^ 1, wd)) {
         ok = false;
         break;
       }
@@ -255,7 +259,7 @@ __device__ __forceinline__ void produce_a(const Params& p, uint32_t sbase, uint3
   Unit w;
   for (int u = blockIdx.x / 2; ok && unit_of(p, u, w); u += gridDim.x / 2)
     for (int st = w.s0; st < w.s1; ++st) {
-      if (!wait_spin<false>(empty(s), ph ^ 1, wd)) {
+      if (!wait_suspended(empty(s), ph ^ 1, wd)) {
         ok = false;
         break;
       }
@@ -280,6 +284,15 @@ __device__ __forceinline__ void produce_a(const Params& p, uint32_t sbase, uint3
   }
 }
 
+// A ring's place and phase, some steps on.
+__device__ __forceinline__ void advance(uint32_t& at, uint32_t& phase, uint32_t by, uint32_t size) {
+  at += by;
+  if (at >= size) {
+    at -= size;
+    phase ^= 1;
+  }
+}
+
 // A warp's 32 channels of every other stage, from shared memory to tensor memory. The two
 // warpgroups take the stages in turn: what a stage costs a warp besides its conversions (the waits and
 // arrivals) so has the time of two.
@@ -287,68 +300,62 @@ __device__ __forceinline__ void convert(const Params& p, uint32_t sbase, const u
                                         int warp, const Watchdog& wd) {
   auto bar = [&](int i) { return sbase + OFF_BAR + 8 * i; };
   const int lane = threadIdx.x & 31, row = 32 * (warp & 3) + lane;
-  const uint32_t group = (warp - WARP_CONV0) / 4;
-  const uint32_t mine = tmem + TMEM_W + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+  const uint32_t mine = tmem + ACC_BUFS * p.bn + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
   const uint32_t t_full = mapa_shared(bar(BAR_T_FULL), 0u);   // the leader's
-  const uint32_t w_stages = p.w_stages;
-  uint32_t s = 0, ph = 0, t = 0, tph = 0, turn = 0;
+  const uint32_t stages = p.w_stages, bufs = p.bufs;
+  uint32_t next = (warp - WARP_CONV0) / 4;                    // this warpgroup's next step of all units'
+  uint32_t s = next, ph = 0, t = next, tph = 0, end = 0;
   Unit w;
   for (int u = blockIdx.x / 2; unit_of(p, u, w); u += gridDim.x / 2)
-    for (int st = w.s0; st < w.s1; ++st, turn ^= 1) {
-      if (turn == group) {
-        if (!warp_wait_cta(bar(BAR_W_FULL + s), ph, wd)) return;
-        const uint8_t* from = smem + s * W_STAGE + row * BK;
+    for (end += w.s1 - w.s0; static_cast<int>(end - next) > 0; next += 2) {
+      if (!warp_wait_cta(bar(BAR_W_FULL + s), ph, wd)) return;
+      const uint8_t* from = smem + s * W_STAGE + row * BK;
+      uint4 raw[8];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint4 raw[4];
+      for (int c = 0; c < 8; ++c)   // the TMA's 128-byte swizzle
+        raw[c] = *reinterpret_cast<const uint4*>(from + ((c ^ (row & 7)) << 4));
+      bool free = mbar_test_wait(bar(BAR_T_EMPTY + t), tph ^ 1);   // mostly it is by now
 #pragma unroll
-          for (int c = 0; c < 4; ++c)   // the TMA's 128-byte swizzle
-            raw[c] = *reinterpret_cast<const uint4*>(from + (((4 * half + c) ^ (row & 7)) << 4));
-          uint32_t v[32];
+      for (int half = 0; half < 2; ++half) {
+        uint32_t v[32];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t x[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+        for (int c = 0; c < 4; ++c) {
+          const uint4 r = raw[4 * half + c];
+          const uint32_t x[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint2 two = to_fp16(x[i]);
-              v[8 * c + 2 * i] = two.x;
-              v[8 * c + 2 * i + 1] = two.y;
-            }
+          for (int i = 0; i < 4; ++i) {
+            const uint2 two = to_fp16(x[i]);
+            v[8 * c + 2 * i] = two.x;
+            v[8 * c + 2 * i + 1] = two.y;
           }
-          if (half == 0) {
-            if (!warp_wait_cta(bar(BAR_T_EMPTY + t), tph ^ 1, wd)) return;
-            tc_fence_after_sync();
-          } else {
-            __syncwarp();   // the stage has been read
-            if (lane == 0) mbar_arrive(bar(BAR_W_EMPTY + s));
-          }
-          tmem_st_32x32b_x32(mine + t * W_COLS + half * (W_COLS / 2), v);
         }
-        tmem_wait_st();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_relaxed(t_full + 8 * t);
+        if (half == 0) {
+          __syncwarp();   // the stage has been read
+          if (lane == 0) mbar_arrive(bar(BAR_W_EMPTY + s));
+          if (!__all_sync(0xffffffffu, free) && !warp_wait_cta(bar(BAR_T_EMPTY + t), tph ^ 1, wd)) return;
+          tc_fence_after_sync();
+        }
+        tmem_st_32x32b_x32(mine + t * W_COLS + half * (W_COLS / 2), v);
       }
-      if (++t == W_BUFS) {
-        t = 0;
-        tph ^= 1;
-      }
-      if (++s == w_stages) {
-        s = 0;
-        ph ^= 1;
-      }
+      tmem_wait_st();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(t_full + 8 * t);
+      advance(s, ph, 2, stages);
+      advance(t, tph, 2, bufs);
     }
 }
 
 // Frees the tokens' stages: the MMAs that have read w's buffer of a step have read the step's tokens.
 __device__ __forceinline__ void tell(const Params& p, uint32_t sbase, const Watchdog& wd) {
+  const uint32_t bufs = p.bufs;
   uint32_t s = 0, t = 0, tph = 0;
   Unit w;
   for (int u = blockIdx.x / 2; unit_of(p, u, w); u += gridDim.x / 2)
     for (int st = w.s0; st < w.s1; ++st) {
       if (!warp_wait_cta(sbase + OFF_BAR + 8 * (BAR_T_EMPTY + t), tph, wd)) return;
       if ((threadIdx.x & 31) == 0) mbar_arrive(sbase + OFF_BAR + 8 * (BAR_A_EMPTY + s));
-      if (++t == W_BUFS) {
+      if (++t == bufs) {
         t = 0;
         tph ^= 1;
       }
@@ -364,6 +371,7 @@ __device__ __forceinline__ void issue(const Params& p, uint32_t sbase, uint32_t 
   const uint32_t bytes = a_stage(p.bn), ring = sbase + p.w_stages * W_STAGE;
   const uint32_t idesc = idesc_f16_f32(2 * BM, p.bn);
   const bool mine = elect_one();
+  const uint32_t bufs = p.bufs;
   uint32_t s = 0, ph = 0, t = 0, tph = 0, handed = 0;
   bool ok = true, issued = false;
   Unit w;
@@ -371,10 +379,10 @@ __device__ __forceinline__ void issue(const Params& p, uint32_t sbase, uint32_t 
     for (int first = w.s0; first < w.s1; first += CUT_STAGES, ++handed) {
       const uint32_t b = handed & 1;
       if (mine && ok) ok = wait_inline<true>(bar(BAR_ACC_EMPTY + b), ((handed >> 1) & 1) ^ 1, wd);
-      const uint32_t d = tmem + b * BN_MAX;
+      const uint32_t d = tmem + b * p.bn;
       const int end = min(first + CUT_STAGES, w.s1);
       for (int st = first; st < end; ++st) {
-        const uint32_t b_addr = ring + s * bytes, from = tmem + TMEM_W + t * W_COLS;
+        const uint32_t b_addr = ring + s * bytes, from = tmem + ACC_BUFS * p.bn + t * W_COLS;
         if (mine && ok) {
           ok = wait_inline<false>(bar(BAR_A_FULL + s), ph, wd) &&
                wait_inline<false>(bar(BAR_T_FULL + t), tph, wd);
@@ -389,7 +397,7 @@ __device__ __forceinline__ void issue(const Params& p, uint32_t sbase, uint32_t 
             issued = true;
           }
         }
-        if (++t == W_BUFS) {
+        if (++t == bufs) {
           t = 0;
           tph ^= 1;
         }
@@ -449,7 +457,7 @@ __device__ __forceinline__ void epilogue(const Params& p, uint32_t sbase, uint32
       const uint32_t b = handed & 1;
       if (!warp_wait_cta(bar(BAR_ACC_FULL + b), (handed >> 1) & 1, wd)) return;
       tc_fence_after_sync();
-      const uint32_t from = tmem + (static_cast<uint32_t>(32 * q) << 16) + b * BN_MAX + col0;
+      const uint32_t from = tmem + (static_cast<uint32_t>(32 * q) << 16) + b * p.bn + col0;
 #pragma unroll
       for (int k = 0; k < BLOCKS; ++k) {
         if (k >= blocks) continue;
@@ -538,7 +546,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
       mbar_init(bar(BAR_A_FULL + s), 1);
       mbar_init(bar(BAR_A_EMPTY + s), 1);
     }
-    for (int t = 0; t < W_BUFS; ++t) {
+    for (int t = 0; t < MAX_W_BUFS; ++t) {
       mbar_init(bar(BAR_T_FULL + t), CONV_WARPS);   // 4 of each CTA
       mbar_init(bar(BAR_T_EMPTY + t), 1);
     }

@@ -130,44 +130,52 @@ __device__ __forceinline__ bool warp_wait_spin(uint32_t bar, uint32_t parity,
   return ok != 0;
 }
 
-// The same for a barrier that only this CTA, its copies and its tensor cores arrive on, where the
-// wait's own latency counts: every lane polls, and nothing is called (a call's conventions would
-// spill what lives across it).
-template <typename Ready>
-__device__ __forceinline__ bool warp_poll(Ready ready, const Watchdog& wd) {
-  uint64_t t0 = 0;
-  for (uint32_t it = 1; !__all_sync(0xffffffffu, ready()); ++it) {
-    if (it & 255) continue;
-    bool over = *wd.abort != 0;
-    const uint64_t now = global_timer_ns();
-    if (t0 == 0) t0 = now;
-    if (now - t0 > wd.limit_ns) {
-      *wd.abort = 1;
-      atomicExch(wd.status, STATUS_TIMEOUT);
-      over = true;
-    }
-    if (__any_sync(0xffffffffu, over)) return false;
-  }
+// A probe that may suspend the thread until the phase completes or WAIT_HINT_NS pass.
+__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(WAIT_HINT_NS)
+      : "memory");
+  return ok != 0;
+}
+
+// What a wait does now and then: whether it is to give up.
+__device__ __forceinline__ bool wait_over(uint64_t& t0, const Watchdog& wd) {
+  if (*wd.abort) return true;
+  const uint64_t now = global_timer_ns();
+  if (t0 == 0) t0 = now;
+  if (now - t0 <= wd.limit_ns) return false;
+  *wd.abort = 1;
+  atomicExch(wd.status, STATUS_TIMEOUT);
   return true;
 }
+
+// Waits on a barrier that only this CTA, its copies and its tensor cores arrive on, without a call (a
+// call's conventions would spill what lives across it). The warp is suspended meanwhile: warps that
+// poll take issue slots from those that work.
 __device__ __forceinline__ bool warp_wait_cta(uint32_t bar, uint32_t parity, const Watchdog& wd) {
-  return warp_poll([&] { return mbar_test_wait(bar, parity); }, wd);
+  uint64_t t0 = 0;
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+    if (__any_sync(0xffffffffu, wait_over(t0, wd))) return false;
+  return true;
 }
 // The same by one thread.
+__device__ __forceinline__ bool wait_suspended(uint32_t bar, uint32_t parity, const Watchdog& wd) {
+  uint64_t t0 = 0;
+  while (!mbar_try_wait(bar, parity))
+    if (wait_over(t0, wd)) return false;
+  return true;
+}
+// By one thread whose wake-up counts: it polls.
 template <bool kCluster>
 __device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, const Watchdog& wd) {
   uint64_t t0 = 0;
-  for (uint32_t it = 1; !(kCluster ? mbar_test_wait_cluster(bar, parity) : mbar_test_wait(bar, parity)); ++it) {
-    if (it & 255) continue;
-    if (*wd.abort) return false;
-    const uint64_t now = global_timer_ns();
-    if (t0 == 0) t0 = now;
-    if (now - t0 > wd.limit_ns) {
-      *wd.abort = 1;
-      atomicExch(wd.status, STATUS_TIMEOUT);
-      return false;
-    }
-  }
+  for (uint32_t it = 1; !(kCluster ? mbar_test_wait_cluster(bar, parity) : mbar_test_wait(bar, parity)); ++it)
+    if ((it & 255) == 0 && wait_over(t0, wd)) return false;
   return true;
 }
 
