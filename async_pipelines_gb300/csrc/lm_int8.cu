@@ -160,6 +160,8 @@ int gemm_ws_int8_matmul(gemm_ws_t* h, const int8_t* a, int64_t lda, const float*
   out.d = d;
   out.ldd = ldd;
   out.type = dtype;
+  out.channels = static_cast<int>(channels);
+  out.pairs = reinterpret_cast<uintptr_t>(d) % 4 == 0 && (tokens == 1 || ldd % 2 == 0);
   out.a_scales = a_scales;
   out.w_scales = w_scales;
   out.bias = bias;

@@ -21,7 +21,8 @@ enum OutType { OUT_BF16 = 0, OUT_F16 = 1, OUT_F32 = 2 };
 struct Output {
   void* d;
   int64_t ldd;
-  int type;
+  int type, channels;
+  bool pairs;      // d's rows allow accesses of two elements
   const float *a_scales, *w_scales, *bias;   // bias may be NULL
 };
 
@@ -151,13 +152,14 @@ constexpr int REGS_LAUNCH = 96, REGS_FEW = 72, REGS_EPI = 128;
 static_assert(WARP_EPI0 * REGS_FEW + EPI_WARPS * REGS_EPI <= THREADS / 32 * REGS_LAUNCH, "registers of a block");
 constexpr int MAX_STAGES = 12;
 constexpr uint32_t W_STAGE = BM * BK;                  // 16 KB
-constexpr uint32_t RING_ROOM = 224 * 1024;
+constexpr uint32_t RING_ROOM = 222 * 1024;
 constexpr int BAR_W_FULL = 0, BAR_W_EMPTY = BAR_W_FULL + MAX_STAGES, BAR_A_FULL = BAR_W_EMPTY + MAX_STAGES,
               BAR_A_EMPTY = BAR_A_FULL + MAX_STAGES, BAR_T_FULL = BAR_A_EMPTY + MAX_STAGES,
               BAR_T_EMPTY = BAR_T_FULL + MAX_W_BUFS, BAR_ACC_FULL = BAR_T_EMPTY + MAX_W_BUFS,
               BAR_ACC_EMPTY = BAR_ACC_FULL + ACC_BUFS, BAR_DRAIN = BAR_ACC_EMPTY + ACC_BUFS,
               NUM_BARS = BAR_DRAIN + 1;
-constexpr uint32_t OFF_BAR = RING_ROOM;
+constexpr uint32_t OFF_SCALES = RING_ROOM;              // the tokens' scales, for each epilogue warp
+constexpr uint32_t OFF_BAR = OFF_SCALES + EPI_WARPS * (BN_MAX / 2) * 4;
 constexpr uint32_t OFF_TMEM = OFF_BAR + NUM_BARS * 8;
 constexpr uint32_t OFF_ABORT = OFF_TMEM + 4;
 constexpr uint32_t SMEM_BYTES = OFF_ABORT + 4 + 1024;   // + slack to align the base
@@ -378,7 +380,10 @@ __device__ __forceinline__ void issue(const Params& p, uint32_t sbase, uint32_t 
   for (int u = blockIdx.x / 2; unit_of(p, u, w); u += gridDim.x / 2)
     for (int first = w.s0; first < w.s1; first += CUT_STAGES, ++handed) {
       const uint32_t b = handed & 1;
-      if (mine && ok) ok = wait_inline<true>(bar(BAR_ACC_EMPTY + b), ((handed >> 1) & 1) ^ 1, wd);
+      if (mine && ok) {
+        ok = wait_inline<false>(bar(BAR_ACC_EMPTY + b), ((handed >> 1) & 1) ^ 1, wd);
+        tc_fence_after_sync();
+      }
       const uint32_t d = tmem + b * p.bn;
       const int end = min(first + CUT_STAGES, w.s1);
       for (int st = first; st < end; ++st) {
@@ -416,43 +421,71 @@ __device__ __forceinline__ void issue(const Params& p, uint32_t sbase, uint32_t 
   __syncwarp();
 }
 
-// 16 tokens of a thread's channel. The sums of all others stay in registers meanwhile, so that
-// what this needs must not be loaded ahead of it.
-__device__ __forceinline__ void store_tokens(const Output& o, int m, int tokens, int n, const int (&sum)[16],
-                                             float w_scale, float bias) {
-  asm volatile("" ::: "memory");
-  auto value = [&](int i) { return fmaf(static_cast<float>(sum[i]) * o.a_scales[m + i], w_scale, bias); };
+// 16 tokens of a thread's channel. In 16 bits neighbouring lanes exchange two tokens' values at a
+// time, so that each stores two channels of one of them.
+__device__ __forceinline__ void store_tokens(const Output& o, int m, int tokens, int n, bool both,
+                                             const int (&sum)[16], const float4* scales, float w_scale,
+                                             float bias) {
+  asm volatile("" ::: "memory");   // nothing of this ahead: the other sums fill the registers
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 f = scales[i];
+    v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = fmaf(static_cast<float>(sum[i]) * v[i], w_scale, bias);
   const int64_t at = static_cast<int64_t>(m) * o.ldd + n;
   if (o.type == OUT_F32) {
     float* d = static_cast<float*>(o.d) + at;
 #pragma unroll
     for (int i = 0; i < 16; ++i, d += o.ldd)
-      if (m + i < tokens) *d = value(i);
-  } else if (o.type == OUT_F16) {
-    __half* d = static_cast<__half*>(o.d) + at;
-#pragma unroll
-    for (int i = 0; i < 16; ++i, d += o.ldd)
-      if (m + i < tokens) *d = __float2half_rn(value(i));
-  } else {
-    __nv_bfloat16* d = static_cast<__nv_bfloat16*>(o.d) + at;
-#pragma unroll
-    for (int i = 0; i < 16; ++i, d += o.ldd)
-      if (m + i < tokens) *d = __float2bfloat16_rn(value(i));
+      if (n < o.channels && m + i < tokens) *d = v[i];
+    return;
   }
-  asm volatile("" ::: "memory");
+  const bool odd = threadIdx.x & 1;
+  const uint32_t pick = odd ? 0x3276 : 0x5410;   // even lanes: both channels' token i, odd ones: token i + 1
+  uint16_t* d = static_cast<uint16_t*>(o.d) + at + (odd ? o.ldd - 1 : 0);
+#pragma unroll
+  for (int i = 0; i < 16; i += 2, d += 2 * o.ldd) {
+    uint32_t own;
+    if (o.type == OUT_F16) {
+      const __half2 h = __floats2half2_rn(v[i], v[i + 1]);
+      own = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      own = pack_bf16x2(v[i], v[i + 1]);
+    }
+    const uint32_t two = __byte_perm(own, __shfl_xor_sync(0xffffffffu, own, 1), pick);
+    if (m + i + odd >= tokens) continue;
+    if (both) {
+      *reinterpret_cast<uint32_t*>(d) = two;
+    } else {   // an unaligned row, or the last channel
+      const int c = n - odd;
+      if (c < o.channels) d[0] = static_cast<uint16_t>(two);
+      if (c + 1 < o.channels) d[1] = static_cast<uint16_t>(two >> 16);
+    }
+  }
 }
 
 // A thread has one channel, and half of the tile's tokens in registers.
-__device__ __forceinline__ void epilogue(const Params& p, uint32_t sbase, uint32_t tmem, uint32_t rank,
-                                         int warp, const Watchdog& wd) {
+__device__ __forceinline__ void epilogue(const Params& p, uint32_t sbase, uint8_t* smem, uint32_t tmem,
+                                         uint32_t rank, int warp, const Watchdog& wd) {
   auto bar = [&](int i) { return sbase + OFF_BAR + 8 * i; };
   constexpr int BLOCKS = BN_MAX / 2 / 16;   // of 16 tokens
   const int lane = threadIdx.x & 31, q = warp & 3, hf = (warp - WARP_EPI0) / 4;
   const int col0 = hf * (p.bn / 2), blocks = p.bn / 32;
+  float* scales = reinterpret_cast<float*>(smem + OFF_SCALES) + (warp - WARP_EPI0) * (BN_MAX / 2);
   uint32_t handed = 0;
   Unit w;
   for (int u = blockIdx.x / 2; unit_of(p, u, w); u += gridDim.x / 2) {
     int sum[BLOCKS][16];
+    // what the tile's end needs, loaded ahead
+    const int in_cta = 32 * q + lane, n = w.n0 + static_cast<int>(rank) * BM + in_cta, m = w.m0 + col0;
+    const bool there = n < p.channels;
+    const float w_scale = there ? p.out.w_scales[n] : 0.0f, bias = there && p.out.bias ? p.out.bias[n] : 0.0f;
+    __syncwarp();   // the tile before has been stored
+    for (int i = lane; i < p.bn / 2; i += 32) scales[i] = m + i < p.tokens ? p.out.a_scales[m + i] : 0.0f;
+    __syncwarp();
     for (int first = w.s0; first < w.s1; first += CUT_STAGES, ++handed) {
       const uint32_t b = handed & 1;
       if (!warp_wait_cta(bar(BAR_ACC_FULL + b), (handed >> 1) & 1, wd)) return;
@@ -477,10 +510,9 @@ __device__ __forceinline__ void epilogue(const Params& p, uint32_t sbase, uint32
         if (rank == 0)
           mbar_arrive(e);
         else
-          mbar_arrive_cluster(mapa_shared(e, 0));
+          mbar_arrive_cluster_relaxed(mapa_shared(e, 0));
       }
     }
-    const int in_cta = 32 * q + lane;
     if (p.splits > 1) {
       // The cuts' sums meet in the warp that arrives last; integers, so in any order.
       auto slot = [&](int cut) {
@@ -514,16 +546,12 @@ __device__ __forceinline__ void epilogue(const Params& p, uint32_t sbase, uint32
         }
       }
     }
-    const int n = w.n0 + static_cast<int>(rank) * BM + in_cta, m = w.m0 + col0;
-    if (n < p.channels) {
-      const float w_scale = p.out.w_scales[n], bias = p.out.bias ? p.out.bias[n] : 0.0f;
+    const bool both = p.out.pairs && (n | 1) < p.channels;
 #pragma unroll
-      for (int k = 0; k < BLOCKS; ++k) {
-        if (k >= blocks) continue;
-        store_tokens(p.out, m + 16 * k, p.tokens, n, sum[k], w_scale, bias);
-      }
+    for (int k = 0; k < BLOCKS; ++k) {
+      if (k >= blocks) continue;
+      store_tokens(p.out, m + 16 * k, p.tokens, n, both, sum[k], reinterpret_cast<const float4*>(scales) + 4 * k, w_scale, bias);
     }
-    __syncwarp();
   }
 }
 
@@ -576,7 +604,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
 
   if (warp >= WARP_EPI0) {
     more_registers<REGS_EPI>();
-    epilogue(p, sbase, tmem, rank, warp, wd);
+    epilogue(p, sbase, smem, tmem, rank, warp, wd);
   } else {
     fewer_registers<REGS_FEW>();
     if (warp >= WARP_CONV0) {
