@@ -37,43 +37,57 @@ int launch_dot(gemm_ws* h, i8::DotParams& q, cudaStream_t s) {
   return e == cudaSuccess ? GEMM_WS_OK : cuda_fail(h, e);
 }
 
-// Up to this many tokens the integer dot products of the CUDA cores keep up with w's bytes.
-constexpr int64_t kDotTokens = 8;
+// Up to four tokens the integer dot products of the CUDA cores keep up with w's bytes (4 tokens x
+// 4096 over 131072: 102 us, by tensor cores 104; 8 tokens 188 and 104), and up to eight where w is so small
+// that the tensor cores' start counts for more (8 x 4096 over 4096: 13 us and 14; 8 x 8192 over
+// 8192: 40 and 24).
+bool few(int64_t tokens, int64_t channels, int64_t k) {
+  return tokens <= 4 || (tokens <= 8 && channels * k <= int64_t{1} << 24);
+}
 
 struct Plan {
   bool dot;
   int bn, splits;
   int64_t tiles_m, tiles_n, stages, clusters;
   int64_t chunks;    // of 16 in a row of the tokens in fp16
-  int64_t bytes;     // of workspace
+  int64_t total, arrived;   // byte offsets in the workspace, behind the tokens in fp16
+  int64_t bytes;            // of workspace
 };
 
-// Tiles as wide as leave the least work to the slowest pair: rounds times tokens, and 24 tokens' worth of
-// time a round for what does not grow with them. K is cut where the tiles do not reach all pairs.
+// Tiles as wide as leave the least work to the slowest pair: rounds times the time of a tile, where a
+// stage of K takes as long as its MMAs, but no less than 128 tokens' (its conversion), and some more; and a
+// tile's end as long as 3 stages, 4 more where cuts of K are joined. K is cut where the tiles do not reach
+// all pairs.
 Plan make_plan(const gemm_ws* h, int64_t tokens, int64_t channels, int64_t k) {
   Plan q;
   std::memset(&q, 0, sizeof q);
-  q.dot = tokens <= kDotTokens || h->max_pair_clusters < 1;
+  q.dot = few(tokens, channels, k) || h->max_pair_clusters < 1;
   if (q.dot) return q;
   q.stages = ceil_div(k, i8::BK);
   q.tiles_n = ceil_div(channels, 2 * i8::BM);
   const int64_t pairs = h->max_pair_clusters;
   int64_t least = 0;
   for (int bn = i8::BN_MAX; bn >= 32; bn -= 32) {
-    const int64_t cost = ceil_div(ceil_div(tokens, bn) * q.tiles_n, pairs) * (bn + 24);
-    if (q.bn == 0 || cost < least) {
-      least = cost;
-      q.bn = bn;
-    }
+    const int64_t tiles = ceil_div(tokens, bn) * q.tiles_n;
+    int64_t splits = pairs / tiles;
+    if (splits > q.stages / 2) splits = q.stages / 2;   // at least 256 of K
+    if (splits < 1) splits = 1;
+    const int64_t end = splits > 1 ? 7 : 3;
+    const int64_t cost =
+        ceil_div(tiles * splits, pairs) * (ceil_div(q.stages, splits) + end) * ((bn > 128 ? bn : 128) + 32);
+    if (q.bn != 0 && cost >= least) continue;
+    least = cost;
+    q.bn = bn;
+    q.splits = static_cast<int>(splits);
   }
   q.tiles_m = ceil_div(tokens, q.bn);
-  const int64_t tiles = q.tiles_m * q.tiles_n;
-  int64_t splits = pairs / tiles;
-  if (splits > q.stages / 2) splits = q.stages / 2;   // at least 256 of K
-  q.splits = splits > 1 ? static_cast<int>(splits) : 1;
-  q.clusters = tiles * q.splits < pairs ? tiles * q.splits : pairs;
+  const int64_t units = q.tiles_m * q.tiles_n * q.splits;
+  q.clusters = units < pairs ? units : pairs;
   q.chunks = ceil_div(k, 16);
-  q.bytes = ceil_div(tokens * q.chunks * 32, 256) * 256;
+  q.total = ceil_div(tokens * q.chunks * 32, 256) * 256;
+  const int64_t tiles = q.splits > 1 ? q.tiles_m * q.tiles_n : 0;
+  q.arrived = q.total + tiles * 2 * q.bn * i8::BM * 4;
+  q.bytes = q.arrived + ceil_div(tiles * 2 * i8::EPI_WARPS * 4, 256) * 256;
   return q;
 }
 
@@ -193,13 +207,15 @@ int gemm_ws_int8_matmul(gemm_ws_t* h, const int8_t* a, int64_t lda, const float*
   e.wide = wide;
   e.chunks = static_cast<int>(plan.chunks);
   e.out = static_cast<uint16_t*>(workspace);
+  e.zero = reinterpret_cast<uint4*>(static_cast<uint8_t*>(workspace) + plan.total);
+  e.zeros = (plan.bytes - plan.total) / 16;
   i8::Params q;
   std::memset(&q, 0, sizeof q);
   const int64_t pitch = 16 * plan.chunks;
   if (!encode(h, &q.tmW, w, false, k, channels, channels > 1 ? ldw : ceil_div(k, 16) * 16, i8::BK, i8::BM) ||
       !encode(h, &q.tmA, workspace, true, pitch, tokens, pitch, i8::HALF_K, plan.bn / 2))
     return GEMM_WS_ERR_CUDA;
-  const int rc = launch(h, i8::expand_kernel, ceil_div(tokens * plan.chunks, i8::EXPAND_THREADS),
+  const int rc = launch(h, i8::expand_kernel, ceil_div(tokens * plan.chunks + e.zeros, i8::EXPAND_THREADS),
                         i8::EXPAND_THREADS, 0, s, e);
   if (rc != GEMM_WS_OK) return rc;
   q.tokens = static_cast<int>(tokens);
@@ -213,8 +229,8 @@ int gemm_ws_int8_matmul(gemm_ws_t* h, const int8_t* a, int64_t lda, const float*
   q.tiles_m = static_cast<int>(plan.tiles_m);
   q.tiles_n = static_cast<int>(plan.tiles_n);
   q.splits = plan.splits;
-  q.partial = reinterpret_cast<int*>(h->partial);
-  q.arrived = h->work + kWorkWords;
+  q.total = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + plan.total);
+  q.arrived = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + plan.arrived);
   q.out = out;
   q.status = h->work + 1;
   q.timeout_ns = h->timeout_ns;

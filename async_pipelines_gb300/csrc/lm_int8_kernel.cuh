@@ -175,8 +175,8 @@ struct Params {
   int bufs;                       // w_bufs(bn)
   int tiles_m, tiles_n;           // tiles of tokens, of channels
   int splits;                     // cuts of K; more than one only where all units run at once
-  int* partial;                   // a CTA's sums of its cut: [column][channel]
-  uint32_t* arrived;              // [tile][CTA of the pair][epilogue warp]: zero at launch, left zero
+  int* total;                     // [tile][CTA of the pair][token][channel], zero at launch: the cuts' sums
+  uint32_t* arrived;              // [tile][CTA of the pair][epilogue warp], zero at launch
   Output out;
   uint32_t* status;
   unsigned long long timeout_ns;
@@ -514,36 +514,28 @@ __device__ __forceinline__ void epilogue(const Params& p, uint32_t sbase, uint8_
       }
     }
     if (p.splits > 1) {
-      // The cuts' sums meet in the warp that arrives last; integers, so in any order.
-      auto slot = [&](int cut) {
-        return p.partial + (static_cast<int64_t>(w.tile * p.splits + cut) * 2 + rank) * (BM * 256) + in_cta;
-      };
-      int* own = slot(w.cut);
+      // The cuts' sums meet in the workspace, which is zero at launch: integers, so in any order.
+      // The warp that arrives last takes what is there.
+      const int64_t which = static_cast<int64_t>(w.tile) * 2 + rank;
+      int* total = p.total + (which * p.bn + col0) * BM + in_cta;
 #pragma unroll
       for (int k = 0; k < BLOCKS; ++k) {
         if (k >= blocks) continue;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) __stcg(own + (col0 + 16 * k + i) * BM, sum[k][i]);
+        for (int i = 0; i < 16; ++i) atomicAdd(total + (16 * k + i) * BM, sum[k][i]);
       }
       __threadfence();
       __syncwarp();
       uint32_t before = 0;
-      uint32_t* arrived = p.arrived + (w.tile * 2 + rank) * EPI_WARPS + (warp - WARP_EPI0);
-      if (lane == 0) before = atomicAdd(arrived, 1u);
+      if (lane == 0) before = atomicAdd(p.arrived + which * EPI_WARPS + (warp - WARP_EPI0), 1u);
       before = __shfl_sync(0xffffffffu, before, 0);
       if (before + 1 != static_cast<uint32_t>(p.splits)) continue;
       __threadfence();
-      if (lane == 0) *arrived = 0u;
-      for (int cut = 0; cut < p.splits; ++cut) {
-        if (cut == w.cut) continue;
-        const int* other = slot(cut);
 #pragma unroll
-        for (int k = 0; k < BLOCKS; ++k) {
-          if (k >= blocks) continue;
+      for (int k = 0; k < BLOCKS; ++k) {
+        if (k >= blocks) continue;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) sum[k][i] += __ldcg(other + (col0 + 16 * k + i) * BM);
-          asm volatile("" ::: "memory");
-        }
+        for (int i = 0; i < 16; ++i) sum[k][i] = __ldcg(total + (16 * k + i) * BM);
       }
     }
     const bool both = p.out.pairs && (n | 1) < p.channels;
@@ -638,6 +630,8 @@ struct ExpandParams {
   int wide;          // a's rows lie on 16-byte boundaries
   int chunks;        // of 16 in a row
   uint16_t* out;     // rows of 16 * chunks fp16, zeros after k, in the order of to_fp16
+  uint4* zero;       // what is to be zero before the product, and how many
+  int64_t zeros;
 };
 
 constexpr int EXPAND_THREADS = 256;
@@ -646,8 +640,14 @@ __global__ void __launch_bounds__(EXPAND_THREADS) expand_kernel(const __grid_con
   grid_dependency_wait();
   grid_launch_dependents();
   const int64_t v = static_cast<int64_t>(blockIdx.x) * EXPAND_THREADS + threadIdx.x;
-  const int64_t row = v / p.chunks;
-  if (row >= p.tokens) return;
+  const int64_t chunks = static_cast<int64_t>(p.tokens) * p.chunks;
+  if (v >= chunks) {
+    if (v - chunks < p.zeros) p.zero[v - chunks] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  // 32-bit divisions where they do
+  const int64_t row = chunks < (int64_t{1} << 31) ? static_cast<uint32_t>(v) / static_cast<uint32_t>(p.chunks)
+                                                  : v / p.chunks;
   const int c = static_cast<int>(v - row * p.chunks) * 16;
   const uint4 raw = load16(p.a + row * p.lda, c, p.k, p.wide);
   const uint2 w[4] = {to_fp16(raw.x), to_fp16(raw.y), to_fp16(raw.z), to_fp16(raw.w)};
