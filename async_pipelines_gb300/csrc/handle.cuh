@@ -21,7 +21,7 @@ struct MapCacheEntry {
 };
 constexpr int kMapCache = 16;
 // The operators' kernels that take more shared memory than a kernel has by default.
-constexpr int kLargeKernels = 64;
+constexpr int kLargeKernels = 96;
 
 struct gemm_ws {
   int device;

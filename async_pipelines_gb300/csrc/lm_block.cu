@@ -37,6 +37,35 @@ Team any_team(const gemm_ws* h, int64_t rows, int64_t cols) {
   return t;
 }
 
+// The rings need some rows of each SM to be worth their set-up.
+constexpr int64_t kRingRows = 4;
+
+// How the rows pass through a ring: `most` groups a thread or half as many, the smallest teams that hold
+// a row, and two rows at least for each team. `vectors`: rows behind the ring. Returns the groups a
+// thread; 0 where two rows do not fit, or a row is more than a CTA's warps hold.
+int plan_ring(const gemm_ws* h, int64_t cols, int64_t size, int inputs, int vectors, int most, int* team,
+              gws::RingPlan* q) {
+  const int64_t row = cols * size, groups = cols / gws::GROUP;
+  int64_t room = (gws::RING_BYTES - vectors * row) / (inputs * row);
+  if (room > gws::RING_MAX_STAGES) room = gws::RING_MAX_STAGES;
+  for (int vpt = most; vpt >= most / 2 && vpt > 0; vpt /= 2) {
+    const int64_t warps = ceil_div(groups, 32 * vpt);
+    if (warps > gws::RING_WARPS) return 0;
+    std::memset(q, 0, sizeof *q);
+    q->row_bytes = static_cast<uint32_t>(row);
+    *team = static_cast<int>(32 * warps);
+    q->teams = static_cast<int>(gws::RING_WARPS / warps);
+    q->stages = static_cast<int>(room / q->teams);
+    q->status = h->work + 1;
+    q->timeout_ns = h->timeout_ns;
+#ifdef GEMM_WS_DEBUG
+    q->debug_fault = h->debug_fault;
+#endif
+    if (q->stages >= 2) return vpt;
+  }
+  return 0;
+}
+
 template <typename T, bool BYTES>
 auto block_kernel(const Team& t) {
   return t.vpt == 1   ? gws::block_norm_kernel<T, 1, 1024, BYTES>
@@ -46,18 +75,39 @@ auto block_kernel(const Team& t) {
 
 template <typename T>
 int launch_block(gemm_ws* h, bool fast, gws::BlockParams& p, cudaStream_t s) {
+  if (fast && p.rows >= kRingRows * h->num_sms) {
+    gws::RingPlan q;
+    const int vpt = plan_ring(h, p.cols, sizeof(T), p.ldg ? 3 : 2, sizeof(T) == 2 ? 3 : 0,
+                              sizeof(T) == 2 ? 4 : 2, &p.team, &q);
+    if (vpt) {
+      constexpr int MOST = sizeof(T) == 2 ? 4 : 2;
+      auto kernel = p.quant == gws::Q_SAME ? gws::block_norm_ring_kernel<T, MOST, false>
+                                           : gws::block_norm_ring_kernel<T, MOST, true>;
+      if (vpt < MOST)
+        kernel = p.quant == gws::Q_SAME ? gws::block_norm_ring_kernel<T, MOST / 2, false>
+                                        : gws::block_norm_ring_kernel<T, MOST / 2, true>;
+      return launch(h, kernel, h->num_sms, gws::RING_THREADS, gws::RING_BYTES, s, p, q);
+    }
+  }
   const Team t = fast ? pick_team(h, p.rows, p.cols, gws::FAST, 1) : any_team(h, p.rows, p.cols);
   p.team = t.threads;
   const int64_t blocks = ceil_div(p.rows, t.rows);
   if (!fast)
-    return launch(h, gws::block_norm_any_kernel<T>, blocks, t.threads * t.rows,
-                  t.rows * partial_pitch(p.cols) * sizeof(float), s, p, kMaxCols * sizeof(float));
+    return launch_sized(h, gws::block_norm_any_kernel<T>, blocks, t.threads * t.rows,
+                        t.rows * partial_pitch(p.cols) * sizeof(float), kMaxCols * sizeof(float), s, p);
   auto kernel = p.quant == gws::Q_SAME ? block_kernel<T, false>(t) : block_kernel<T, true>(t);
   return launch(h, kernel, blocks, t.threads * t.rows, 0, s, p);
 }
 
 template <typename T>
 int launch_quantize(gemm_ws* h, bool fast, gws::QuantizeParams& p, cudaStream_t s) {
+  if (fast && p.rows >= kRingRows * h->num_sms) {
+    gws::RingPlan q;
+    const int vpt = plan_ring(h, p.cols, sizeof(T), 1, 0, 4, &p.team, &q);
+    if (vpt)
+      return launch(h, vpt == 4 ? gws::quantize_rows_ring_kernel<T, 4> : gws::quantize_rows_ring_kernel<T, 2>,
+                    h->num_sms, gws::RING_THREADS, gws::RING_BYTES, s, p, q);
+  }
   const Team t = fast ? pick_team(h, p.rows, p.cols, gws::FAST, 1) : any_team(h, p.rows, p.cols);
   p.team = t.threads;
   auto kernel = !fast        ? gws::quantize_rows_any_kernel<T>
@@ -94,6 +144,32 @@ int launch_sums(gemm_ws* h, gws::BlockSumsParams& q, cudaStream_t s) {
 template <typename T>
 int launch_grad(gemm_ws* h, bool fast, gws::BlockGradParams& p, gws::BlockSumsParams& q, bool first,
                 bool second, cudaStream_t s) {
+  const int64_t sums = first + second;
+  auto finish = [&](int rc, int64_t blocks) {
+    if (rc != GEMM_WS_OK || !sums) return rc;
+    q.partial = p.partial;
+    q.partial_s = p.partial_s;
+    q.blocks = static_cast<int>(blocks);
+    q.cols = p.cols;
+    q.pitch = static_cast<int>(partial_pitch(p.cols));
+    return launch_sums<T>(h, q, s);
+  };
+  auto place = [&](int64_t blocks) {
+    p.partial = first ? h->partial : nullptr;
+    p.partial_s = second ? h->partial + (first ? blocks * partial_pitch(p.cols) : 0) : nullptr;
+  };
+  if (fast && p.rows >= h->num_sms) {
+    gws::RingPlan r;
+    const int vpt = plan_ring(h, p.cols, sizeof(T), 3 + (p.dh ? 1 : 0) + (p.ldg ? 1 : 0), sizeof(T) == 2 ? 3 : 0,
+                              sizeof(T) == 2 ? 2 : 1, &p.team, &r);
+    if (vpt) {
+      place(h->num_sms);
+      auto kernel = gws::block_norm_grad_ring_kernel<T, 1>;
+      if constexpr (sizeof(T) == 2)
+        if (vpt == 2) kernel = gws::block_norm_grad_ring_kernel<T, 2>;
+      return finish(launch(h, kernel, h->num_sms, gws::RING_THREADS, gws::RING_BYTES, s, p, r), h->num_sms);
+    }
+  }
   const Team t = fast ? grad_team(h, p.rows, p.cols) : any_team(h, p.rows, p.cols);
   p.team = t.threads;
   auto kernel = !fast                          ? gws::block_norm_grad_any_kernel<T>
@@ -111,19 +187,10 @@ int launch_grad(gemm_ws* h, bool fast, gws::BlockGradParams& p, gws::BlockSumsPa
   if (smem > 0 && each > static_cast<int64_t>(200 * 1024 / smem)) each = 200 * 1024 / smem;
   if (each < 1) each = 1;
   if (blocks > each * h->num_sms) blocks = each * h->num_sms;
-  const int64_t sums = first + second;
   if (sums && blocks > h->num_sms * kPartialPerSm / (pitch * sums))
     blocks = h->num_sms * kPartialPerSm / (pitch * sums);
-  p.partial = first ? h->partial : nullptr;
-  p.partial_s = second ? h->partial + (first ? blocks * pitch : 0) : nullptr;
-  const int rc = launch(h, kernel, blocks, threads, smem, s, p, 3 * kMaxCols * sizeof(float));
-  if (rc != GEMM_WS_OK || !sums) return rc;
-  q.partial = p.partial;
-  q.partial_s = p.partial_s;
-  q.blocks = static_cast<int>(blocks);
-  q.cols = p.cols;
-  q.pitch = static_cast<int>(pitch);
-  return launch_sums<T>(h, q, s);
+  place(blocks);
+  return finish(launch_sized(h, kernel, blocks, threads, smem, 3 * kMaxCols * sizeof(float), s, p), blocks);
 }
 
 }  // namespace

@@ -281,6 +281,235 @@ __global__ void __launch_bounds__(ANY_MOST) block_norm_any_kernel(const __grid_c
   }
 }
 
+// How a launch's rows pass through the ring in shared memory.
+struct RingPlan {
+  int stages, teams;    // stages of a team
+  uint32_t row_bytes;   // of one matrix
+  uint32_t* status;
+  unsigned long long timeout_ns;
+#ifdef GEMM_WS_DEBUG
+  int debug_fault;      // 3: only the first stages are ever filled
+#endif
+};
+
+// A team's place in the ring.
+struct TeamRing {
+  int which, t;
+  RingRows rows;
+  uint32_t stage0, stage_bytes, bars;
+  int stages;
+  int s = 0;            // this row's stage and its phase
+  uint32_t ph = 0;
+  __device__ __forceinline__ uint32_t full(int stage) const { return bars + 8 * (which * stages + stage); }
+  __device__ __forceinline__ void next() {
+    if (++s == stages) {
+      s = 0;
+      ph ^= 1;
+    }
+  }
+  // Given up at row k: the copies under way land before the CTA ends.
+  __device__ __forceinline__ void drain(int64_t k) const {
+    if (k < rows.count && t == 0)
+      for (int64_t j = k; j < rows.count && j < k + stages; ++j)
+        wait_drain(full(static_cast<int>(j % stages)), static_cast<uint32_t>(j / stages) & 1);
+  }
+};
+
+// Sets the barriers up and finds the team's place (all threads of the CTA call it).
+__device__ __forceinline__ TeamRing enter_ring(const RingPlan& q, int64_t rows, int team, int inputs,
+                                               uint8_t* ring, uint64_t* bars, uint32_t* aborted) {
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < q.teams * q.stages; ++s) mbar_init(smem_addr(&bars[s]), 1);
+    *aborted = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  grid_launch_dependents();
+  TeamRing r;
+  r.t = threadIdx.x % team;
+  r.which = threadIdx.x / team;
+  r.rows = ring_rows(rows, q.teams, r.which);
+  r.stage_bytes = inputs * q.row_bytes;
+  r.stage0 = smem_addr(ring) + r.which * q.stages * r.stage_bytes;
+  r.bars = smem_addr(bars);
+  r.stages = q.stages;
+  return r;
+}
+
+// Up to three vectors over the columns, for all of a launch's rows: a thread's groups of them in its
+// registers, or in 16 bits, where the threads have more groups, in shared memory behind the ring (in registers
+// they would spill, and what shared memory leaves of the L1 cache does not hold that: gradient of
+// 8192 x 8192 213 us).
+template <typename T, int VPT>
+struct Vectors {
+  static constexpr bool SHARED = sizeof(T) == 2;
+  Raw<T> held[SHARED ? 1 : 3][SHARED ? 1 : VPT];
+  const Raw<T>* at;
+  int groups, team;
+  // All threads of the CTA call it; `vectors` NULL: zeros.
+  __device__ __forceinline__ Vectors(uint8_t* behind, const void* const (&vectors)[3], int groups_, int team_, int t)
+      : at(reinterpret_cast<const Raw<T>*>(behind) + t), groups(groups_), team(team_) {
+#pragma unroll
+    for (int v = 0; v < 3; ++v) {
+      const Raw<T>* from = static_cast<const Raw<T>*>(vectors[v]);
+      if constexpr (SHARED) {
+        for (int g = threadIdx.x; g < groups; g += blockDim.x)
+          reinterpret_cast<Raw<T>*>(behind)[v * groups + g] = from ? from[g] : Raw<T>{};
+      } else {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+          held[v][j] = {};
+          if (from && j * team + t < groups) held[v][j] = from[j * team + t];
+        }
+      }
+    }
+    if (SHARED) __syncthreads();
+  }
+  // Vector v, the thread's group j (which has to be there).
+  __device__ __forceinline__ Raw<T> get(int v, int j) const {
+    if constexpr (SHARED)
+      return at[v * groups + j * team];
+    else
+      return held[v][j];
+  }
+};
+
+// Many rows that lie FAST come through a ring of bulk copies, so that the next rows are on their
+// way while a team waits for its row's two sums. One thread of a team fetches; the barrier of the
+// second sum says that all of it has the row in registers, and the stage is filled anew.
+template <typename T, int VPT, bool BYTES>
+__global__ void __launch_bounds__(RING_THREADS, 1)
+    block_norm_ring_kernel(const __grid_constant__ BlockParams p, const __grid_constant__ RingPlan q) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ __align__(8) uint64_t bars[RING_MAX_STAGES];
+  __shared__ SumMax box[2][RING_WARPS];
+  __shared__ float box1[2][RING_WARPS];
+  __shared__ uint32_t aborted;
+  const int cols = p.cols, groups = cols / GROUP, team = p.team;
+  const bool each = p.ldg != 0;
+  TeamRing at = enter_ring(q, p.rows, team, each ? 3 : 2, ring, bars, &aborted);
+  const Watchdog wd{&aborted, q.status, q.timeout_ns};
+  const int t = at.t, which = at.which;
+  const void* const vectors[3] = {p.weight, p.post, each ? nullptr : p.gate};
+  const Vectors<T, VPT> vec(ring + q.teams * q.stages * at.stage_bytes, vectors, groups, team, t);
+  if (at.rows.count == 0) return;
+  const float inv_cols = 1.0f / static_cast<float>(cols);
+  auto fetch = [&](int64_t k, int s) {
+#ifdef GEMM_WS_DEBUG
+    if (q.debug_fault == 3 && k >= q.stages) return;   // injected fault: the row never comes
+#endif
+    const int64_t row = at.rows.first + k * at.rows.step;
+    const uint32_t dst = at.stage0 + s * at.stage_bytes, bar = at.full(s);
+    mbar_arrive_expect_tx(bar, at.stage_bytes);
+    bulk_load_1d(dst, static_cast<const T*>(p.x) + row * p.ldx, q.row_bytes, bar);
+    bulk_load_1d(dst + q.row_bytes, static_cast<const T*>(p.residual) + row * p.ldr, q.row_bytes, bar);
+    if (each)
+      bulk_load_1d(dst + 2 * q.row_bytes, static_cast<const T*>(p.gate) + row * p.ldg, q.row_bytes, bar);
+  };
+  if (t == 0)
+    for (int k = 0; k < q.stages && k < at.rows.count; ++k) fetch(k, k);
+  int turn = 0;
+  int64_t k = 0;
+  for (; k < at.rows.count; ++k, turn ^= 1) {
+    const int64_t row = at.rows.first + k * at.rows.step;
+    bool ok = warp_wait_cta(at.full(at.s), at.ph, wd);
+    const uint8_t* stage = ring + (which * q.stages + at.s) * at.stage_bytes;
+    const Raw<T>* x = reinterpret_cast<const Raw<T>*>(stage) + t;
+    const Raw<T>* res = reinterpret_cast<const Raw<T>*>(stage + q.row_bytes) + t;
+    const Raw<T>* gate = reinterpret_cast<const Raw<T>*>(stage + 2 * q.row_bytes) + t;
+    float r1 = 1.0f;
+    if (p.post) {
+      Pair sums = 0;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j)
+        if (j * team + t < groups) {
+          Pair v[GROUP / 2];
+          unpack(x[j * team], v);
+#pragma unroll
+          for (int i = 0; i < GROUP / 2; ++i) sums = fma2(v[i], v[i], sums);
+        }
+      const float sum =
+          ring_sum(values_of(sums).x + values_of(sums).y, which, team, box1[turn], &ok);
+      if (!ok) break;
+      r1 = rsqrtf(sum * inv_cols + p.eps);
+      if (p.post_rstd && t == 0) p.post_rstd[row] = r1;
+    }
+    const Pair r11 = pair_of(r1, r1), alpha = pair_of(p.alpha, p.alpha);
+    Raw<T>* h = reinterpret_cast<Raw<T>*>(static_cast<T*>(p.h) + row * p.ldh) + t;
+    float v[VPT][GROUP];
+    Pair sums = 0;
+    float top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const bool mine = j * team + t < groups;
+#pragma unroll
+      for (int i = 0; i < GROUP; ++i) v[j][i] = 0.0f;
+      if (mine) {
+        Pair a[GROUP / 2], f[GROUP / 2];
+        unpack(x[j * team], a);
+        if (p.post) {
+          unpack(vec.get(1, j), f);
+#pragma unroll
+          for (int i = 0; i < GROUP / 2; ++i) a[i] = mul2(mul2(a[i], r11), f[i]);
+        }
+        if (p.gate) {
+          unpack(each ? gate[j * team] : vec.get(2, j), f);
+#pragma unroll
+          for (int i = 0; i < GROUP / 2; ++i) a[i] = mul2(a[i], f[i]);
+        }
+        unpack(res[j * team], f);
+#pragma unroll
+        for (int i = 0; i < GROUP / 2; ++i) {
+          a[i] = fma2(alpha, f[i], a[i]);
+          sums = fma2(a[i], a[i], sums);
+          v[j][2 * i] = values_of(a[i]).x;
+          v[j][2 * i + 1] = values_of(a[i]).y;
+        }
+        if (BYTES) {
+          unpack(vec.get(0, j), f);
+#pragma unroll
+          for (int i = 0; i < GROUP / 2; ++i) {
+            const float2 b = values_of(mul2(a[i], f[i]));
+            top = max_nan(top, max_nan(fabsf(b.x), fabsf(b.y)));
+          }
+        }
+        if (p.h) h[j * team] = pack<T>(v[j]);
+      }
+    }
+    const SumMax all = ring_sum_max({values_of(sums).x + values_of(sums).y, top}, which, team, box[turn], &ok);
+    if (!ok) break;
+    if (t == 0 && k + q.stages < at.rows.count) fetch(k + q.stages, at.s);   // the row is in registers
+    const float r2 = rsqrtf(all.sum * inv_cols + p.eps);
+    if (p.rstd && t == 0) p.rstd[row] = r2;
+    float scale = 0.0f;
+    if (BYTES && p.quant != Q_E4M3_GROUP) {
+      scale = row_scale(p.quant, all.max, r2);
+      if (t == 0) p.scales[row] = scale;
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int g = j * team + t;
+      if (g < groups) {
+        float w[GROUP];
+        unpack(vec.get(0, j), w);
+#pragma unroll
+        for (int i = 0; i < GROUP; ++i) v[j][i] = v[j][i] * r2 * w[i];
+      }
+      if (!BYTES) {
+        if (g < groups) (reinterpret_cast<Raw<T>*>(static_cast<T*>(p.y) + row * p.ldy))[g] = pack<T>(v[j]);
+      } else {
+        if (p.quant == Q_E4M3_GROUP)
+          scale = group_scale(v[j], p.scales + row * ((cols + QUANT_GROUP - 1) / QUANT_GROUP), g, groups);
+        const uint2 out = p.quant == Q_INT8_ROW ? int8_quotients(v[j], scale) : quotients(v[j], scale);
+        if (g < groups) reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + row * p.ldy)[g] = out;
+      }
+    }
+    at.next();
+  }
+  at.drain(k);
+}
+
 // ------------------------------------------------------------ backward
 
 struct BlockGradParams {
@@ -446,6 +675,200 @@ __global__ void __launch_bounds__(MOST, 1)
     if (p.partial && teams > 1) __syncthreads();   // `share` has been read
     leave_partial(acc_s, share, p.partial_s, groups, team, teams, threadIdx.x / team, t);
   }
+}
+
+// The gradient of many rows that lie FAST, through the ring (loaded straight into registers the
+// rows of an SM stop at each of a row's two sums). Every pass over a row reads it from the ring; the
+// barrier of the next row's first sum says that all of the team is done with it. Two groups a thread, so
+// that its shares of the two sums over the rows and the three vectors fit its registers.
+template <typename T, int VPT>
+__global__ void __launch_bounds__(RING_THREADS, 1)
+    block_norm_grad_ring_kernel(const __grid_constant__ BlockGradParams p, const __grid_constant__ RingPlan q) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ __align__(8) uint64_t bars[RING_MAX_STAGES];
+  __shared__ float box[2][RING_WARPS];
+  __shared__ uint32_t aborted;
+  const int cols = p.cols, groups = cols / GROUP, team = p.team;
+  const bool each = p.ldg != 0, post = p.post != nullptr;
+  const int gate_at = p.dh ? 4 : 3;
+  TeamRing at = enter_ring(q, p.rows, team, gate_at + (each ? 1 : 0), ring, bars, &aborted);
+  const Watchdog wd{&aborted, q.status, q.timeout_ns};
+  const int t = at.t, which = at.which;
+  const void* const vectors[3] = {p.weight, p.post, each ? nullptr : p.gate};
+  const Vectors<T, VPT> vec(ring + q.teams * q.stages * at.stage_bytes, vectors, groups, team, t);
+  const float inv_cols = 1.0f / static_cast<float>(cols);
+
+  Pair acc[VPT][GROUP / 2], acc_s[VPT][GROUP / 2];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j)
+#pragma unroll
+    for (int i = 0; i < GROUP / 2; ++i) acc[j][i] = acc_s[j][i] = 0;
+
+  if (at.rows.count > 0) {
+    auto fetch = [&](int64_t k, int s) {
+#ifdef GEMM_WS_DEBUG
+      if (q.debug_fault == 3 && k >= q.stages) return;   // injected fault: the row never comes
+#endif
+      const int64_t row = at.rows.first + k * at.rows.step;
+      const uint32_t dst = at.stage0 + s * at.stage_bytes, bar = at.full(s), each_row = q.row_bytes;
+      mbar_arrive_expect_tx(bar, at.stage_bytes);
+      bulk_load_1d(dst, static_cast<const T*>(p.dy) + row * p.lddy, each_row, bar);
+      bulk_load_1d(dst + each_row, static_cast<const T*>(p.h) + row * p.ldh, each_row, bar);
+      bulk_load_1d(dst + 2 * each_row, static_cast<const T*>(p.x) + row * p.ldx, each_row, bar);
+      if (p.dh) bulk_load_1d(dst + 3 * each_row, static_cast<const T*>(p.dh) + row * p.lddh, each_row, bar);
+      if (each)
+        bulk_load_1d(dst + gate_at * each_row, static_cast<const T*>(p.gate) + row * p.ldg, each_row, bar);
+    };
+    if (t == 0)
+      for (int k = 0; k < q.stages && k < at.rows.count; ++k) fetch(k, k);
+    int turn = 0, before = q.stages - 1;   // the row before's stage
+    float next2 = p.rstd[at.rows.first], next1 = post ? p.post_rstd[at.rows.first] : 1.0f;
+    const Pair alpha = pair_of(p.alpha, p.alpha);
+    int64_t k = 0;
+    for (; k < at.rows.count; ++k) {
+      const int64_t row = at.rows.first + k * at.rows.step;
+      const float r2 = next2, r1 = next1;
+      if (k + 1 < at.rows.count) {
+        next2 = p.rstd[row + at.rows.step];
+        if (post) next1 = p.post_rstd[row + at.rows.step];
+      }
+      bool ok = warp_wait_cta(at.full(at.s), at.ph, wd);
+      const uint8_t* stage = ring + (which * q.stages + at.s) * at.stage_bytes;
+      const Raw<T>* dy = reinterpret_cast<const Raw<T>*>(stage) + t;
+      const Raw<T>* h = reinterpret_cast<const Raw<T>*>(stage + q.row_bytes) + t;
+      const Raw<T>* x = reinterpret_cast<const Raw<T>*>(stage + 2 * q.row_bytes) + t;
+      const Raw<T>* dh = reinterpret_cast<const Raw<T>*>(stage + 3 * q.row_bytes) + t;
+      const Raw<T>* gate = reinterpret_cast<const Raw<T>*>(stage + gate_at * q.row_bytes) + t;
+      const Pair r22 = pair_of(r2, r2), r11 = pair_of(r1, r1);
+      Pair sums = 0;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j)
+        if (j * team + t < groups) {
+          Pair a[GROUP / 2], m[GROUP / 2], w[GROUP / 2];
+          unpack(dy[j * team], a);
+          unpack(h[j * team], m);
+          unpack(vec.get(0, j), w);
+#pragma unroll
+          for (int i = 0; i < GROUP / 2; ++i) {
+            const Pair am = mul2(a[i], m[i]);
+            acc[j][i] = fma2(am, r22, acc[j][i]);
+            sums = fma2(am, w[i], sums);
+          }
+        }
+      float sum = ring_sum(values_of(sums).x + values_of(sums).y, which, team, box[turn], &ok);
+      turn ^= 1;
+      if (!ok) break;
+      // The whole team has been in the sum, so it has done with the row before.
+      if (t == 0 && k > 0 && k - 1 + q.stages < at.rows.count) fetch(k - 1 + q.stages, before);
+      // g = dh + r2 dy weight - h r2^2 mean(dy weight h r2), then e * post
+      const float c2 = -r2 * r2 * (r2 * sum * inv_cols);
+      const Pair c22 = pair_of(c2, c2);
+      Raw<T>* dres = reinterpret_cast<Raw<T>*>(static_cast<T*>(p.dres) + row * p.lddres) + t;
+      Raw<T>* dgate = reinterpret_cast<Raw<T>*>(static_cast<T*>(p.dgate) + row * p.lddg) + t;
+      Raw<T>* dx = reinterpret_cast<Raw<T>*>(static_cast<T*>(p.dx) + row * p.lddx) + t;
+      auto put = [](Raw<T>& to, const Pair (&v)[GROUP / 2]) {
+        float f[GROUP];
+#pragma unroll
+        for (int i = 0; i < GROUP / 2; ++i) {
+          f[2 * i] = values_of(v[i]).x;
+          f[2 * i + 1] = values_of(v[i]).y;
+        }
+        to = pack<T>(f);
+      };
+      Pair d[VPT][GROUP / 2];
+      sums = 0;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        if (j * team + t >= groups) continue;
+        Pair a[GROUP / 2], f[GROUP / 2];
+        {
+          Raw<T> dr = {};
+          if (p.dh) dr = dh[j * team];
+          unpack(dr, d[j]);
+        }
+        unpack(dy[j * team], a);
+        unpack(vec.get(0, j), f);
+#pragma unroll
+        for (int i = 0; i < GROUP / 2; ++i) d[j][i] = fma2(mul2(a[i], f[i]), r22, d[j][i]);
+        unpack(h[j * team], a);
+#pragma unroll
+        for (int i = 0; i < GROUP / 2; ++i) d[j][i] = fma2(a[i], c22, d[j][i]);
+        if (p.dres) {
+#pragma unroll
+          for (int i = 0; i < GROUP / 2; ++i) a[i] = mul2(d[j][i], alpha);
+          put(dres[j * team], a);
+        }
+        Pair n[GROUP / 2];
+        unpack(x[j * team], n);
+#pragma unroll
+        for (int i = 0; i < GROUP / 2; ++i) n[i] = mul2(n[i], r11);
+        if (post) unpack(vec.get(1, j), f);
+        if (each) {
+          if (p.dgate) {
+#pragma unroll
+            for (int i = 0; i < GROUP / 2; ++i) {
+              a[i] = mul2(d[j][i], n[i]);
+              if (post) a[i] = mul2(a[i], f[i]);
+            }
+            put(dgate[j * team], a);
+          }
+          unpack(gate[j * team], a);
+#pragma unroll
+          for (int i = 0; i < GROUP / 2; ++i) d[j][i] = mul2(d[j][i], a[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < GROUP / 2; ++i) acc_s[j][i] = fma2(d[j][i], n[i], acc_s[j][i]);
+        if (p.gate && !each) {
+          unpack(vec.get(2, j), a);
+#pragma unroll
+          for (int i = 0; i < GROUP / 2; ++i) d[j][i] = mul2(d[j][i], a[i]);
+        }
+        if (post) {
+#pragma unroll
+          for (int i = 0; i < GROUP / 2; ++i) {
+            d[j][i] = mul2(d[j][i], f[i]);
+            sums = fma2(d[j][i], n[i], sums);
+          }
+        } else {
+          put(dx[j * team], d[j]);
+        }
+      }
+      if (post) {
+        sum = ring_sum(values_of(sums).x + values_of(sums).y, which, team, box[turn], &ok);
+        turn ^= 1;
+        if (!ok) break;
+        const float c1 = -r1 * (r1 * sum * inv_cols);
+        const Pair c11 = pair_of(c1, c1);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+          if (j * team + t >= groups) continue;
+          Pair n[GROUP / 2];
+          unpack(x[j * team], n);
+#pragma unroll
+          for (int i = 0; i < GROUP / 2; ++i) d[j][i] = fma2(n[i], c11, mul2(d[j][i], r11));
+          put(dx[j * team], d[j]);
+        }
+      }
+      before = at.s;
+      at.next();
+    }
+    at.drain(k);
+  }
+  float mine[VPT][GROUP];
+  auto leave = [&](const Pair (&of)[VPT][GROUP / 2], float* partial) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+      for (int i = 0; i < GROUP / 2; ++i) {
+        mine[j][2 * i] = values_of(of[j][i]).x;
+        mine[j][2 * i + 1] = values_of(of[j][i]).y;
+      }
+    __syncthreads();   // all teams have done with the ring, or with the sum before
+    leave_partial(mine, reinterpret_cast<float*>(ring), partial, groups, team, q.teams, which, t);
+  };
+  static_assert(RING_THREADS * VPT * GROUP * sizeof(float) <= RING_BYTES, "the teams' rows fit the ring");
+  if (p.partial) leave(acc, p.partial);
+  if (p.partial_s) leave(acc_s, p.partial_s);
 }
 
 // The same for rows that lie anywhere: e * post and the columns' shares of the sums are in shared memory, and
@@ -627,6 +1050,62 @@ __global__ void __launch_bounds__(MOST, 1)
     unpack(xr[k], v);
     if (k * team + t < groups) y[k * team + t] = int8_quotients(v, scale);
   }
+}
+
+// Many rows that lie FAST, through the ring.
+template <typename T, int VPT>
+__global__ void __launch_bounds__(RING_THREADS, 1)
+    quantize_rows_ring_kernel(const __grid_constant__ QuantizeParams p, const __grid_constant__ RingPlan q) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ __align__(8) uint64_t bars[RING_MAX_STAGES];
+  __shared__ SumMax box[2][RING_WARPS];
+  __shared__ uint32_t aborted;
+  const int groups = p.cols / GROUP, team = p.team;
+  TeamRing at = enter_ring(q, p.rows, team, 1, ring, bars, &aborted);
+  const Watchdog wd{&aborted, q.status, q.timeout_ns};
+  if (at.rows.count == 0) return;
+  const int t = at.t, which = at.which;
+  auto fetch = [&](int64_t k, int s) {
+#ifdef GEMM_WS_DEBUG
+    if (q.debug_fault == 3 && k >= q.stages) return;   // injected fault: the row never comes
+#endif
+    const int64_t row = at.rows.first + k * at.rows.step;
+    mbar_arrive_expect_tx(at.full(s), at.stage_bytes);
+    bulk_load_1d(at.stage0 + s * at.stage_bytes, static_cast<const T*>(p.x) + row * p.ldx, q.row_bytes, at.full(s));
+  };
+  if (t == 0)
+    for (int k = 0; k < q.stages && k < at.rows.count; ++k) fetch(k, k);
+  int turn = 0;
+  int64_t k = 0;
+  for (; k < at.rows.count; ++k, turn ^= 1) {
+    const int64_t row = at.rows.first + k * at.rows.step;
+    bool ok = warp_wait_cta(at.full(at.s), at.ph, wd);
+    const Raw<T>* x = reinterpret_cast<const Raw<T>*>(ring + (which * q.stages + at.s) * at.stage_bytes) + t;
+    Raw<T> xr[VPT] = {};
+    SumMax s = {0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      if (j * team + t < groups) xr[j] = x[j * team];
+      float v[GROUP];
+      unpack(xr[j], v);
+#pragma unroll
+      for (int i = 0; i < GROUP; ++i) s.max = max_nan(s.max, fabsf(v[i]));
+    }
+    s = ring_sum_max(s, which, team, box[turn], &ok);
+    if (!ok) break;
+    if (t == 0 && k + q.stages < at.rows.count) fetch(k + q.stages, at.s);   // the row is in registers
+    const float scale = int8_scale(s.max);
+    if (t == 0) p.scales[row] = scale;
+    uint2* y = reinterpret_cast<uint2*>(p.y + row * p.ldy) + t;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      float v[GROUP];
+      unpack(xr[j], v);
+      if (j * team + t < groups) y[j * team] = int8_quotients(v, scale);
+    }
+    at.next();
+  }
+  at.drain(k);
 }
 
 // Rows that lie anywhere, read twice (the second time from L2).

@@ -60,9 +60,9 @@ bool any_overlap(const Span (&out)[O], const Span (&in)[I]) {
 // A launch that may start while the stream's previous kernel ends; each of
 // these kernels waits for that one before it touches global memory. `most`: the most
 // shared memory that the kernel is ever launched with, where that is not always the same.
-template <typename P>
-int launch(gemm_ws* h, void (*kernel)(P), int64_t blocks, int threads, size_t smem, cudaStream_t s,
-           const P& params, size_t most = 0) {
+template <typename... P>
+int launch_sized(gemm_ws* h, void (*kernel)(P...), int64_t blocks, int threads, size_t smem, size_t most,
+                 cudaStream_t s, const P&... params) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
@@ -78,8 +78,13 @@ int launch(gemm_ws* h, void (*kernel)(P), int64_t blocks, int threads, size_t sm
   cudaError_t e = cudaSuccess;
   if (smem > kDefaultSmem)
     e = allow_smem(h, reinterpret_cast<const void*>(kernel), most > smem ? most : smem);
-  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, params);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, params...);
   return e == cudaSuccess ? GEMM_WS_OK : cuda_fail(h, e);
+}
+template <typename... P>
+int launch(gemm_ws* h, void (*kernel)(P...), int64_t blocks, int threads, size_t smem, cudaStream_t s,
+           const P&... params) {
+  return launch_sized(h, kernel, blocks, threads, smem, smem, s, params...);
 }
 
 // The threads of a row and the groups that each holds.

@@ -12,8 +12,9 @@ constexpr size_t kSmemMost = 4 * (kSliceMost + 2 * kSliceMost / 32 + 2 * gws::MA
 
 template <typename T, typename U>
 int launch_logits(gemm_ws* h, bool fast, size_t smem, const gws::LogitParams& p, cudaStream_t s) {
-  return launch(h, fast ? gws::adjust_logits_kernel<T, U, gws::FAST> : gws::adjust_logits_kernel<T, U, gws::ANY>,
-                p.rows * p.slices, gws::LOGIT_THREADS, smem, s, p, kSmemMost);
+  return launch_sized(
+      h, fast ? gws::adjust_logits_kernel<T, U, gws::FAST> : gws::adjust_logits_kernel<T, U, gws::ANY>,
+      p.rows * p.slices, gws::LOGIT_THREADS, smem, kSmemMost, s, p);
 }
 
 }  // namespace

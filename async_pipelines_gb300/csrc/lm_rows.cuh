@@ -612,6 +612,29 @@ __device__ __forceinline__ float ring_sum(float sum, int which, int team, float*
   return sum;
 }
 
+// The same for a sum and a maximum.
+__device__ __forceinline__ SumMax ring_sum_max(SumMax v, int which, int team, SumMax* box, bool* ok) {
+  const int warps = team / 32, lane = threadIdx.x % 32;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    v.sum += __shfl_xor_sync(0xffffffffu, v.sum, o);
+    v.max = max_nan(v.max, __shfl_xor_sync(0xffffffffu, v.max, o));
+  }
+  if (warps == 1) {
+    __syncwarp();
+    return v;
+  }
+  if (lane == 0) box[threadIdx.x / 32] = v;
+  *ok = team_sync(1 + which, team, *ok);
+  v = (lane & 15) < warps ? box[which * warps + (lane & 15)] : SumMax{0.0f, 0.0f};
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    v.sum += __shfl_xor_sync(0xffffffffu, v.sum, o);
+    v.max = max_nan(v.max, __shfl_xor_sync(0xffffffffu, v.max, o));
+  }
+  return v;
+}
+
 // ------------------------------------------------------------ sums over the rows
 
 // A block's row of partial sums by columns: the teams' shares added in the teams' order.
