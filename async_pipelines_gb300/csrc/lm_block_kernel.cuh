@@ -83,9 +83,11 @@ struct Join {
   }
 };
 
-// Rows that lie FAST: a team holds one in registers. BYTES: y in 8 bits.
-template <typename T, int VPT, int MOST, bool BYTES>
-__global__ void __launch_bounds__(MOST, 1)
+// Rows that lie FAST: a team holds one in registers. BYTES: y in 8 bits. LATE: many rows, and no gate for each
+// value; the vectors are then loaded, from L2 or L1, when they are needed, as their registers would cost
+// the SM a row (8192 x 8192 bf16 87 us, 96 with all loads first; 600 x 4096 5.3 and 4.0).
+template <typename T, int VPT, int MOST, bool BYTES, bool LATE>
+__global__ void __launch_bounds__(MOST, LATE && MOST == 256 ? 3 : 1)
     block_norm_kernel(const __grid_constant__ BlockParams p) {
   __shared__ SumMax box[2][32];
   grid_dependency_wait();
@@ -105,8 +107,8 @@ __global__ void __launch_bounds__(MOST, 1)
     if (g < groups) {
       xr[k] = group(p.x, p.ldx, g);
       rr[k] = group(p.residual, p.ldr, g);
-      if (p.gate) gr[k] = group(p.gate, p.ldg, g);
-      if (p.post) pr[k] = group(p.post, 0, g);
+      if (!LATE && p.gate) gr[k] = group(p.gate, p.ldg, g);
+      if (!LATE && p.post) pr[k] = group(p.post, 0, g);
     }
   }
   float r1 = 1.0f;
@@ -133,6 +135,10 @@ __global__ void __launch_bounds__(MOST, 1)
     float f[GROUP], post[GROUP], gates[GROUP];
     unpack(xr[k], v[k]);
     unpack(rr[k], f);
+    if (LATE && g < groups) {
+      if (p.post) pr[k] = group(p.post, 0, g);
+      if (p.gate) gr[k] = group(p.gate, 0, g);
+    }
     unpack(pr[k], post);
     unpack(gr[k], gates);
     join(v[k], post, gates, f);
@@ -1050,62 +1056,6 @@ __global__ void __launch_bounds__(MOST, 1)
     unpack(xr[k], v);
     if (k * team + t < groups) y[k * team + t] = int8_quotients(v, scale);
   }
-}
-
-// Many rows that lie FAST, through the ring.
-template <typename T, int VPT>
-__global__ void __launch_bounds__(RING_THREADS, 1)
-    quantize_rows_ring_kernel(const __grid_constant__ QuantizeParams p, const __grid_constant__ RingPlan q) {
-  extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ __align__(8) uint64_t bars[RING_MAX_STAGES];
-  __shared__ SumMax box[2][RING_WARPS];
-  __shared__ uint32_t aborted;
-  const int groups = p.cols / GROUP, team = p.team;
-  TeamRing at = enter_ring(q, p.rows, team, 1, ring, bars, &aborted);
-  const Watchdog wd{&aborted, q.status, q.timeout_ns};
-  if (at.rows.count == 0) return;
-  const int t = at.t, which = at.which;
-  auto fetch = [&](int64_t k, int s) {
-#ifdef GEMM_WS_DEBUG
-    if (q.debug_fault == 3 && k >= q.stages) return;   // injected fault: the row never comes
-#endif
-    const int64_t row = at.rows.first + k * at.rows.step;
-    mbar_arrive_expect_tx(at.full(s), at.stage_bytes);
-    bulk_load_1d(at.stage0 + s * at.stage_bytes, static_cast<const T*>(p.x) + row * p.ldx, q.row_bytes, at.full(s));
-  };
-  if (t == 0)
-    for (int k = 0; k < q.stages && k < at.rows.count; ++k) fetch(k, k);
-  int turn = 0;
-  int64_t k = 0;
-  for (; k < at.rows.count; ++k, turn ^= 1) {
-    const int64_t row = at.rows.first + k * at.rows.step;
-    bool ok = warp_wait_cta(at.full(at.s), at.ph, wd);
-    const Raw<T>* x = reinterpret_cast<const Raw<T>*>(ring + (which * q.stages + at.s) * at.stage_bytes) + t;
-    Raw<T> xr[VPT] = {};
-    SumMax s = {0.0f, 0.0f};
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      if (j * team + t < groups) xr[j] = x[j * team];
-      float v[GROUP];
-      unpack(xr[j], v);
-#pragma unroll
-      for (int i = 0; i < GROUP; ++i) s.max = max_nan(s.max, fabsf(v[i]));
-    }
-    s = ring_sum_max(s, which, team, box[turn], &ok);
-    if (!ok) break;
-    if (t == 0 && k + q.stages < at.rows.count) fetch(k + q.stages, at.s);   // the row is in registers
-    const float scale = int8_scale(s.max);
-    if (t == 0) p.scales[row] = scale;
-    uint2* y = reinterpret_cast<uint2*>(p.y + row * p.ldy) + t;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      float v[GROUP];
-      unpack(xr[j], v);
-      if (j * team + t < groups) y[j * team] = int8_quotients(v, scale);
-    }
-    at.next();
-  }
-  at.drain(k);
 }
 
 // Rows that lie anywhere, read twice (the second time from L2).

@@ -5,16 +5,19 @@
 #include "lm_host.cuh"
 #include "lm_logits_kernel.cuh"
 
+static_assert((gws::LOGIT_STEP & (gws::LOGIT_STEP - 1)) == 0 && (gws::LOGIT_GROUPS & (gws::LOGIT_GROUPS - 1)) == 0,
+              "slices are powers of two");
+
 namespace {
 
-constexpr int64_t kSliceMost = 16384;   // tokens of the largest slice: 64 KB of counts
-constexpr size_t kSmemMost = 4 * (kSliceMost + 2 * kSliceMost / 32 + 2 * gws::MAX_BIASES);
+constexpr size_t kSmemMost = 4 * (2 * gws::LOGIT_SLICE + 4 * gws::LOGIT_SLICE / 32 + 2 * gws::MAX_BIASES +
+                                   gws::LISTED);
 
 template <typename T, typename U>
 int launch_logits(gemm_ws* h, bool fast, size_t smem, const gws::LogitParams& p, cudaStream_t s) {
   return launch_sized(
       h, fast ? gws::adjust_logits_kernel<T, U, gws::FAST> : gws::adjust_logits_kernel<T, U, gws::ANY>,
-      p.rows * p.slices, gws::LOGIT_THREADS, smem, kSmemMost, s, p);
+      p.rows * p.blocks, gws::LOGIT_THREADS, smem, kSmemMost, s, p);
 }
 
 }  // namespace
@@ -82,16 +85,33 @@ int gemm_ws_adjust_logits(gemm_ws_t* h, int dtype, const void* logits, int64_t l
   q.biases = bias_tokens ? static_cast<int>(biases) : 0;
   q.allowed = allowed;
   q.lda = lda;
-  // Slices as long as they may be, but short enough that few rows still reach all SMs.
-  const int64_t steps = ceil_div(vocab, gws::LOGIT_STEP);
-  int64_t per = kSliceMost / gws::LOGIT_STEP;
-  const int64_t spread = ceil_div(steps * rows, 2 * h->num_sms);
+  // Slices as long as they may be, but short enough that few rows still reach all SMs. Then as many of
+  // them a block as leave the least work to the slowest SM, which holds two blocks: a block begins with
+  // loads that wait for each other, which takes as long as about three slices, and where the
+  // history does not fit the lists that is so for each slice.
+  const int64_t steps = ceil_div(vocab, gws::LOGIT_STEP), held = 2 * h->num_sms;
+  int64_t per = gws::LOGIT_GROUPS;
+  const int64_t spread = ceil_div(steps * rows, held);
   if (per > spread) per = spread;
   q.slice = static_cast<int>(per * gws::LOGIT_STEP);
   q.slices = static_cast<int>(ceil_div(vocab, q.slice));
-  if (rows * q.slices > kMaxDim) return GEMM_WS_ERR_INVALID_ARG;
-  const size_t smem = 4 * ((tokens ? q.slice + q.slice / 32 : 0) +
-                           (q.biases ? q.slice / 32 + 2 * q.biases : 0));
+  const bool listed = tokens && history <= gws::LISTED;
+  int64_t least = 0;
+  for (int64_t blocks = ceil_div(q.slices, gws::MAX_LISTS); blocks < 2 * q.slices; blocks *= 2) {
+    const int64_t each = ceil_div(q.slices, blocks);
+    const int64_t slice = tokens && !listed ? 3 : 1, begin = tokens ? 3 : 1;
+    const int64_t cost = ceil_div(rows * ceil_div(q.slices, each), held) * (each * slice + begin);
+    if (q.each != 0 && cost >= least) continue;
+    least = cost;
+    q.each = static_cast<int>(each);
+    q.blocks = static_cast<int>(ceil_div(q.slices, each));
+  }
+  q.shift = 0;
+  while ((1 << q.shift) < q.slice) ++q.shift;
+  q.lists = listed && q.each > 1;
+  if (rows * q.blocks > kMaxDim) return GEMM_WS_ERR_INVALID_ARG;
+  const size_t smem = 4 * ((tokens ? 2 * q.slice + 2 * q.slice / 32 : 0) +
+                           (q.biases ? 2 * q.slice / 32 + 2 * q.biases : 0) + (q.lists ? gws::LISTED : 0));
   const bool fast = ml.wide() && mo.wide() && vocab % gws::GROUP == 0;
   DeviceGuard guard(h->device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
