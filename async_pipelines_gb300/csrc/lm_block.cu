@@ -24,15 +24,16 @@ static_assert(kPartialPerSm >= 2 * kMaxCols, "a block's partial sums fit its SM'
 int64_t partial_pitch(int64_t cols) { return ceil_div(cols, gws::GROUP) * gws::GROUP; }
 
 // The general path's teams: a warp for short rows, up to 8 of them a block, or a block whose
-// threads take up to four groups one after the other.
-Team any_team(const gemm_ws* h, int64_t rows, int64_t cols) {
+// threads take one group each where rows are few, and else `most` one after the other (8192 x 8191 bf16 forward
+// with four 191 us, with two 234; gradient of 2000 x 4001 104 and 82).
+Team any_team(const gemm_ws* h, int64_t rows, int64_t cols, int most) {
   const int64_t groups = ceil_div(cols, gws::GROUP);
   Team t = {32, 1, 1};
   if (groups <= 32) {
     t.rows = rows >= 8 * h->num_sms ? 8 : rows >= 2 * h->num_sms ? 4 : 1;
     return t;
   }
-  const int64_t threads = ceil_div(groups, rows >= 8 * h->num_sms ? 4 : 1);
+  const int64_t threads = ceil_div(groups, rows >= 8 * h->num_sms ? most : 1);
   t.threads = static_cast<int>(threads > gws::ANY_MOST ? gws::ANY_MOST : ceil_div(threads, 32) * 32);
   return t;
 }
@@ -91,7 +92,7 @@ int launch_block(gemm_ws* h, bool fast, gws::BlockParams& p, cudaStream_t s) {
     if (vpt)
       return launch(h, kernel, h->num_sms, gws::RING_THREADS, gws::RING_BYTES, s, p, q);
   }
-  const Team t = fast ? pick_team(h, p.rows, p.cols, gws::FAST, 1) : any_team(h, p.rows, p.cols);
+  const Team t = fast ? pick_team(h, p.rows, p.cols, gws::FAST, 1) : any_team(h, p.rows, p.cols, 4);
   p.team = t.threads;
   const int64_t blocks = ceil_div(p.rows, t.rows);
   if (!fast)
@@ -107,7 +108,7 @@ int launch_block(gemm_ws* h, bool fast, gws::BlockParams& p, cudaStream_t s) {
 
 template <typename T>
 int launch_quantize(gemm_ws* h, bool fast, gws::QuantizeParams& p, cudaStream_t s) {
-  const Team t = fast ? pick_team(h, p.rows, p.cols, gws::FAST, 1) : any_team(h, p.rows, p.cols);
+  const Team t = fast ? pick_team(h, p.rows, p.cols, gws::FAST, 1) : any_team(h, p.rows, p.cols, 4);
   p.team = t.threads;
   auto kernel = !fast        ? gws::quantize_rows_any_kernel<T>
                 : t.vpt == 1 ? gws::quantize_rows_kernel<T, 1, 1024>
@@ -170,7 +171,7 @@ int launch_grad(gemm_ws* h, bool fast, gws::BlockGradParams& p, gws::BlockSumsPa
       return finish(launch(h, kernel, h->num_sms, gws::RING_THREADS, gws::RING_BYTES, s, p, r), h->num_sms);
     }
   }
-  const Team t = fast ? grad_team(h, p.rows, p.cols) : any_team(h, p.rows, p.cols);
+  const Team t = fast ? grad_team(h, p.rows, p.cols) : any_team(h, p.rows, p.cols, 2);
   p.team = t.threads;
   auto kernel = !fast                          ? gws::block_norm_grad_any_kernel<T>
                 : t.vpt == 1                   ? gws::block_norm_grad_kernel<T, 1, 1024>

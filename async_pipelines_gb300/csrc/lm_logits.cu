@@ -34,7 +34,7 @@ int gemm_ws_adjust_logits(gemm_ws_t* h, int dtype, const void* logits, int64_t l
                           void* stream) {
   if (!h || dtype < GEMM_WS_BF16 || dtype > GEMM_WS_F32 ||
       (out_dtype != dtype && out_dtype != GEMM_WS_F32) || rows < 0 || rows > kMaxDim || vocab < 1 ||
-      vocab > kMaxDim - 4096 || history < 0 || history > kMaxDim || biases < 0 || biases > gws::MAX_BIASES)
+      vocab > kMaxDim - 4096 || history < 0 || history > kMaxDim - 8192 || biases < 0 || biases > gws::MAX_BIASES)
     return GEMM_WS_ERR_INVALID_ARG;
   if (rows == 0) return GEMM_WS_OK;
   if (history == 0) tokens = nullptr;

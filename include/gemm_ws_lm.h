@@ -245,7 +245,7 @@ int64_t gemm_ws_int8_matmul_workspace(gemm_ws_t* h, int64_t tokens, int64_t chan
  *    token outside [0, vocab) is left out, one given twice gets both, added in their order.
  *  - allowed: rows x ceil(vocab / 32) words, lda words between rows; token v is allowed iff
  *    bit v % 32 of word v / 32 is set. NULL: all are. A row may allow nothing.
- *  - 0 <= rows; 1 <= vocab < 2^31 - 4096; 0 <= history < 2^31. */
+ *  - 0 <= rows < 2^31; 1 <= vocab < 2^31 - 4096; 0 <= history < 2^31 - 8192. */
 int gemm_ws_adjust_logits(gemm_ws_t* h, int dtype, const void* logits, int64_t ldl, int out_dtype,
                           void* out, int64_t ldo, const void* tokens, int token_bytes, int64_t ldt,
                           int64_t history, const int32_t* lengths, const int32_t* prompt_lengths,
