@@ -174,9 +174,10 @@ struct Params {
   int w_stages, a_stages;         // of the two rings in shared memory
   int bufs;                       // w_bufs(bn)
   int tiles_m, tiles_n;           // tiles of tokens, of channels
-  int splits;                     // cuts of K; more than one only where all units run at once
-  int* total;                     // [tile][CTA of the pair][token][channel], zero at launch: the cuts' sums
-  uint32_t* arrived;              // [tile][CTA of the pair][epilogue warp], zero at launch
+  int whole;                      // tiles of their own; of those after them K is cut
+  int splits;                     // into so many units, all of which run at once
+  int* total;                     // [cut tile][CTA of the pair][token][channel], zero at launch: the cuts' sums
+  uint32_t* arrived;              // [cut tile][CTA of the pair][epilogue warp], zero at launch
   Output out;
   uint32_t* status;
   unsigned long long timeout_ns;
@@ -188,20 +189,25 @@ struct Params {
 // A unit of work: a tile, or a cut of its K.
 struct Unit {
   int n0, m0;      // first channel of the pair, first token
-  int tile, cut;
+  int cut_tile;    // the tile's number among those whose K is cut, or -1
   int s0, s1;      // stages of K
 };
 
 constexpr int GROUP_N = 8;   // tiles walk 8 tiles of channels down, then step on in the tokens (L2 reuse)
 
 __device__ __forceinline__ bool unit_of(const Params& p, int u, Unit& w) {
-  const int tiles = p.tiles_m * p.tiles_n;
-  if (u >= tiles * p.splits) return false;
-  const int t = p.splits > 1 ? u / p.splits : u;
-  w.tile = t;
-  w.cut = u - t * p.splits;
-  w.s0 = static_cast<int>(static_cast<int64_t>(w.cut) * p.stages / p.splits);
-  w.s1 = static_cast<int>(static_cast<int64_t>(w.cut + 1) * p.stages / p.splits);
+  int t = u;
+  w.cut_tile = -1;
+  w.s0 = 0;
+  w.s1 = p.stages;
+  if (u >= p.whole) {
+    w.cut_tile = (u - p.whole) / p.splits;
+    t = p.whole + w.cut_tile;
+    if (t >= p.tiles_m * p.tiles_n) return false;
+    const int cut = u - p.whole - w.cut_tile * p.splits;
+    w.s0 = static_cast<int>(static_cast<int64_t>(cut) * p.stages / p.splits);
+    w.s1 = static_cast<int>(static_cast<int64_t>(cut + 1) * p.stages / p.splits);
+  }
   const int group = t / (GROUP_N * p.tiles_m), first = group * GROUP_N;
   const int r = t - group * GROUP_N * p.tiles_m;
   const int high = min(GROUP_N, p.tiles_n - first);
@@ -513,10 +519,10 @@ __device__ __forceinline__ void epilogue(const Params& p, uint32_t sbase, uint8_
           mbar_arrive_cluster_relaxed(mapa_shared(e, 0));
       }
     }
-    if (p.splits > 1) {
+    if (w.cut_tile >= 0) {
       // The cuts' sums meet in the workspace, which is zero at launch: integers, so in any order.
       // The warp that arrives last takes what is there.
-      const int64_t which = static_cast<int64_t>(w.tile) * 2 + rank;
+      const int64_t which = static_cast<int64_t>(w.cut_tile) * 2 + rank;
       int* total = p.total + (which * p.bn + col0) * BM + in_cta;
 #pragma unroll
       for (int k = 0; k < BLOCKS; ++k) {
@@ -590,12 +596,13 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
   tc_fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   const Watchdog wd{abort_flag, p.status, p.timeout_ns};
-  // The set-up above overlaps the previous kernel's end; nothing below does.
-  grid_dependency_wait();
+  // The set-up above, and w's way into tensor memory, overlap the end of the kernel that writes the tokens in
+  // fp16: that one has waited for everything before it, and does not touch w. Who needs its results waits.
   if (threadIdx.x == 0) grid_launch_dependents();
 
   if (warp >= WARP_EPI0) {
     more_registers<REGS_EPI>();
+    grid_dependency_wait();
     epilogue(p, sbase, smem, tmem, rank, warp, wd);
   } else {
     fewer_registers<REGS_FEW>();
@@ -604,6 +611,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
     } else if (warp == WARP_W) {
       if (lane == 0) produce_w(p, sbase, rank, wd);
     } else if (warp == WARP_A) {
+      grid_dependency_wait();
       if (lane == 0) produce_a(p, sbase, rank, wd);
     } else if (warp == WARP_TELL) {
       tell(p, sbase, wd);
