@@ -1,5 +1,6 @@
 // Host side of the product of 8-bit integers (include/gemm_ws_lm.h): argument checks, the
 // plan and the launches.
+#include <atomic>
 #include <cstring>
 
 #include "lm_host.cuh"
@@ -109,12 +110,12 @@ bool encode(gemm_ws* h, CUtensorMap* m, const void* ptr, bool half, int64_t inne
 // Whether the product kernel has the registers at launch that its warpgroups share out: with fewer
 // they would wait for each other forever. (A property of the built kernel.)
 bool registers_as_planned() {
-  static bool seen = false;
-  if (seen) return true;
+  static std::atomic<bool> seen{false};   // handles may be used by several threads
+  if (seen.load(std::memory_order_relaxed)) return true;
   cudaFuncAttributes a;
-  if (cudaFuncGetAttributes(&a, i8::product_kernel) != cudaSuccess) return false;
-  seen = a.numRegs == i8::REGS_LAUNCH;
-  return seen;
+  if (cudaFuncGetAttributes(&a, i8::product_kernel) != cudaSuccess || a.numRegs != i8::REGS_LAUNCH) return false;
+  seen.store(true, std::memory_order_relaxed);
+  return true;
 }
 
 int launch_product(gemm_ws* h, const Plan& q, const i8::Params& p, cudaStream_t s) {

@@ -63,7 +63,9 @@ __device__ __forceinline__ uint4 load16(const int8_t* row, int at, int k, bool w
 }
 
 // TOKENS rows of a (from blockIdx.y * TOKENS on) against all of w, by the integer dot products of
-// the CUDA cores. `split` warps share DOT_ROWS channels, 16 bytes of K a lane and step.
+// the CUDA cores. `split` warps share DOT_ROWS channels, 16 bytes of K a lane and step: four rows of w at a
+// time are enough bytes in flight, and a lane's 16 bytes of each token serve all four. Bound by w's bytes
+// (one token x 4096 over 131072: 82 us, 6.5 TB/s; four 102).
 template <int TOKENS>
 __global__ void __launch_bounds__(DOT_THREADS) dot_kernel(const __grid_constant__ DotParams p) {
   __shared__ int box[DOT_WARPS][DOT_ROWS * TOKENS];
@@ -124,13 +126,19 @@ __global__ void __launch_bounds__(DOT_THREADS) dot_kernel(const __grid_constant_
 //
 // A pair of CTAs has a tile of 256 channels x bn tokens, each its 128 channels as
 // TMEM lanes. Tensor memory: two accumulators of bn columns, up to 160, and in what is left of its 512
-// columns buffers of w, 128 x 128 in 64 columns each: three to seven. From a buffer's hand-over until it is
-// seen free again pass about 1500 cycles (both CTAs' warps, the MMAs, and the way between
-// the CTAs), which is why there have to be several.
+// columns buffers of w, 128 x 128 in 64 columns each: three to seven. A buffer's way from its hand-over
+// until it is seen free again (both CTAs' warps, the MMAs, and between the CTAs) takes the time of
+// two stages' MMAs, which is why there have to be several.
 //
 // One warp issues all MMAs, and what it does beside that has to fit into their time: for 128 of K it
-// polls both operands at once and commits once, to w's buffer. That the tokens' stage of the same step
+// polls the two operands' barriers and commits once, to w's buffer. That the tokens' stage of the same step
 // is free again a warp of its own tells on, when it sees w's buffer free.
+//
+// Times in a graph: 8192 x 8192 over 8192 653 us (1.68 P operations a second, 0.87 of a bf16 product's
+// rate; from 645 to 680 between chips), bound by how fast w's stages get into tensor memory, some 800 cycles
+// a stage against some 720 of its MMAs. 64 x 4096 over 131072 103 us (w at 5.2 TB/s). Small products are bound by
+// what comes one after the other: 64 x 4096 over 4096 takes 16 us, of which the tokens' kernel 3, set-up
+// and first loads 3.5, a joined cut's end 2.5.
 
 constexpr int BM = 128;              // channels of a CTA's tile
 constexpr int BN_MAX = 160;          // tokens of a tile, at most
@@ -387,7 +395,7 @@ __device__ __forceinline__ void issue(const Params& p, uint32_t sbase, uint32_t 
     for (int first = w.s0; first < w.s1; first += CUT_STAGES, ++handed) {
       const uint32_t b = handed & 1;
       if (mine && ok) {
-        ok = wait_inline<false>(bar(BAR_ACC_EMPTY + b), ((handed >> 1) & 1) ^ 1, wd);
+        ok = wait_inline(bar(BAR_ACC_EMPTY + b), ((handed >> 1) & 1) ^ 1, wd);
         tc_fence_after_sync();
       }
       const uint32_t d = tmem + b * p.bn;
@@ -395,8 +403,8 @@ __device__ __forceinline__ void issue(const Params& p, uint32_t sbase, uint32_t 
       for (int st = first; st < end; ++st) {
         const uint32_t b_addr = ring + s * bytes, from = tmem + ACC_BUFS * p.bn + t * W_COLS;
         if (mine && ok) {
-          ok = wait_inline<false>(bar(BAR_A_FULL + s), ph, wd) &&
-               wait_inline<false>(bar(BAR_T_FULL + t), tph, wd);
+          ok = wait_inline(bar(BAR_A_FULL + s), ph, wd) &&
+               wait_inline(bar(BAR_T_FULL + t), tph, wd);
           if (ok) {
             tc_fence_after_sync();
 #pragma unroll
@@ -644,6 +652,8 @@ struct ExpandParams {
 
 constexpr int EXPAND_THREADS = 256;
 
+// 16 of K a thread, which are one load and two stores; bound by memory where tokens are many (8192 x 8192 within
+// the product's 653 us: 201 MB), by its launch where they are few (3 us).
 __global__ void __launch_bounds__(EXPAND_THREADS) expand_kernel(const __grid_constant__ ExpandParams p) {
   grid_dependency_wait();
   grid_launch_dependents();

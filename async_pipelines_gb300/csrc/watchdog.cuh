@@ -171,10 +171,9 @@ __device__ __forceinline__ bool wait_suspended(uint32_t bar, uint32_t parity, co
   return true;
 }
 // By one thread whose wake-up counts: it polls.
-template <bool kCluster>
 __device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, const Watchdog& wd) {
   uint64_t t0 = 0;
-  for (uint32_t it = 1; !(kCluster ? mbar_test_wait_cluster(bar, parity) : mbar_test_wait(bar, parity)); ++it)
+  for (uint32_t it = 1; !mbar_test_wait(bar, parity); ++it)
     if ((it & 255) == 0 && wait_over(t0, wd)) return false;
   return true;
 }
