@@ -6,12 +6,11 @@
 #include "lm_logits_kernel.cuh"
 
 static_assert((gws::LOGIT_STEP & (gws::LOGIT_STEP - 1)) == 0 && (gws::LOGIT_GROUPS & (gws::LOGIT_GROUPS - 1)) == 0,
-              "slices are powers of two");
+              "slices are powers of two, and so slots");
 
 namespace {
 
-constexpr size_t kSmemMost = 4 * (2 * gws::LOGIT_SLICE + 4 * gws::LOGIT_SLICE / 32 + 2 * gws::MAX_BIASES +
-                                   gws::LISTED);
+constexpr size_t kSmemMost = 8 * (gws::MAX_SLOTS + gws::MAX_BIASES);
 
 template <typename T, typename U>
 int launch_logits(gemm_ws* h, bool fast, size_t smem, const gws::LogitParams& p, cudaStream_t s) {
@@ -86,32 +85,36 @@ int gemm_ws_adjust_logits(gemm_ws_t* h, int dtype, const void* logits, int64_t l
   q.allowed = allowed;
   q.lda = lda;
   // Slices as long as they may be, but short enough that few rows still reach all SMs. Then as many of
-  // them a block as leave the least work to the slowest SM, which holds two blocks: a block begins with
-  // loads that wait for each other, which takes as long as about three slices, and where the
-  // history does not fit the lists that is so for each slice.
-  const int64_t steps = ceil_div(vocab, gws::LOGIT_STEP), held = 2 * h->num_sms;
+  // them a block as cost least: memory is shared, so the time is that of all blocks' slices and begins by the
+  // blocks held at once, but not less than one block's. What a block does for a history takes as long as
+  // three slices, for biases alone half of one (256 rows of 131072 fp32 with 2048 tokens of history: 8 slices a
+  // block 60 us, 16 70, 4 62; with biases alone 47, 63 and 48; 32 rows bf16: 4 slices 5.0, 8 6.6).
+  // With a history too long for a hash table it is one slice.
+  const int64_t steps = ceil_div(vocab, gws::LOGIT_STEP), held = gws::LOGIT_HELD * h->num_sms;
   int64_t per = gws::LOGIT_GROUPS;
   const int64_t spread = ceil_div(steps * rows, held);
-  if (per > spread) per = spread;
+  while (per > 1 && per > spread) per /= 2;
   q.slice = static_cast<int>(per * gws::LOGIT_STEP);
   q.slices = static_cast<int>(ceil_div(vocab, q.slice));
-  const bool listed = tokens && history <= gws::LISTED;
+  q.blocks = q.slices;
+  q.each = 1;
+  const int64_t begin = tokens ? 12 : bias_tokens ? 2 : 1;   // quarters of a slice
   int64_t least = 0;
-  for (int64_t blocks = ceil_div(q.slices, gws::MAX_LISTS); blocks < 2 * q.slices; blocks *= 2) {
-    const int64_t each = ceil_div(q.slices, blocks);
-    const int64_t slice = tokens && !listed ? 3 : 1, begin = tokens ? 3 : 1;
-    const int64_t cost = ceil_div(rows * ceil_div(q.slices, each), held) * (each * slice + begin);
-    if (q.each != 0 && cost >= least) continue;
-    least = cost;
-    q.each = static_cast<int>(each);
-    q.blocks = static_cast<int>(ceil_div(q.slices, each));
-  }
-  q.shift = 0;
-  while ((1 << q.shift) < q.slice) ++q.shift;
-  q.lists = listed && q.each > 1;
+  if (history <= gws::LISTED)
+    for (int64_t blocks = 1; blocks < 2 * q.slices; blocks *= 2) {
+      const int64_t each = ceil_div(q.slices, blocks), there = ceil_div(q.slices, each);
+      const int64_t cost = (rows * there > held ? rows * there : held) * (4 * each + begin);
+      if (least != 0 && cost >= least) continue;
+      least = cost;
+      q.each = static_cast<int>(each);
+      q.blocks = static_cast<int>(there);
+    }
   if (rows * q.blocks > kMaxDim) return GEMM_WS_ERR_INVALID_ARG;
-  const size_t smem = 4 * ((tokens ? 2 * q.slice + 2 * q.slice / 32 : 0) +
-                           (q.biases ? 2 * q.slice / 32 + 2 * q.biases : 0) + (q.lists ? gws::LISTED : 0));
+  q.slots = 64;
+  while (q.slots < gws::MAX_SLOTS && q.slots < 2 * (history + q.biases)) q.slots *= 2;
+  q.hashed = q.each > 1 || q.slots < q.slice;
+  if (!q.hashed) q.slots = q.slice;
+  const size_t smem = 8 * (tokens || q.biases ? q.slots + q.biases : 0);
   const bool fast = ml.wide() && mo.wide() && vocab % gws::GROUP == 0;
   DeviceGuard guard(h->device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -6,16 +6,14 @@
 //   z = z - (frequency * c + presence * [c > 0]) + the sum of v's biases
 //   v is not allowed:                 z = -inf
 //
-// A block takes some slices of a row's vocabulary, one after the other, and counts in shared memory
-// what of the history lies in each. The counts are not cleared beforehand, which would take as many
-// accesses as the logits themselves: a bit for each token says whether its count
-// means anything, and only the counts of tokens that occur are set to zero first. The next slice's
-// logits are loaded, and its counts taken, around this one's arithmetic. A history of up to 4096 tokens is
-// first put into lists by slices, so that a slice's counts cost what lies in it; a longer one is read
-// again for each slice. (256 rows of 131072 fp32 and a history of 2048: one slice a block, the history
-// read for each, 88 us; several slices a block, each looking through the whole history, 92; as it is 82,
-// 3.3 TB/s: the counts and their barriers leave memory waiting, without penalties it is 68 and without biases
-// too 54.)
+// A block takes some slices of a row's vocabulary. What of the history and the biases lies in them it counts
+// in a table in shared memory; the logits stream past that with nothing but the mask applied,
+// and without a barrier; then the table's few tokens are computed from the logits once more and
+// put over what the stream wrote. A history of up to 4096 tokens has a hash table of at least twice its tokens, so
+// that a block may take many slices for one look at the history; a longer one is
+// counted at its tokens' places in one slice. 256 rows of 131072 fp32 with a history of 2048: 60 us, 4.6 TB/s
+// (biases alone 47, 5.8); the counting is latency that other blocks' streams cover in part. With counts looked up at
+// each group of the stream, and so a barrier a slice, it was 82. Blocks of 256 threads, four an SM: 69.
 #pragma once
 
 #include <stdint.h>
@@ -24,15 +22,18 @@
 
 namespace gws {
 
-constexpr int LOGIT_THREADS = 512;
+constexpr int LOGIT_THREADS = 512, LOGIT_HELD = 2;   // of a block; blocks of an SM
 constexpr int LOGIT_STEP = LOGIT_THREADS * GROUP;   // tokens that a block's threads take at once
 constexpr int LOGIT_GROUPS = 2;                     // groups of a thread in a slice, at most
 constexpr int LOGIT_SLICE = LOGIT_GROUPS * LOGIT_STEP;
 constexpr int MAX_BIASES = 1024;                    // of a row
 constexpr int TOKENS_AHEAD = 8;                     // tokens of the history that a thread loads at once
-constexpr int LISTED = TOKENS_AHEAD * LOGIT_THREADS;
-constexpr int MAX_LISTS = 64;                       // slices of a block, at most
-constexpr uint32_t SEEN = 1u << 31;                 // a count's top bit: the token stands in the prompt
+constexpr int ROUND = TOKENS_AHEAD * LOGIT_THREADS; // of the block
+constexpr int LISTED = 4096;                        // tokens of a history with a hash table
+constexpr int MAX_SLOTS = 8192;                     // of a table
+static_assert(LISTED + MAX_BIASES < MAX_SLOTS, "a search for a token meets an empty slot");
+constexpr uint32_t TOP = 1u << 31;                  // of a count: the token stands in the prompt; of a key: it has biases
+constexpr uint32_t EMPTY = TOP - 1;                 // no token: vocabularies are smaller
 
 struct LogitParams {
   const void* logits;
@@ -41,9 +42,9 @@ struct LogitParams {
   int64_t rows;
   int vocab;
   int slice, slices;                 // tokens of a slice, a multiple of LOGIT_STEP up to LOGIT_SLICE; slices of a row
-  int shift;                         // slice is 1 << shift
-  int each, blocks;                  // slices of a block, at most MAX_LISTS; blocks of a row
-  int lists;                         // the history is put into lists first: more than one slice, up to LISTED tokens
+  int each, blocks;                  // slices of a block; blocks of a row
+  int slots;                         // of the table, a power of two
+  int hashed;                        // tokens anywhere in the table; else each at its place in the block's one slice
   const void* tokens;                // rows x history, or NULL
   int64_t ldt;
   int wide_tokens;                   // int64, else int32
@@ -65,19 +66,11 @@ __device__ __forceinline__ int64_t token_at(const void* p, int wide, int64_t i) 
 
 // T: the logits' type; U: the output's.
 template <typename T, typename U, Path PATH>
-__global__ void __launch_bounds__(LOGIT_THREADS, 2) adjust_logits_kernel(const __grid_constant__ LogitParams p) {
+__global__ void __launch_bounds__(LOGIT_THREADS, LOGIT_HELD) adjust_logits_kernel(const __grid_constant__ LogitParams p) {
   extern __shared__ __align__(16) uint32_t logit_smem[];
   constexpr bool WHOLE = PATH != ANY;
-  // Twice each: counts, the bits that say which of them mean something, and the tokens with biases; and the
-  // row's biases.
-  const int words = p.slice / 32;
-  uint32_t* const counts = logit_smem;
-  uint32_t* const knowns = counts + (p.tokens ? 2 * p.slice : 0);
-  uint32_t* const biaseds = knowns + (p.tokens ? 2 * words : 0);
-  int* const bias_at = reinterpret_cast<int*>(biaseds + (p.biases ? 2 * words : 0));
-  float* const bias_value = reinterpret_cast<float*>(bias_at + p.biases);
-  uint32_t* const list = reinterpret_cast<uint32_t*>(bias_value + p.biases);
-  __shared__ int list_at[MAX_LISTS + 1], list_size[MAX_LISTS];
+  uint32_t *const keys = logit_smem, *const counts = keys + p.slots;
+  uint2* const biases = reinterpret_cast<uint2*>(counts + p.slots);   // token and value
   grid_dependency_wait();
   grid_launch_dependents();
   const int64_t row = blockIdx.x / p.blocks;
@@ -88,9 +81,6 @@ __global__ void __launch_bounds__(LOGIT_THREADS, 2) adjust_logits_kernel(const _
     const int at = k * LOGIT_STEP + static_cast<int>(threadIdx.x) * GROUP;
     return at < p.slice && at < p.vocab - slice * p.slice ? slice * p.slice + at : p.vocab;
   };
-  // a token's place in the slice that begins at `base`, where it is below p.slice; no token is -1
-  auto local = [](int token, int base) { return static_cast<uint32_t>(token) - static_cast<uint32_t>(base); };
-  const uint32_t width = p.slice;
   Raw<T> raw[LOGIT_GROUPS] = {};
   uint32_t bits[LOGIT_GROUPS];
   auto load_logits = [&](int slice) {
@@ -104,124 +94,79 @@ __global__ void __launch_bounds__(LOGIT_THREADS, 2) adjust_logits_kernel(const _
       }
     }
   };
-  // A round of the history: this thread's tokens, -1 for what does not count.
-  int length = 0, prompt = 0;
-  int token[TOKENS_AHEAD];
-  auto load_tokens = [&](int base) {
-    int64_t t[TOKENS_AHEAD];
+  int length = 0;
+  if (p.tokens) length = p.lengths ? min(max(p.lengths[row], 0), p.history) : p.history;
+  const bool counted = length > 0 || p.biases > 0;
+  // A round of the history, and of the biases, is on its way while the table is cleared.
+  int64_t t[TOKENS_AHEAD];
+  auto load_tokens = [&](int r) {
 #pragma unroll
     for (int j = 0; j < TOKENS_AHEAD; ++j) {
-      const int i = base + j * LOGIT_THREADS + static_cast<int>(threadIdx.x);
+      const int i = r + j * LOGIT_THREADS + static_cast<int>(threadIdx.x);
       t[j] = i < length ? token_at(p.tokens, p.wide_tokens, row * p.ldt + i) : -1;
     }
-#pragma unroll
-    for (int j = 0; j < TOKENS_AHEAD; ++j) token[j] = t[j] >= 0 && t[j] < p.vocab ? static_cast<int>(t[j]) : -1;
   };
-  load_logits(first);
+  int64_t bias = -1;
+  float value = 0.0f;
+  auto load_bias = [&](int i) {
+    if (i < p.biases) {
+      bias = token_at(p.bias_tokens, p.wide_biases, row * p.ldb + i);
+      value = p.bias_values[row * p.ldv + i];
+    }
+  };
+  int prompt = 0;
   float rep = 1.0f, freq = 0.0f, pres = 0.0f;
-  constexpr int ROUND = TOKENS_AHEAD * LOGIT_THREADS;
-  int rounds = 0;
   if (p.tokens) {
-    length = p.lengths ? min(max(p.lengths[row], 0), p.history) : p.history;
-    prompt = p.prompts ? p.prompts[row] : 0;
+    if (p.prompts) prompt = p.prompts[row];
     if (p.repetition) rep = p.repetition[row];
     if (p.frequency) freq = p.frequency[row];
     if (p.presence) pres = p.presence[row];
-    rounds = (length + ROUND - 1) / ROUND;
-    if (rounds == 1) load_tokens(0);
   }
-  for (int i = threadIdx.x; i < p.biases; i += LOGIT_THREADS) {
-    const int64_t t = token_at(p.bias_tokens, p.wide_biases, row * p.ldb + i);
-    bias_at[i] = t >= 0 && t < p.vocab ? static_cast<int>(t) : -1;
-    bias_value[i] = p.bias_values[row * p.ldv + i];
-  }
-  const bool counted = rounds > 0 || p.biases > 0;
-  const bool lists = p.lists && rounds > 0;
-  if (lists) {
-    // Each token's place in its slice's list; the lists' begins; the lists.
-    for (int i = threadIdx.x; i < MAX_LISTS; i += LOGIT_THREADS) list_size[i] = 0;
-    __syncthreads();
-    int rank[TOKENS_AHEAD];
-    const uint32_t from = static_cast<uint32_t>(first) << p.shift, span = static_cast<uint32_t>(last - first) << p.shift;
-#pragma unroll
-    for (int j = 0; j < TOKENS_AHEAD; ++j) {
-      const uint32_t at = static_cast<uint32_t>(token[j]) - from;
-      rank[j] = token[j] >= 0 && at < span ? atomicAdd(list_size + (at >> p.shift), 1) : -1;
+  const uint32_t base = static_cast<uint32_t>(first) * static_cast<uint32_t>(p.slice);
+  if (counted) {
+    load_tokens(0);
+    load_bias(threadIdx.x);
+    const uint32_t none = p.hashed ? EMPTY : 0;
+    for (int i = threadIdx.x; i < p.slots; i += LOGIT_THREADS) {
+      keys[i] = none;
+      counts[i] = 0;
     }
-    __syncthreads();
-    if (threadIdx.x < 32) {
-      const int a = list_size[2 * threadIdx.x], b = list_size[2 * threadIdx.x + 1];
-      int sum = a + b;
-#pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const int left = __shfl_up_sync(0xffffffffu, sum, o);
-        if (static_cast<int>(threadIdx.x) >= o) sum += left;
+    // The block's tokens are `span` from `base` on.
+    const uint32_t width = static_cast<uint32_t>(p.slice) * static_cast<uint32_t>(last - first);
+    const uint32_t span = min(width, static_cast<uint32_t>(p.vocab) - base);
+    // A token's slot. Every block has more slots than tokens to put there.
+    auto slot_of = [&](uint32_t token) {
+      if (!p.hashed) return token - base;
+      const uint32_t mask = p.slots - 1;
+      uint32_t at = (token * 2654435761u >> 16) & mask;   // Knuth's multiplicative hash
+      for (uint32_t i = 0; i < mask; ++i, at = (at + 1) & mask) {
+        const uint32_t was = atomicCAS(keys + at, EMPTY, token);
+        if (was == EMPTY || (was & ~TOP) == token) break;
       }
-      list_at[2 * threadIdx.x] = sum - a - b;
-      list_at[2 * threadIdx.x + 1] = sum - b;
-      if (threadIdx.x == 31) list_at[MAX_LISTS] = sum;
-    }
+      return at;
+    };
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < TOKENS_AHEAD; ++j) {
-      if (rank[j] < 0) continue;
-      const uint32_t at = static_cast<uint32_t>(token[j]) - from;
-      const bool of_prompt = j * LOGIT_THREADS + static_cast<int>(threadIdx.x) < prompt;
-      list[list_at[at >> p.shift] + rank[j]] = (at & (width - 1)) | (of_prompt ? SEEN : 0);
-    }
-    __syncthreads();
-  }
-  // f(place, whether it is of the prompt) for the history's tokens in a slice.
-  auto each_token = [&](int slice, auto f) {
-    if (lists) {
-      const int end = list_at[slice - first + 1];
-      for (int i = list_at[slice - first] + threadIdx.x; i < end; i += LOGIT_THREADS)
-        f(list[i] & ~SEEN, (list[i] & SEEN) != 0);
-      return;
-    }
-    const int base = slice << p.shift;
-    for (int r = 0; r < rounds; ++r) {
-      if (rounds > 1) load_tokens(r * ROUND);
-      const int left = length - r * ROUND;
+    for (int r = 0; r < length; r += ROUND) {
+      if (r > 0) load_tokens(r);
 #pragma unroll
       for (int j = 0; j < TOKENS_AHEAD; ++j) {
-        if (j * LOGIT_THREADS >= left) break;
-        const uint32_t at = local(token[j], base);
-        if (at < width) f(at, r * ROUND + j * LOGIT_THREADS + static_cast<int>(threadIdx.x) < prompt);
+        if (t[j] < base || t[j] - base >= span) continue;
+        uint32_t* count = counts + slot_of(static_cast<uint32_t>(t[j]));
+        if (r + j * LOGIT_THREADS + static_cast<int>(threadIdx.x) < prompt)
+          atomicOr(count, TOP);
+        else
+          atomicAdd(count, 1u);
       }
     }
-  };
-  // What a slice's counts need before they can be taken.
-  auto clear = [&](int slice) {
-    const int b = slice & 1;
-    if (p.tokens)
-      for (int i = threadIdx.x; i < words; i += LOGIT_THREADS) knowns[b * words + i] = 0;
-    if (p.biases)
-      for (int i = threadIdx.x; i < words; i += LOGIT_THREADS) biaseds[b * words + i] = 0;
-    uint32_t* count = counts + b * p.slice;
-    each_token(slice, [&](uint32_t at, bool) { count[at] = 0; });
-  };
-  auto take = [&](int slice) {
-    const int b = slice & 1;
-    uint32_t *count = counts + b * p.slice, *known = knowns + b * words, *biased = biaseds + b * words;
-    each_token(slice, [&](uint32_t at, bool of_prompt) {
-      if (of_prompt)
-        atomicOr(count + at, SEEN);
-      else
-        atomicAdd(count + at, 1u);
-      atomicOr(known + at / 32, 1u << (at % 32));
-    });
     for (int i = threadIdx.x; i < p.biases; i += LOGIT_THREADS) {
-      const uint32_t at = local(bias_at[i], slice * p.slice);
-      if (at < width) atomicOr(biased + at / 32, 1u << (at % 32));
+      if (i >= LOGIT_THREADS) load_bias(i);
+      const bool mine = bias >= base && bias - base < span;
+      biases[i] = make_uint2(mine ? static_cast<uint32_t>(bias) : ~0u, __float_as_uint(value));
+      if (mine) atomicOr(keys + slot_of(static_cast<uint32_t>(bias)), TOP);
     }
-  };
-  if (counted) {
-    clear(first);
-    __syncthreads();
-    take(first);
   }
   U* out = static_cast<U*>(p.out) + row * p.ldo;
+  load_logits(first);
   for (int slice = first; slice < last; ++slice) {
     Raw<T> now[LOGIT_GROUPS];
     uint32_t may[LOGIT_GROUPS];
@@ -231,56 +176,56 @@ __global__ void __launch_bounds__(LOGIT_THREADS, 2) adjust_logits_kernel(const _
       may[k] = bits[k];
     }
     if (slice + 1 < last) load_logits(slice + 1);
-    if (counted) {
-      if (slice + 1 < last) clear(slice + 1);
-      __syncthreads();
-    }
-    const int b = slice & 1;
-    const uint32_t *count = counts + b * p.slice, *known = knowns + b * words, *biased = biaseds + b * words;
 #pragma unroll
     for (int k = 0; k < LOGIT_GROUPS; ++k) {
       if (k * LOGIT_STEP >= p.slice) break;
-      const int c = column(slice, k), c0 = c - slice * p.slice;
-      const bool mine = c < p.vocab;
-      uint32_t seen = 0, plus = 0;
-      if (mine) {
-        if (rounds > 0) seen = known[c0 / 32] >> (c0 % 32) & 0xFF;
-        if (p.biases) plus = biased[c0 / 32] >> (c0 % 32) & 0xFF;
-      }
+      const int c = column(slice, k);
       float z[GROUP];
       unpack(now[k], z);
-      // One token after the other, in a loop that is rarely entered.
-#pragma unroll 1
-      for (uint32_t left = seen | plus; left; left &= left - 1) {
-        const int i = __ffs(left) - 1;
-        float v = 0.0f;
+      const uint32_t mask = may[k] >> (c % 32);
 #pragma unroll
-        for (int j = 0; j < GROUP; ++j) v = j == i ? z[j] : v;
-        if (seen >> i & 1) {
-          const uint32_t n = count[c0 + i];
-          v = v > 0.0f ? v / rep : v * rep;
-          if (n & ~SEEN) v -= fmaf(freq, static_cast<float>(n & ~SEEN), pres);
-        }
-        if (plus >> i & 1) {
-          float add = 0.0f;
-          for (int j = 0; j < p.biases; ++j)
-            if (bias_at[j] == c + i) add += bias_value[j];
-          v += add;
-        }
-#pragma unroll
-        for (int j = 0; j < GROUP; ++j) z[j] = j == i ? v : z[j];
-      }
-      if (p.allowed) {
-        const uint32_t mask = may[k] >> (c % 32);
-#pragma unroll
-        for (int i = 0; i < GROUP; ++i) z[i] = mask & 1u << i ? z[i] : -INFINITY;
-      }
-      if (PATH == ANY || mine)
+      for (int i = 0; i < GROUP; ++i) z[i] = mask & 1u << i ? z[i] : -INFINITY;
+      if (PATH == ANY || c < p.vocab)
         store_group<WHOLE>(out, c, p.vocab, threadIdx.x, LOGIT_THREADS, pack<U>(z));
     }
-    if (counted && slice + 1 < last) {
-      take(slice + 1);
-      __syncthreads();   // this slice's counts have been read
+  }
+  if (!counted) return;
+  __syncthreads();   // the table is complete, and what follows is written over what the stream wrote
+  constexpr int AT_ONCE = 4;
+  for (int i0 = threadIdx.x; i0 < p.slots; i0 += AT_ONCE * LOGIT_THREADS) {
+    uint32_t n[AT_ONCE], may[AT_ONCE];
+    int c[AT_ONCE];
+    bool biased[AT_ONCE];
+    T z[AT_ONCE];
+#pragma unroll
+    for (int j = 0; j < AT_ONCE; ++j) {
+      const int i = i0 + j * LOGIT_THREADS;
+      n[j] = may[j] = 0;
+      if (i >= p.slots) continue;
+      const uint32_t key = keys[i];
+      n[j] = counts[i];
+      biased[j] = key & TOP;
+      if (n[j] == 0 && !biased[j]) continue;
+      c[j] = static_cast<int>(p.hashed ? key & ~TOP : base + i);
+      may[j] = p.allowed ? p.allowed[row * p.lda + c[j] / 32] >> (c[j] % 32) & 1 : 1;
+      z[j] = in.at[c[j]];   // where out is the logits, the stream has left what is allowed as it was
+    }
+#pragma unroll
+    for (int j = 0; j < AT_ONCE; ++j) {
+      if (!may[j]) continue;
+      float v = to_float(z[j]);
+      if (n[j] != 0) v = v > 0.0f ? v / rep : v * rep;
+      if (n[j] & ~TOP) v -= fmaf(freq, static_cast<float>(n[j] & ~TOP), pres);
+      if (biased[j]) {
+        float add = 0.0f;
+#pragma unroll 8
+        for (int k = 0; k < p.biases; ++k) {
+          const uint2 b = biases[k];
+          add += b.x == static_cast<uint32_t>(c[j]) ? __uint_as_float(b.y) : 0.0f;
+        }
+        v += add;
+      }
+      out[c[j]] = round_to(v, U());
     }
   }
 }

@@ -241,3 +241,43 @@ def test_one_matrix_of_lists_for_all_rows_and_odd_lengths(g, rows, vocab):
     off = (out - plain).abs()
     off[:, 3] -= 2.0 ** -22 * (logits[:, 3].abs() + 300.0 * freq)   # two roundings of at most 2^-24 each
     assert float(off.max()) <= 0.0
+
+
+@gpu
+@pytest.mark.parametrize("dtype,out_type", [(F32, F32), (BF16, F32), (BF16, BF16)])
+@pytest.mark.parametrize("rows,vocab,history,biases", [(400, 20000, 4096, 1024), (2, 6000, 4096, 1024), (700, 70001, 4096, 1024),
+                                                       (700, 30000, 4097, 1024), (700, 30000, 0, 1024), (900, 16400, 31, 1)])
+def test_the_fullest_tables(g, dtype, out_type, rows, vocab, history, biases):
+    """All tokens of the history and all with biases different."""
+    gen = torch.Generator().manual_seed(8)
+    logits = values(gen, rows, vocab, dtype=dtype)
+    order = torch.randperm(vocab, generator=gen)
+    order = order.repeat(1 + (history + biases) // vocab)[:history + biases].repeat(rows, 1)
+    order = ((order + torch.arange(rows)[:, None]) % vocab).cuda()
+    tokens, at = order[:, :history], order[:, history:]
+    value = torch.randn(rows, biases, generator=gen).cuda()
+    rep, freq = 0.5 + torch.rand(rows, generator=gen).cuda(), torch.rand(rows, generator=gen).cuda()
+    out = torch.empty(rows, vocab, dtype=out_type, device="cuda")
+    penalties = dict(tokens=tokens, repetition=rep, frequency=freq) if history else {}
+    g.adjust_logits(logits, out, bias_tokens=at, bias_values=value, **penalties)
+    z = logits.double()
+    size = z.abs()
+    if history:
+        count = torch.zeros(rows, vocab, device="cuda").scatter_add_(1, tokens, torch.ones(rows, history, device="cuda"))
+        r64 = rep.double()[:, None]
+        z = torch.where(count > 0, torch.where(z > 0, z / r64, z * r64), z)
+        z = z - freq.double()[:, None] * count
+        size = size * torch.clamp(torch.maximum(r64, 1 / r64), min=1.0) + freq.double()[:, None] * count
+    plus = torch.zeros(rows, vocab, dtype=torch.float64, device="cuda").scatter_add_(1, at, value.double())
+    most = torch.zeros(rows, vocab, dtype=torch.float64, device="cuda").scatter_add_(1, at, value.double().abs())
+    z = z + plus
+    # five roundings to 32 bits of at most 2^-24 of the magnitudes, and the output's own
+    unit = {F32: 2.0 ** -24, BF16: 2.0 ** -8}[out_type]
+    tol = unit * z.abs() + 2.0 ** -21 * (size + most) + 1e-30
+    off = (out.double() - z).abs()
+    assert bool((off <= tol).all()), f"worst {float((off / tol).max()):.3g} of the tolerance"
+    inplace = logits.clone()
+    if out_type is dtype:
+        g.adjust_logits(inplace, inplace, bias_tokens=at, bias_values=value, **penalties)
+        assert torch.equal(inplace, out)
+    assert g.query_status() == gemm_ws.OK
