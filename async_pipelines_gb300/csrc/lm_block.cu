@@ -171,16 +171,21 @@ int launch_grad(gemm_ws* h, bool fast, gws::BlockGradParams& p, gws::BlockSumsPa
       return finish(launch(h, kernel, h->num_sms, gws::RING_THREADS, gws::RING_BYTES, s, p, r), h->num_sms);
     }
   }
-  const Team t = fast ? grad_team(h, p.rows, p.cols) : any_team(h, p.rows, p.cols, 2);
+  Team t = fast ? grad_team(h, p.rows, p.cols) : any_team(h, p.rows, p.cols, 2);
+  // Rows of which a thread would hold two groups, and the block more threads than have registers for the sums besides
+  // (in 16 bits above 8192 columns: 4096 x 16384 bf16 298 us, 398 with what does not fit in local memory; fp32
+  // above 4096: 4096 x 8192 without the first norm 190 and 215, with it 233 and 229).
+  const bool wide = fast && t.vpt == 2 && t.threads > (sizeof(T) == 4 ? 256 : 512);
+  if (wide) t.threads = 1024;
   p.team = t.threads;
-  auto kernel = !fast                          ? gws::block_norm_grad_any_kernel<T>
+  auto kernel = wide                           ? gws::block_norm_grad_any_kernel<T, true>
+                : !fast                        ? gws::block_norm_grad_any_kernel<T, false>
                 : t.vpt == 1                   ? gws::block_norm_grad_kernel<T, 1, 1024>
-                : t.threads * t.rows <= 512    ? gws::block_norm_grad_kernel<T, 2, 512>
-                                               : gws::block_norm_grad_kernel<T, 2, 1024>;
+                                               : gws::block_norm_grad_kernel<T, 2, 512>;
   const int threads = t.threads * t.rows;
   const int64_t pitch = partial_pitch(p.cols);
-  // at most 16 KB on the aligned path, 192 KB on the general one
-  const size_t smem = (fast ? (t.rows > 1 ? t.rows : 0) : 3 * t.rows) * pitch * sizeof(float);
+  // at most 16 KB on the aligned path, 192 KB on the general one and of wide rows
+  const size_t smem = (fast && !wide ? (t.rows > 1 ? t.rows : 0) : 3 * t.rows) * pitch * sizeof(float);
   // As many blocks as run at once, no more than the partials have room for.
   int64_t blocks = ceil_div(p.rows, t.rows);
   const int held = fast && t.vpt == 2 ? 512 : 1024;

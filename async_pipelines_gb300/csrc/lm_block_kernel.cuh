@@ -347,7 +347,7 @@ __device__ __forceinline__ TeamRing enter_ring(const RingPlan& q, int64_t rows, 
 // Up to three vectors over the columns, for all of a launch's rows: a thread's groups of them in its
 // registers, or in 16 bits, where the threads have more groups, in shared memory behind the ring (in registers
 // they would spill, and what shared memory leaves of the L1 cache does not hold that: gradient of
-// 8192 x 8192 213 us, 173 like this).
+// 8192 x 8192 213 us, 165 like this).
 template <typename T, int VPT>
 struct Vectors {
   static constexpr bool SHARED = sizeof(T) == 2;
@@ -685,11 +685,11 @@ __global__ void __launch_bounds__(MOST, 1)
 }
 
 // The gradient of many rows that lie FAST, through the ring (loaded straight into registers the
-// rows of an SM stop at each of a row's two sums). Every pass over a row reads it from the ring; the
-// barrier of the next row's first sum says that all of the team is done with it. Two groups a thread, so
+// rows of an SM stop at each of a row's two sums). The barrier of a row's second sum says that all of the
+// team has what it still needs of it in registers; without the norm after the block that of the next row's first sum. Two groups a thread, so
 // that its shares of the two sums over the rows fit its registers. 8192 x 8192 bf16 with dh and dresidual: 805 MB
-// in 173 us, 4.7 TB/s; bound by the arithmetic of five unpacked inputs and the two barriers a row, with at most
-// three rows of an SM on their way.
+// in 165 us, 4.9 TB/s; bound by latency: an SM has 16 warps, two rows in its ring, and two barriers a row
+// (warps issue in 45 of 100 cycles, a quarter of their time they wait for the row).
 template <typename T, int VPT>
 __global__ void __launch_bounds__(RING_THREADS, 1)
     block_norm_grad_ring_kernel(const __grid_constant__ BlockGradParams p, const __grid_constant__ RingPlan q) {
@@ -749,6 +749,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
       const Raw<T>* dh = reinterpret_cast<const Raw<T>*>(stage + 3 * q.row_bytes) + t;
       const Raw<T>* gate = reinterpret_cast<const Raw<T>*>(stage + gate_at * q.row_bytes) + t;
       const Pair r22 = pair_of(r2, r2), r11 = pair_of(r1, r1);
+      Pair d[VPT][GROUP / 2];
       Pair sums = 0;
 #pragma unroll
       for (int j = 0; j < VPT; ++j)
@@ -759,16 +760,16 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
           unpack(vec.get(0, j), w);
 #pragma unroll
           for (int i = 0; i < GROUP / 2; ++i) {
-            const Pair am = mul2(a[i], m[i]);
-            acc[j][i] = fma2(am, r22, acc[j][i]);
-            sums = fma2(am, w[i], sums);
+            acc[j][i] = fma2(mul2(a[i], m[i]), r22, acc[j][i]);
+            d[j][i] = mul2(a[i], w[i]);
+            sums = fma2(d[j][i], m[i], sums);
           }
         }
       float sum = ring_sum(values_of(sums).x + values_of(sums).y, which, team, box[turn], &ok);
       turn ^= 1;
       if (!ok) break;
       // The whole team has been in the sum, so it has done with the row before.
-      if (t == 0 && k > 0 && k - 1 + q.stages < at.rows.count) fetch(k - 1 + q.stages, before);
+      if (!post && t == 0 && k > 0 && k - 1 + q.stages < at.rows.count) fetch(k - 1 + q.stages, before);
       // g = dh + r2 dy weight - h r2^2 mean(dy weight h r2), then e * post
       const float c2 = -r2 * r2 * (r2 * sum * inv_cols);
       const Pair c22 = pair_of(c2, c2);
@@ -784,7 +785,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
         }
         to = pack<T>(f);
       };
-      Pair d[VPT][GROUP / 2];
+      Raw<T> xr[VPT];
       sums = 0;
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
@@ -793,12 +794,10 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
         {
           Raw<T> dr = {};
           if (p.dh) dr = dh[j * team];
-          unpack(dr, d[j]);
+          unpack(dr, f);
         }
-        unpack(dy[j * team], a);
-        unpack(vec.get(0, j), f);
 #pragma unroll
-        for (int i = 0; i < GROUP / 2; ++i) d[j][i] = fma2(mul2(a[i], f[i]), r22, d[j][i]);
+        for (int i = 0; i < GROUP / 2; ++i) d[j][i] = fma2(d[j][i], r22, f[i]);
         unpack(h[j * team], a);
 #pragma unroll
         for (int i = 0; i < GROUP / 2; ++i) d[j][i] = fma2(a[i], c22, d[j][i]);
@@ -808,7 +807,8 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
           put(dres[j * team], a);
         }
         Pair n[GROUP / 2];
-        unpack(x[j * team], n);
+        xr[j] = x[j * team];
+        unpack(xr[j], n);
 #pragma unroll
         for (int i = 0; i < GROUP / 2; ++i) n[i] = mul2(n[i], r11);
         if (post) unpack(vec.get(1, j), f);
@@ -846,13 +846,14 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
         sum = ring_sum(values_of(sums).x + values_of(sums).y, which, team, box[turn], &ok);
         turn ^= 1;
         if (!ok) break;
+        if (t == 0 && k + q.stages < at.rows.count) fetch(k + q.stages, at.s);   // what is left is in registers
         const float c1 = -r1 * (r1 * sum * inv_cols);
         const Pair c11 = pair_of(c1, c1);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
           if (j * team + t >= groups) continue;
           Pair n[GROUP / 2];
-          unpack(x[j * team], n);
+          unpack(xr[j], n);
 #pragma unroll
           for (int i = 0; i < GROUP / 2; ++i) d[j][i] = fma2(n[i], c11, mul2(d[j][i], r11));
           put(dx[j * team], d[j]);
@@ -880,10 +881,12 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
   if (p.partial_s) leave(acc_s, p.partial_s);
 }
 
-// The same for rows that lie anywhere: e * post and the columns' shares of the sums are in shared memory, and
-// the rows' values are read once more (from L2) for the second pass.
-template <typename T>
-__global__ void __launch_bounds__(ANY_MOST)
+// The same for rows that lie anywhere, and (WHOLE) for long aligned ones, whose shares of the sums no
+// registers hold: e * post and the columns' shares are in shared memory, and the rows' values are read once more
+// (from L2) for the second pass. The team's next row is called into L2 meanwhile. (8192 x 8191 bf16 600 us, 1.3 TB/s: the
+// pieces that unaligned groups are cut from, and put together to, cost most; 4096 x 16384 298, 2.7.)
+template <typename T, bool WHOLE>
+__global__ void __launch_bounds__(WHOLE ? 1024 : ANY_MOST)
     block_norm_grad_any_kernel(const __grid_constant__ BlockGradParams p) {
   __shared__ SumMax box[2][2][32];
   extern __shared__ __align__(16) float row_smem[];
@@ -901,27 +904,34 @@ __global__ void __launch_bounds__(ANY_MOST)
     sums.put(g, zero);
     sums_s.put(g, zero);
   }
+  auto fetch = [&](int64_t row) {
+    if (row >= p.rows) return;
+    for (int g = t; g < groups; g += team) {
+      auto ahead = [&](const void* m, int64_t ld) { prefetch_group(row_of<T>(m, row, p.rows, ld), g * GROUP); };
+      ahead(p.dy, p.lddy);
+      ahead(p.h, p.ldh);
+      ahead(p.x, p.ldx);
+      if (p.dh) ahead(p.dh, p.lddh);
+      if (p.ldg) ahead(p.gate, p.ldg);
+    }
+  };
   int turn = 0;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * teams + which; row < p.rows;
-       row += static_cast<int64_t>(gridDim.x) * teams, turn ^= 1) {
+  const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * teams + which;
+  fetch(row);
+  for (; row < p.rows; row += step, turn ^= 1) {
+    fetch(row + step);
     const Row<T> dy = row_of<T>(p.dy, row, p.rows, p.lddy), h = row_of<T>(p.h, row, p.rows, p.ldh),
                  dh = row_of<T>(p.dh, row, p.rows, p.lddh), x = row_of<T>(p.x, row, p.rows, p.ldx),
                  gate = p.ldg ? row_of<T>(p.gate, row, p.rows, p.ldg) : row_of<T>(p.gate, 0, 1, 0);
-    for (int g = t; g < groups; g += team) {
-      prefetch_group(dy, g * GROUP);
-      prefetch_group(h, g * GROUP);
-      prefetch_group(x, g * GROUP);
-      if (p.dh) prefetch_group(dh, g * GROUP);
-      if (p.gate) prefetch_group(gate, g * GROUP);
-    }
     const GradRow of{p.post != nullptr, p.ldg != 0, p.gate != nullptr, p.alpha,
                      p.post ? p.post_rstd[row] : 1.0f, p.rstd[row]};
     SumMax s = {0.0f, 0.0f};
     for (int g = t; g < groups; g += team) {
       float a[GROUP], v[GROUP], w[GROUP], acc[GROUP];
-      unpack(load_group<false>(dy, g * GROUP, cols), a);
-      unpack(load_group<false>(h, g * GROUP, cols), v);
-      unpack(load_group<false>(weight, g * GROUP, cols), w);
+      unpack(load_group<WHOLE>(dy, g * GROUP, cols), a);
+      unpack(load_group<WHOLE>(h, g * GROUP, cols), v);
+      unpack(load_group<WHOLE>(weight, g * GROUP, cols), w);
       sums.get(g, acc);
       s.sum += of.first(a, v, w, acc);
       sums.put(g, acc);
@@ -935,27 +945,28 @@ __global__ void __launch_bounds__(ANY_MOST)
       float d[GROUP] = {}, a[GROUP] = {}, dgate[GROUP] = {};
       if (g < groups) {
         float v[GROUP], w[GROUP], acc[GROUP];
-        unpack(load_group<false>(dy, c, cols), a);
-        unpack(load_group<false>(h, c, cols), v);
-        unpack(load_group<false>(weight, c, cols), w);
-        if (p.dh) unpack(load_group<false>(dh, c, cols), d);
+        unpack(load_group<WHOLE>(dy, c, cols), a);
+        unpack(load_group<WHOLE>(h, c, cols), v);
+        unpack(load_group<WHOLE>(weight, c, cols), w);
+        if (p.dh) unpack(load_group<WHOLE>(dh, c, cols), d);
         of.second(a, v, w, c2, d);
 #pragma unroll
         for (int i = 0; i < GROUP; ++i) a[i] = p.alpha * d[i];
-        unpack(load_group<false>(x, c, cols), v);
+        unpack(load_group<WHOLE>(x, c, cols), v);
         float gates[GROUP] = {};
-        if (p.gate) unpack(load_group<false>(gate, c, cols), gates);
-        if (p.post) unpack(load_group<false>(post, c, cols), w);
+        if (p.gate) unpack(load_group<WHOLE>(gate, c, cols), gates);
+        if (p.post) unpack(load_group<WHOLE>(post, c, cols), w);
         sums_s.get(g, acc);
         s.sum += of.third(v, gates, w, d, acc, dgate);
         sums_s.put(g, acc);
         cells.put(g, d);
       }
       __syncwarp();
+      if (WHOLE && g >= groups) continue;
       if (p.dres)
-        store_group<false>(static_cast<T*>(p.dres) + row * p.lddres, c, cols, t, team, pack<T>(a));
+        store_group<WHOLE>(static_cast<T*>(p.dres) + row * p.lddres, c, cols, t, team, pack<T>(a));
       if (p.dgate)
-        store_group<false>(static_cast<T*>(p.dgate) + row * p.lddg, c, cols, t, team, pack<T>(dgate));
+        store_group<WHOLE>(static_cast<T*>(p.dgate) + row * p.lddg, c, cols, t, team, pack<T>(dgate));
     }
     float c1 = 0.0f;
     if (p.post) c1 = reduce_team<false>(s, team / 32, box[turn][1]).sum * inv_cols * of.r1;
@@ -965,10 +976,11 @@ __global__ void __launch_bounds__(ANY_MOST)
       if (g < groups) {
         float v[GROUP];
         cells.get(g, d);
-        unpack(load_group<false>(x, c, cols), v);
+        unpack(load_group<WHOLE>(x, c, cols), v);
         of.fourth(v, c1, d);
       }
-      store_group<false>(static_cast<T*>(p.dx) + row * p.lddx, c, cols, t, team, pack<T>(d));
+      if (!WHOLE || g < groups)
+        store_group<WHOLE>(static_cast<T*>(p.dx) + row * p.lddx, c, cols, t, team, pack<T>(d));
     }
   }
   __syncthreads();
