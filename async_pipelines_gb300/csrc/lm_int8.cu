@@ -58,7 +58,7 @@ struct Plan {
 
 // Tiles as wide as leave the least work to the slowest pair: rounds times the time of a tile, where a
 // stage of K takes as long as its MMAs, but no less than 128 tokens' (its conversion), and some more; and a
-// tile's end as long as 3 stages, 7 where cuts of K are joined. Of the tiles of a last round that do not reach
+// tile's end as long as 3 stages, 7 where cuts of K are joined. Of the tiles of a last wave that do not reach
 // all pairs K is cut (5000 x 4000 over 3000, 384 tiles for 76 pairs: 96 us, 113 with them whole).
 Plan make_plan(const gemm_ws* h, int64_t tokens, int64_t channels, int64_t k) {
   Plan q;
