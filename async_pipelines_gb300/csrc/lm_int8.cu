@@ -5,6 +5,9 @@
 
 #include "lm_host.cuh"
 #include "lm_int8_kernel.cuh"
+#ifdef GEMM_WS_DEBUG
+#include "gemm_ws_debug.h"
+#endif
 
 namespace {
 
@@ -223,10 +226,10 @@ int gemm_ws_int8_matmul(gemm_ws_t* h, const int8_t* a, int64_t lda, const float*
   q.channels = static_cast<int>(channels);
   q.stages = static_cast<int>(plan.stages);
   q.bn = plan.bn;
-  q.bufs = i8::w_bufs(q.bn);
-  q.a_stages = q.bufs + 2 < 6 ? 6 : q.bufs + 2;   // freed later than w's, which take what these leave
-  q.w_stages = static_cast<int>((i8::RING_ROOM - q.a_stages * i8::a_stage(q.bn)) / i8::W_STAGE);
-  if (q.w_stages > i8::MAX_STAGES) q.w_stages = i8::MAX_STAGES;
+  const i8::Rings rings = i8::rings_of(q.bn);
+  q.bufs = rings.bufs;
+  q.a_stages = rings.a_stages;
+  q.w_stages = rings.w_stages;
   q.tiles_m = static_cast<int>(plan.tiles_m);
   q.tiles_n = static_cast<int>(plan.tiles_n);
   q.whole = static_cast<int>(plan.whole);
@@ -241,5 +244,19 @@ int gemm_ws_int8_matmul(gemm_ws_t* h, const int8_t* a, int64_t lda, const float*
 #endif
   return launch_product(h, plan, q, s);
 }
+
+#ifdef GEMM_WS_DEBUG
+int gemm_ws_debug_int8_rings(int bn, int* rings) {
+  if (bn < 32 || bn > i8::BN_MAX || bn % 32 != 0 || !rings) return GEMM_WS_ERR_INVALID_ARG;
+  const i8::Rings r = i8::rings_of(bn);
+  rings[0] = r.bufs;
+  rings[1] = r.w_stages;
+  rings[2] = r.a_stages;
+  rings[3] = i8::T_FULL_ARRIVALS;
+  rings[4] = i8::CONV_WARPS;
+  rings[5] = i8::CUT_STAGES;
+  return GEMM_WS_OK;
+}
+#endif
 
 }  // extern "C"

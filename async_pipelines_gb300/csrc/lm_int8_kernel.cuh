@@ -175,6 +175,33 @@ static_assert(SMEM_BYTES <= 232448, "exceeds the 227 KiB per-CTA shared memory")
 
 __host__ __device__ constexpr uint32_t a_stage(int bn) { return static_cast<uint32_t>(bn / 2) * BK * 2; }
 
+// Arrivals that fill a buffer of w: a warpgroup's warps that convert, of both CTAs, and both CTAs' tellers, which
+// so have seen the step before in the buffer go before the next can. Without theirs a teller that is late by
+// the time of all buffers would find the barrier's other parity, and wait for a phase that cannot come: the tokens'
+// ring has more stages than there are buffers, and does not hold the next step back.
+constexpr int TELLERS = 2, T_FULL_ARRIVALS = CONV_WARPS + TELLERS;
+
+// Stages of the two rings. The tokens' are freed later than w's, which take what those leave.
+struct Rings {
+  int bufs, w_stages, a_stages;
+};
+__host__ __device__ constexpr Rings rings_of(int bn) {
+  const int bufs = w_bufs(bn), a_stages = bufs + 2 < 6 ? 6 : bufs + 2;
+  const int room = static_cast<int>((RING_ROOM - a_stages * a_stage(bn)) / W_STAGE);
+  return {bufs, room < MAX_STAGES ? room : MAX_STAGES, a_stages};
+}
+// The two warpgroups that convert take w's stages in turn. One of them, at step i, has seen the buffer of step i - 2 - bufs free, so
+// all steps up to that have been converted, by the other as well; with these many stages the one before in its own
+// stage is among them.
+constexpr bool rings_fit() {
+  for (int bn = 32; bn <= BN_MAX; bn += 32) {
+    const Rings r = rings_of(bn);
+    if (r.w_stages < r.bufs + 2 || r.a_stages > MAX_STAGES || r.bufs > MAX_W_BUFS) return false;
+  }
+  return true;
+}
+static_assert(rings_fit(), "a wait by parity is at most one phase behind");
+
 struct Params {
   CUtensorMap tmW, tmA;
   int tokens, channels, stages;   // stages of K
@@ -190,7 +217,7 @@ struct Params {
   uint32_t* status;
   unsigned long long timeout_ns;
 #ifdef GEMM_WS_DEBUG
-  int debug_fault;                // 3: w's producer brings nothing
+  int debug_fault;                // 3: w's producer brings nothing; 4: the tellers are late
 #endif
 };
 
@@ -362,15 +389,27 @@ __device__ __forceinline__ void convert(const Params& p, uint32_t sbase, const u
     }
 }
 
-// Frees the tokens' stages: the MMAs that have read w's buffer of a step have read the step's tokens.
+// Frees the tokens' stages: the MMAs that have read w's buffer of a step have read the step's tokens. The
+// arrival on the buffer's own barrier holds its next step back until this one has been seen (see
+// T_FULL_ARRIVALS); in time it is early, as the buffer is still to be filled then.
 __device__ __forceinline__ void tell(const Params& p, uint32_t sbase, const Watchdog& wd) {
-  const uint32_t bufs = p.bufs;
+  const uint32_t bufs = p.bufs, t_full = mapa_shared(sbase + OFF_BAR + 8 * BAR_T_FULL, 0u);   // the leader's
+  const bool first = (threadIdx.x & 31) == 0;
   uint32_t s = 0, t = 0, tph = 0;
   Unit w;
+  if (first)
+    for (uint32_t i = 0; i < bufs; ++i) mbar_arrive_cluster_relaxed(t_full + 8 * i);   // none before the first
   for (int u = blockIdx.x / 2; unit_of(p, u, w); u += gridDim.x / 2)
     for (int st = w.s0; st < w.s1; ++st) {
+#ifdef GEMM_WS_DEBUG
+      if (p.debug_fault == 4)   // injected delay: many steps' time
+        for (const uint64_t t0 = global_timer_ns(); global_timer_ns() - t0 < 20000ull;) __nanosleep(1000);
+#endif
       if (!warp_wait_cta(sbase + OFF_BAR + 8 * (BAR_T_EMPTY + t), tph, wd)) return;
-      if ((threadIdx.x & 31) == 0) mbar_arrive(sbase + OFF_BAR + 8 * (BAR_A_EMPTY + s));
+      if (first) {
+        mbar_arrive(sbase + OFF_BAR + 8 * (BAR_A_EMPTY + s));
+        mbar_arrive_cluster_relaxed(t_full + 8 * t);
+      }
       if (++t == bufs) {
         t = 0;
         tph ^= 1;
@@ -581,7 +620,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
       mbar_init(bar(BAR_A_EMPTY + s), 1);
     }
     for (int t = 0; t < MAX_W_BUFS; ++t) {
-      mbar_init(bar(BAR_T_FULL + t), CONV_WARPS);   // 4 of each CTA
+      mbar_init(bar(BAR_T_FULL + t), T_FULL_ARRIVALS);   // of each CTA 4 that convert, and the teller
       mbar_init(bar(BAR_T_EMPTY + t), 1);
     }
     for (int b = 0; b < ACC_BUFS; ++b) {

@@ -88,7 +88,7 @@ def load_library(path: Optional[str] = None):
 DEBUG_EXPORTS = ("gemm_ws_debug_configure", "gemm_ws_debug_launch_shape",
                  "gemm_ws_debug_schedule", "gemm_ws_debug_phases",
                  "gemm_ws_debug_noalloc_configure", "gemm_ws_debug_ce_units",
-                 "gemm_ws_debug_row_columns")
+                 "gemm_ws_debug_row_columns", "gemm_ws_debug_int8_rings")
 
 _debug_lib = None
 
@@ -122,6 +122,8 @@ def load_debug_library():
         lib.gemm_ws_debug_ce_units.restype = ctypes.c_int
         lib.gemm_ws_debug_row_columns.argtypes = [i64, i64, ctypes.c_int, ctypes.c_void_p]
         lib.gemm_ws_debug_row_columns.restype = ctypes.c_int
+        lib.gemm_ws_debug_int8_rings.argtypes = [ctypes.c_int, ctypes.c_void_p]
+        lib.gemm_ws_debug_int8_rings.restype = ctypes.c_int
         _debug_lib = lib
     return _debug_lib
 

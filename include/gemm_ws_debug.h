@@ -33,7 +33,9 @@ extern "C" {
  *    gemm_ws_query_status to clear); 3 the cross entropy's product kernel never
  *    loads its first operand, and the norm's kernels that bring rows
  *    through shared memory load none after the first stages, so each wait for
- *    them can only end by the watchdog.
+ *    them can only end by the watchdog; 4 the 8-bit product's warps that
+ *    free the tokens' stages take 20 us for each (a delay, after which results are
+ *    the same).
  *  - trace: device buffer of num_units * ctas_per_cluster * 2 uint64 (see
  *    gemm_ws_debug_launch_shape) or NULL. For work unit u and CTA rank r
  *    in its cluster, trace[(u*ctas_per_cluster + r)*2] = global time (ns) at which
@@ -111,6 +113,12 @@ int gemm_ws_debug_ce_units(int cta_group, int clusters, int bn, int count, const
  * for each of `count` threads 3 ints: its first column, whether all eight columns from
  * there are in the row, and whether sixteen are. */
 int gemm_ws_debug_row_columns(int64_t cols, int64_t first, int count, int* rows);
+
+/* The rings of the 8-bit product's kernel for tiles of `bn` tokens (32, 64, ..., 160), as it is
+ * launched with; host arithmetic only. rings, 6 ints: buffers of the weight in tensor memory, the
+ * weight's and the tokens' stages in shared memory, arrivals that fill a buffer, warps of them that
+ * convert (half of them of each CTA), and stages of an accumulator. */
+int gemm_ws_debug_int8_rings(int bn, int* rings);
 
 #ifdef __cplusplus
 }
