@@ -217,7 +217,7 @@ struct Params {
   uint32_t* status;
   unsigned long long timeout_ns;
 #ifdef GEMM_WS_DEBUG
-  int debug_fault;                // 3: w's producer brings nothing; 4: the tellers are late
+  int debug_fault;                // 3: w's producer brings nothing; 4: the tellers are late; 5: the MMA warp gives up
 #endif
 };
 
@@ -263,22 +263,19 @@ __device__ __forceinline__ uint2 to_fp16(uint32_t w) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&e), *reinterpret_cast<const uint32_t*>(&o));
 }
 
-__device__ __forceinline__ void produce_w(const Params& p, uint32_t sbase, uint32_t rank, const Watchdog& wd) {
+// Returns how many stages it has armed.
+__device__ __forceinline__ uint32_t produce_w(const Params& p, uint32_t sbase, uint32_t rank, const Watchdog& wd) {
   auto full = [&](uint32_t s) { return sbase + OFF_BAR + 8 * (BAR_W_FULL + s); };
   auto empty = [&](uint32_t s) { return sbase + OFF_BAR + 8 * (BAR_W_EMPTY + s); };
   const uint32_t stages = p.w_stages;
   uint32_t s = 0, ph = 0, g = 0;
-  bool ok = true;
   Unit w;
 #ifdef GEMM_WS_DEBUG
-  if (p.debug_fault == 3) return;   // injected fault: no stage ever fills
+  if (p.debug_fault == 3) return 0;   // injected fault: no stage ever fills
 #endif
-  for (int u = blockIdx.x / 2; ok && unit_of(p, u, w); u += gridDim.x / 2)
+  for (int u = blockIdx.x / 2; unit_of(p, u, w); u += gridDim.x / 2)
     for (int st = w.s0; st < w.s1; ++st) {
-      if (!wait_suspended(empty(s), ph ^ 1, wd)) {
-        ok = false;
-        break;
-      }
+      if (!wait_suspended(empty(s), ph ^ 1, wd)) return g;
       mbar_arrive_expect_tx(full(s), W_STAGE);
       tma_load_3d(sbase + s * W_STAGE, &p.tmW, full(s), st * BK, w.n0 + static_cast<int>(rank) * BM, 0);
       ++g;
@@ -287,25 +284,25 @@ __device__ __forceinline__ void produce_w(const Params& p, uint32_t sbase, uint3
         ph ^= 1;
       }
     }
-  // Abort: the copies of the stages armed last land before the CTA goes on.
-  if (!ok)
-    for (uint32_t j = g > stages ? g - stages : 0; j < g; ++j) wait_drain(full(j % stages), (j / stages) & 1);
+  return g;
 }
 
-__device__ __forceinline__ void produce_a(const Params& p, uint32_t sbase, uint32_t rank, const Watchdog& wd) {
+// After an abort, whichever warp gave up, and when nothing more is issued: the copies of the stages armed last land
+// before the CTA ends. `full`: the first stage's barrier.
+__device__ __forceinline__ void drain(uint32_t full, uint32_t stages, uint32_t g) {
+  for (uint32_t j = g > stages ? g - stages : 0; j < g; ++j) wait_drain(full + 8 * (j % stages), (j / stages) & 1);
+}
+
+__device__ __forceinline__ uint32_t produce_a(const Params& p, uint32_t sbase, uint32_t rank, const Watchdog& wd) {
   auto full = [&](uint32_t s) { return sbase + OFF_BAR + 8 * (BAR_A_FULL + s); };
   auto empty = [&](uint32_t s) { return sbase + OFF_BAR + 8 * (BAR_A_EMPTY + s); };
   const uint32_t stages = p.a_stages, bytes = a_stage(p.bn), ring = sbase + p.w_stages * W_STAGE;
   const bool leader = rank == 0;   // arms full[s] for the pair
   uint32_t s = 0, ph = 0, g = 0;
-  bool ok = true;
   Unit w;
-  for (int u = blockIdx.x / 2; ok && unit_of(p, u, w); u += gridDim.x / 2)
+  for (int u = blockIdx.x / 2; unit_of(p, u, w); u += gridDim.x / 2)
     for (int st = w.s0; st < w.s1; ++st) {
-      if (!wait_suspended(empty(s), ph ^ 1, wd)) {
-        ok = false;
-        break;
-      }
+      if (!wait_suspended(empty(s), ph ^ 1, wd)) return g;
       if (leader) mbar_arrive_expect_tx(full(s), 2 * bytes);
       const uint32_t bar = mapa_shared(full(s), 0u), dst = ring + s * bytes;
       const int row = w.m0 + static_cast<int>(rank) * (p.bn / 2);
@@ -317,14 +314,7 @@ __device__ __forceinline__ void produce_a(const Params& p, uint32_t sbase, uint3
         ph ^= 1;
       }
     }
-  if (!ok && leader) {
-    for (uint32_t j = g > stages ? g - stages : 0; j < g; ++j) wait_drain(full(j % stages), (j / stages) & 1);
-  } else if (!ok) {
-    // Copies into a stage that the leader never armed have no barrier: give
-    // them 100 us (they take a few).
-    const uint64_t t0 = global_timer_ns();
-    while (global_timer_ns() - t0 < 100000ull) __nanosleep(1000);
-  }
+  return g;
 }
 
 // A ring's place and phase, some steps on.
@@ -441,6 +431,13 @@ __device__ __forceinline__ void issue(const Params& p, uint32_t sbase, uint32_t 
       const int end = min(first + CUT_STAGES, w.s1);
       for (int st = first; st < end; ++st) {
         const uint32_t b_addr = ring + s * bytes, from = tmem + ACC_BUFS * p.bn + t * W_COLS;
+#ifdef GEMM_WS_DEBUG
+        if (mine && ok && p.debug_fault == 5 && st == w.s0 + 1) {   // injected fault: it gives up while all others work
+          ok = false;
+          *wd.abort = 1;
+          atomicExch(wd.status, STATUS_TIMEOUT);
+        }
+#endif
         if (mine && ok) {
           ok = wait_inline(bar(BAR_A_FULL + s), ph, wd) &&
                wait_inline(bar(BAR_T_FULL + t), tph, wd);
@@ -647,6 +644,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
   // fp16: that one has waited for everything before it, and does not touch w. Who needs its results waits.
   if (threadIdx.x == 0) grid_launch_dependents();
 
+  uint32_t loaded = 0;   // stages, of the two producers
   if (warp >= WARP_EPI0) {
     more_registers<REGS_EPI>();
     grid_dependency_wait();
@@ -656,10 +654,10 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
     if (warp >= WARP_CONV0) {
       convert(p, sbase, smem, tmem, warp, wd);
     } else if (warp == WARP_W) {
-      if (lane == 0) produce_w(p, sbase, rank, wd);
+      if (lane == 0) loaded = produce_w(p, sbase, rank, wd);
     } else if (warp == WARP_A) {
       grid_dependency_wait();
-      if (lane == 0) produce_a(p, sbase, rank, wd);
+      if (lane == 0) loaded = produce_a(p, sbase, rank, wd);
     } else if (warp == WARP_TELL) {
       tell(p, sbase, wd);
     } else if (warp == WARP_MMA) {
@@ -669,6 +667,19 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
+  // No warp of the CTA gives up after this, and without that every copy has been waited for.
+  if (*abort_flag && lane == 0) {
+    if (warp == WARP_W) {
+      drain(sbase + OFF_BAR + 8 * BAR_W_FULL, p.w_stages, loaded);
+    } else if (warp == WARP_A && rank == 0) {
+      drain(sbase + OFF_BAR + 8 * BAR_A_FULL, p.a_stages, loaded);
+    } else if (warp == WARP_A) {
+      // Its copies have the leader's barriers: give them 100 us (they take a few).
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 100000ull) __nanosleep(1000);
+    }
+  }
+  __syncwarp();
   cluster_sync();
   if (warp == WARP_MMA) {
     tc_fence_after_sync();

@@ -227,3 +227,26 @@ def test_late_tellers(M, N, K):
     configure(g, fault=0)
     assert torch.equal(d, late_d)
     g.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(20, 600, 4096), (160, 5000, 1500), (700, 3000, 640), (2000, 9000, 1500)])
+def test_another_warp_gives_up_while_copies_are_under_way(M, N, K):
+    """Copies of both operands have been started when the warp that issues the matrix instructions gives up: they land before the
+    kernel ends, the call reports the timeout, and the next one is untroubled."""
+    gen = torch.Generator().manual_seed(M)
+    g = debug_handle(timeout_ms=100)
+    a, w, sa, sw = integers(M, K, gen), integers(N, K, gen, (K + 15) // 16 * 16), scales(M, gen), scales(N, gen)
+    want, d = torch.empty(M, N, device="cuda"), torch.empty(M, N, device="cuda")
+    g.int8_matmul(a, w, sa, sw, want)
+    assert g.query_status() == gemm_ws.OK
+    for _ in range(3):
+        configure(g, fault=5)
+        g.int8_matmul(a, w, sa, sw, d)
+        assert g.query_status() == gemm_ws.ERR_TIMEOUT
+        configure(g, fault=0)
+        d.fill_(float("nan"))
+        g.int8_matmul(a, w, sa, sw, d)
+        assert g.query_status() == gemm_ws.OK
+        assert torch.equal(d, want)
+    g.close()
