@@ -295,7 +295,7 @@ struct RingPlan {
   uint32_t* status;
   unsigned long long timeout_ns;
 #ifdef GEMM_WS_DEBUG
-  int debug_fault;      // 3: only the first stages are ever filled
+  int debug_fault;      // 3: only the first stages are ever filled; 5: the next row is given up
 #endif
 };
 
@@ -314,12 +314,22 @@ struct TeamRing {
       ph ^= 1;
     }
   }
-  // Given up at row k: the copies under way land before the CTA ends.
-  __device__ __forceinline__ void drain(int64_t k) const {
-    if (k < rows.count && t == 0)
-      for (int64_t j = k; j < rows.count && j < k + stages; ++j)
+  // Given up at row k, those before row `fetched` on their way: they land before the CTA ends.
+  __device__ __forceinline__ void drain(int64_t k, int64_t fetched) const {
+    if (t == 0)
+      for (int64_t j = k; j < rows.count && j < fetched; ++j)
         wait_drain(full(static_cast<int>(j % stages)), static_cast<uint32_t>(j / stages) & 1);
   }
+#ifdef GEMM_WS_DEBUG
+  // Injected fault: false, as if the wait for a row that has come had run out.
+  __device__ __forceinline__ bool give_up(const Watchdog& wd) const {
+    if (t == 0) {
+      *wd.abort = 1;
+      atomicExch(wd.status, STATUS_TIMEOUT);
+    }
+    return false;
+  }
+#endif
 };
 
 // Sets the barriers up and finds the team's place (all threads of the CTA call it).
@@ -421,6 +431,9 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
   for (; k < at.rows.count; ++k, turn ^= 1) {
     const int64_t row = at.rows.first + k * at.rows.step;
     bool ok = warp_wait_cta(at.full(at.s), at.ph, wd);
+#ifdef GEMM_WS_DEBUG
+    if (q.debug_fault == 5 && k == q.stages) ok = at.give_up(wd);
+#endif
     const uint8_t* stage = ring + (which * q.stages + at.s) * at.stage_bytes;
     const Raw<T>* x = reinterpret_cast<const Raw<T>*>(stage) + t;
     const Raw<T>* res = reinterpret_cast<const Raw<T>*>(stage + q.row_bytes) + t;
@@ -514,7 +527,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
     }
     at.next();
   }
-  at.drain(k);
+  at.drain(k, k + q.stages);
 }
 
 // ------------------------------------------------------------ backward
@@ -742,6 +755,9 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
         if (post) next1 = p.post_rstd[row + at.rows.step];
       }
       bool ok = warp_wait_cta(at.full(at.s), at.ph, wd);
+#ifdef GEMM_WS_DEBUG
+      if (q.debug_fault == 5 && k == q.stages) ok = at.give_up(wd);
+#endif
       const uint8_t* stage = ring + (which * q.stages + at.s) * at.stage_bytes;
       const Raw<T>* dy = reinterpret_cast<const Raw<T>*>(stage) + t;
       const Raw<T>* h = reinterpret_cast<const Raw<T>*>(stage + q.row_bytes) + t;
@@ -862,7 +878,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
       before = at.s;
       at.next();
     }
-    at.drain(k);
+    at.drain(k, k + q.stages - (!post && k > 0));   // without `post` a stage is filled anew one row later
   }
   float mine[VPT][GROUP];
   auto leave = [&](const Pair (&of)[VPT][GROUP / 2], float* partial) {

@@ -36,7 +36,8 @@ extern "C" {
  *    them can only end by the watchdog; 4 the 8-bit product's warps that
  *    free the tokens' stages take 20 us for each (a delay, after which results are
  *    the same); 5 its warp that issues the matrix instructions gives up at its
- *    second stage, while everything else works, as if its wait had run out.
+ *    second stage, and the block norms' rings at the row after their first stages',
+ *    while everything else works, as if a wait had run out.
  *  - trace: device buffer of num_units * ctas_per_cluster * 2 uint64 (see
  *    gemm_ws_debug_launch_shape) or NULL. For work unit u and CTA rank r
  *    in its cluster, trace[(u*ctas_per_cluster + r)*2] = global time (ns) at which
