@@ -7,8 +7,10 @@ runtime's driver-entry-point query, so it needs no libcuda at link time.
 from __future__ import annotations
 
 import os
+import re
 import shutil
 import subprocess
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -51,15 +53,40 @@ def _cmd(out: str, extra=(), verbose: bool = False):
     return cmd
 
 
+def used_registers(report: str, kernel: str) -> int:
+    """Registers a thread of `kernel` in ptxas's report of one translation unit (-Xptxas=-v)."""
+    m = re.search(rf"entry function '\w*{kernel}\w*'.*?Used (\d+) registers", report, re.S)
+    if not m:
+        raise RuntimeError(f"no {kernel} in ptxas's report")
+    return int(m.group(1))
+
+
+def check_registers(report: str) -> None:
+    """Raises where the 8-bit product's kernel has other registers at launch than its warpgroups share
+    out: they would wait for each other, so the library would refuse the calls."""
+    with open(os.path.join(CSRC, "lm_int8_kernel.cuh")) as f:
+        planned = int(re.search(r"REGS_LAUNCH = (\d+)", f.read()).group(1))
+    used = used_registers(report, "product_kernel")
+    if used != planned:
+        raise RuntimeError(f"lm_int8.cu: product_kernel was compiled with {used} registers a thread, planned are "
+                           f"{planned} (REGS_LAUNCH): change the plan for this compiler")
+
+
 def build(out: str = LIB, extra=(), verbose: bool = False, debug: bool = True) -> str:
     """Builds the production library (and, by default, the debug library) in
     parallel nvcc processes."""
     procs = [subprocess.Popen(_cmd(out, extra, verbose))]
     if debug:
         procs.append(subprocess.Popen(_cmd(DEBUG_LIB, ("-DGEMM_WS_DEBUG", *extra))))
-    codes = [p.wait() for p in procs]
+    # One unit by itself: reports of units compiled in parallel come mixed.
+    with tempfile.TemporaryDirectory() as scratch:
+        unit = subprocess.run(
+            [nvcc(), ARCH, "-O3", "-lineinfo", "-std=c++17", f"-I{INCLUDE}", "-Xptxas=-v", "-cubin", *extra, "-o",
+             os.path.join(scratch, "unit"), os.path.join(CSRC, "lm_int8.cu")], capture_output=True, text=True)
+    codes = [p.wait() for p in procs] + [unit.returncode]
     if any(codes):
-        raise subprocess.CalledProcessError(max(codes), "nvcc")
+        raise subprocess.CalledProcessError(max(codes), "nvcc", stderr=unit.stderr)
+    check_registers(unit.stdout + unit.stderr)
     return out
 
 

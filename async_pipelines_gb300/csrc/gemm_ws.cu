@@ -654,13 +654,14 @@ const char* gemm_ws_status_string(int status) {
     case GEMM_WS_ERR_UNSUPPORTED: return "unsupported device (needs sm_103)";
     case GEMM_WS_ERR_CUDA: return "CUDA error";
     case GEMM_WS_ERR_TIMEOUT: return "device wait timed out";
+    case GEMM_WS_ERR_BUILD: return "library compiled with other registers than planned";
     default: return "unknown status";
   }
 }
 
 #ifdef GEMM_WS_DEBUG
 int gemm_ws_debug_configure(gemm_ws_t* h, int fault, unsigned long long* trace) {
-  if (!h || fault < 0 || fault > 5) return GEMM_WS_ERR_INVALID_ARG;
+  if (!h || fault < 0 || fault > 6) return GEMM_WS_ERR_INVALID_ARG;
   h->debug_fault = fault;
   h->trace = trace;
   return GEMM_WS_OK;

@@ -112,7 +112,11 @@ bool encode(gemm_ws* h, CUtensorMap* m, const void* ptr, bool half, int64_t inne
 
 // Whether the product kernel has the registers at launch that its warpgroups share out: with fewer
 // they would wait for each other forever. (A property of the built kernel.)
-bool registers_as_planned() {
+bool registers_as_planned(const gemm_ws* h) {
+#ifdef GEMM_WS_DEBUG
+  if (h->debug_fault == 6) return false;   // injected fault
+#endif
+  (void)h;
   static std::atomic<bool> seen{false};   // handles may be used by several threads
   if (seen.load(std::memory_order_relaxed)) return true;
   cudaFuncAttributes a;
@@ -122,7 +126,6 @@ bool registers_as_planned() {
 }
 
 int launch_product(gemm_ws* h, const Plan& q, const i8::Params& p, cudaStream_t s) {
-  if (!registers_as_planned()) return GEMM_WS_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   cfg.gridDim = dim3(static_cast<unsigned>(2 * q.clusters), 1, 1);
@@ -137,8 +140,7 @@ int launch_product(gemm_ws* h, const Plan& q, const i8::Params& p, cudaStream_t 
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = h->pdl ? 2 : 1;
-  cudaError_t e = allow_smem(h, reinterpret_cast<const void*>(i8::product_kernel), i8::SMEM_BYTES);
-  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, i8::product_kernel, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, i8::product_kernel, p);
   return e == cudaSuccess ? GEMM_WS_OK : cuda_fail(h, e);
 }
 
@@ -202,6 +204,10 @@ int gemm_ws_int8_matmul(gemm_ws_t* h, const int8_t* a, int64_t lda, const float*
     if (tokens <= 4) return launch_dot<4>(h, q, s);
     return launch_dot<8>(h, q, s);
   }
+  // What may be refused is, before anything is launched.
+  if (!registers_as_planned(h)) return GEMM_WS_ERR_BUILD;
+  const cudaError_t allowed = allow_smem(h, reinterpret_cast<const void*>(i8::product_kernel), i8::SMEM_BYTES);
+  if (allowed != cudaSuccess) return cuda_fail(h, allowed);
   i8::ExpandParams e;
   std::memset(&e, 0, sizeof e);
   e.a = a;

@@ -22,6 +22,7 @@ ERR_ALIGNMENT = 2
 ERR_UNSUPPORTED = 3
 ERR_CUDA = 4
 ERR_TIMEOUT = 5
+ERR_BUILD = 6
 
 EXPORTS = (
     "gemm_ws_create", "gemm_ws_destroy", "gemm_ws_run", "gemm_ws_run_streamout",

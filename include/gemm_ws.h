@@ -64,7 +64,9 @@ typedef enum gemm_ws_status {
   GEMM_WS_ERR_UNSUPPORTED = 3, /* device is not sm_103 (GB300) */
   GEMM_WS_ERR_CUDA = 4,        /* a CUDA runtime/driver call failed; see
                                   gemm_ws_last_cuda_error */
-  GEMM_WS_ERR_TIMEOUT = 5      /* a bounded on-device wait gave up (watchdog) */
+  GEMM_WS_ERR_TIMEOUT = 5,     /* a bounded on-device wait gave up (watchdog) */
+  GEMM_WS_ERR_BUILD = 6        /* the library was compiled with other registers than a kernel
+                                  shares out among its warps (see gemm_ws_int8_matmul) */
 } gemm_ws_status;
 
 typedef struct gemm_ws gemm_ws_t;

@@ -37,7 +37,8 @@ extern "C" {
  *    free the tokens' stages take 20 us for each (a delay, after which results are
  *    the same); 5 its warp that issues the matrix instructions gives up at its
  *    second stage, and the block norms' rings at the row after their first stages',
- *    while everything else works, as if a wait had run out.
+ *    while everything else works, as if a wait had run out; 6 the 8-bit
+ *    product's kernel is taken to have been compiled with other registers.
  *  - trace: device buffer of num_units * ctas_per_cluster * 2 uint64 (see
  *    gemm_ws_debug_launch_shape) or NULL. For work unit u and CTA rank r
  *    in its cluster, trace[(u*ctas_per_cluster + r)*2] = global time (ns) at which

@@ -216,7 +216,9 @@ int gemm_ws_quantize_rows(gemm_ws_t* h, int dtype, const void* x, int64_t ldx, i
  *  - workspace: gemm_ws_int8_matmul_workspace bytes on the device, 256-byte aligned,
  *    for this call alone (its contents mean nothing before or after); NULL where it is 0.
  *  - 0 <= tokens, 1 <= channels, each at most 2^31 - 4096; 1 <= k < 2^17;
- *    tokens * k, channels * k and tokens * channels at most 2^40. */
+ *    tokens * k, channels * k and tokens * channels at most 2^40.
+ * GEMM_WS_ERR_BUILD for more than a few tokens where the compiler gave the kernel other registers than
+ * its warps share out, with which they would wait for each other (the build checks it). */
 int gemm_ws_int8_matmul(gemm_ws_t* h, const int8_t* a, int64_t lda, const float* a_scales,
                         const int8_t* w, int64_t ldw, const float* w_scales, const float* bias,
                         void* d, int64_t ldd, int dtype, int64_t tokens, int64_t channels,
