@@ -67,7 +67,7 @@ int cuda_fail(gemm_ws* h, cudaError_t e) {
 
 // Allows `kernel` `bytes` of dynamic shared memory before its first launch by the handle
 // (whose device is current). Not at the handle's creation: that would load every such
-// kernel, 22 of them, for callers that use none (21 ms instead of 0.6).
+// kernel, some fifty of them, for callers that use none (21 ms instead of 0.6 with 22 of them).
 [[maybe_unused]] cudaError_t allow_smem(gemm_ws* h, const void* kernel, size_t bytes) {
   for (const void*& k : h->large) {
     if (k == kernel) return cudaSuccess;

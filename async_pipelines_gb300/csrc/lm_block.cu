@@ -177,7 +177,8 @@ int launch_grad(gemm_ws* h, bool fast, gws::BlockGradParams& p, gws::BlockSumsPa
   Team t = fast ? grad_team(h, p.rows, p.cols) : any_team(h, p.rows, p.cols, 2);
   // Rows of which a thread would hold two groups, and the block more threads than have registers for the sums besides
   // (in 16 bits above 8192 columns: 4096 x 16384 bf16 298 us, 398 with what does not fit in local memory; fp32
-  // above 4096: 4096 x 8192 without the first norm 190 and 215, with it 233 and 229).
+  // above 4096: without the first norm 4096 x 8192 191 and 219, 8192 x 4104 241 and 271, with it 234 and 234, 296 and
+  // 320; only at 8192 columns with it, a channel's gate and no dh are the registers ahead, 223 and 212).
   const bool wide = fast && t.vpt == 2 && t.threads > (sizeof(T) == 4 ? 256 : 512);
   if (wide) t.threads = 1024;
   p.team = t.threads;

@@ -469,7 +469,7 @@ __device__ __forceinline__ uint2 quotients(const float (&v)[GROUP], float scale)
   return e4m3(q);
 }
 
-// The 8-bit integers nearest to v / scale (halves to even), lowest column first, |v| <= 127 scale;
+// The 8-bit integers nearest to v / scale (halves to even), lowest column first, |v| < 127.5 scale;
 // zeros where scale is NaN. As the quotients above: put between two products, and divided only
 // where those round differently. A sum with 1.5 * 2^23 leaves the rounded integer in the
 // sum's low bits, without the conversion unit's quarter rate.
@@ -677,8 +677,9 @@ constexpr int DW_THREADS = DW_QUADS * DW_LANES;
 
 // put(c, the sum of column c over the blocks' partial rows), in a fixed order, for block
 // number `block` of the columns. A thread has four columns of every 128th row, eight of them in flight at
-// once. There are 152 rows from a ring (two a thread), and up to 2432 (19 a thread) where
-// the blocks are smallest: of 64 threads, of unaligned rows of 257 to 512 columns.
+// once. There are 152 rows from a ring (two a thread), and most where the blocks are smallest, for unaligned rows of
+// 257 to 512 columns: of add_rms_norm up to 2432, from blocks of 64 threads (19 a thread), of block_norm 4864,
+// from blocks of one warp (38; 16384 x 511 bf16 104 us in all).
 template <typename Put>
 __device__ __forceinline__ void column_sums(const float* partial, int block, int blocks, int cols,
                                             int pitch, Put put) {

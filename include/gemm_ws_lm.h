@@ -26,7 +26,7 @@
  * nothing. Results have the same bits on every run.
  *
  * A matrix is `rows` rows of `cols` contiguous elements, `ld` elements from
- * one row to the next (ld >= cols). What lies between two rows of an input may be
+ * one row to the next (cols <= ld <= 2^40). What lies between two rows of an input may be
  * read, and plays no part; between two rows of an output nothing is written. An
  * output may be exactly one of the call's inputs where that is said; any other
  * overlap of an output with another argument (first to last element, what lies
@@ -81,7 +81,8 @@ int gemm_ws_dropout(gemm_ws_t* h, int dtype, const void* x, int64_t ldx, void* y
  *    hidden may be x or residual, and y may be x.
  *  - output: a gemm_ws_norm_output. The scale of a row (or of 128 columns, the
  *    last ones fewer) is max |y| / 448, at least 2^-126, and y holds the
- *    e4m3 roundings of y / scale. scales: rows (or rows x ceil(cols / 128)) fp32.
+ *    e4m3 roundings of y / scale. scales: rows (or rows x ceil(cols / 128)) fp32. (A row's
+ *    largest |y| is taken from hidden * weight, whose products have to lie in the range of normal fp32.)
  *  - rstd: rows fp32, 1 / sqrt(mean(hidden^2) + eps), for the backward pass; or NULL.
  *  - 1 <= cols <= 32768; 0 <= rows < 2^31; p and rng as in gemm_ws_dropout. */
 int gemm_ws_add_rms_norm(gemm_ws_t* h, int dtype, const void* x, int64_t ldx,
@@ -212,7 +213,7 @@ int gemm_ws_quantize_rows(gemm_ws_t* h, int dtype, const void* x, int64_t ldx, i
  * exact in 32-bit integers; what follows is fp32, rounded once to `dtype`.
  *  - a: tokens x k, w: channels x k, 8-bit integers, -128 included; a_scales: tokens,
  *    w_scales: channels, bias: channels (NULL: none), fp32; d: tokens x channels of `dtype`.
- *  - w 16-byte aligned, ldw a multiple of 16 (a, d and k are free).
+ *  - w 16-byte aligned, ldw a multiple of 16, channels * ldw at most 2^40 (a, d and k are free).
  *  - workspace: gemm_ws_int8_matmul_workspace bytes on the device, 256-byte aligned,
  *    for this call alone (its contents mean nothing before or after); NULL where it is 0.
  *  - 0 <= tokens, 1 <= channels, each at most 2^31 - 4096; 1 <= k < 2^17;
