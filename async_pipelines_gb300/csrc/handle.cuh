@@ -58,7 +58,9 @@ namespace {
 [[maybe_unused]] constexpr int kWorkWords = 4;
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxElems = int64_t{1} << 40;
-[[maybe_unused]] constexpr size_t kDefaultSmem = 48 * 1024;   // dynamic shared memory a kernel has unasked
+// Dynamic shared memory that a kernel has unasked: of 48 KB, which what it declares itself counts towards, so
+// that 12280 fp32 columns and the 512 bytes of a sum's boxes would be too much.
+[[maybe_unused]] constexpr size_t kDefaultSmem = 40 * 1024;
 
 int cuda_fail(gemm_ws* h, cudaError_t e) {
   if (h) h->last_cuda_error = static_cast<int>(e);
